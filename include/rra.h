@@ -457,6 +457,110 @@ RRA_API rra_status rra_get_device_error(int32_t* code, int clear);
 RRA_API rra_status rra_bind_error_word(int32_t* word);
 RRA_API rra_status rra_read_error_word(int32_t* word, int32_t* code, int clear);
 
+/* ------------------------------------------------------------------------
+ * A language model's block on packed rows.  The kept image tokens of a
+ * vision-language model go on, packed, into prompts of different lengths;
+ * these calls are that block's hot operators: a linear layer with its whole
+ * epilogue, the norms and rotation of queries and keys, attention over whole
+ * prompts, and attention of new tokens over a cache.
+ *
+ * They take head size d = 64 or 128, F16 or BF16, Hq query heads sharing
+ * Hkv key/value heads (Hq a multiple of Hkv; query head h reads key/value
+ * head h / (Hq / Hkv)), and row tensors [cap, H, d] whose rows may lie
+ * `stride` elements apart (a multiple of 8, at least H*d), so the three parts
+ * of a fused query/key/value projection are used where they are.  Counts of
+ * rows are read on the device from cu_seqlens; rows past cu_seqlens[B] are
+ * neither read into a result nor written.  int32 arrays are 4-byte aligned.
+ * No workspace; every call is one launch, asynchronous on `stream`, and can be
+ * captured.  Outputs may not overlap inputs except where said. */
+
+typedef enum {
+  RRA_ACT_NONE = 0,
+  RRA_ACT_RELU = 1,      /* max(x, 0); NaN stays NaN                           */
+  RRA_ACT_GELU = 2,      /* x/2 (1 + erf(x / sqrt 2))                          */
+  RRA_ACT_GELU_TANH = 3, /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))      */
+  RRA_ACT_SILU = 4       /* x / (1 + exp(-x))                                  */
+} rra_activation;
+
+/* c[t, :] = act(a[t, :] W^T + bias) + residual[t, :] for t < T = cu_seqlens[B].
+ *   a [cap, K], w [N, K] of in_dtype; bias float [N] or NULL; residual
+ *   [cap, N] of out_dtype or NULL (it may be c itself: the sum in place);
+ *   c [cap, N] of out_dtype (F16, BF16 or F32).
+ * K and N multiples of 8, 8 <= K <= 65536 (else RRA_ERR_UNSUPPORTED).  The
+ * products accumulate in fp32, bias, activation and residual are applied in
+ * fp32, and the result is rounded once.  A cu_seqlens[B] outside [0, cap]
+ * records RRA_DEVERR_INDEX_RANGE and writes nothing. */
+RRA_API rra_status rra_linear_epilogue(const void* a, const void* w, const float* bias, const void* residual,
+                                       const int32_t* cu_seqlens, int B, int cap, int K, int N,
+                                       rra_dtype in_dtype, rra_activation act, void* c, rra_dtype out_dtype,
+                                       void* stream);
+
+/* Norms of queries and keys for each head and their position rotation in one
+ * pass, optionally with the write into a cache.  For token t < cu_seqlens[B]
+ * and each head row x of q and of k, in fp32, rounded once:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (q_weight / k_weight, float [d];
+ *                                              NULL: y = x)
+ *   for i < rot/2, angle = positions[t] * inv_freq[i]:
+ *     (y[a], y[b]) = rope_scale * (y[a] cos - y[b] sin, y[a] sin + y[b] cos)
+ *   with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when `interleaved` is set.
+ * Elements from `rot` on are not rotated (nor scaled).  rot = 0: no rotation
+ * (inv_freq and positions are not read); else rot is a multiple of 16 up to d
+ * and inv_freq float [rot/2] holds the frequencies, already scaled for long
+ * contexts where the model does so.  The angle is reduced exactly enough for
+ * every position in [0, 2^24); a token with another position records
+ * RRA_DEVERR_INDEX_RANGE and is not written.
+ *   q_out [cap, Hq, d] receives row t; k_out (and v_out, a copy of v, when
+ *   both are not NULL) row t, or row kv_rows[t] of kv_out_rows rows when
+ *   kv_rows is not NULL: the slots of the tokens in a cache.  A kv_rows[t] outside
+ *   [0, kv_out_rows) records RRA_DEVERR_INDEX_RANGE and leaves that token's
+ *   key and value unwritten.  The slots are distinct; of two tokens with one
+ *   slot either may end there, head by head.
+ * q_out may be q and k_out may be k (without kv_rows), with the same stride:
+ * in place.  Other overlaps are refused (RRA_ERR_INVALID_ARG); slices of one
+ * wider row buffer that do not touch are not overlaps. */
+RRA_API rra_status rra_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                                    const void* v, long long v_stride, const int32_t* positions,
+                                    const int32_t* cu_seqlens, int B, int cap, int Hq, int Hkv, int d,
+                                    rra_dtype dtype, const float* q_weight, const float* k_weight, float eps,
+                                    const float* inv_freq, int rot, int interleaved, float rope_scale,
+                                    void* q_out, long long q_out_stride, void* k_out, long long k_out_stride,
+                                    void* v_out, long long v_out_stride, const int32_t* kv_rows,
+                                    long long kv_out_rows, void* stream);
+
+/* Attention over whole prompts: B packed sequences, sequence b in rows
+ * cu_seqlens[b] .. cu_seqlens[b+1], of any length up to max_seqlen (which has
+ * no upper limit but B * Hq * ceil(max_seqlen / 128) < 2^31).  Row i of a sequence
+ * attends to its rows j <= i when `causal` is set, else to all its rows:
+ *   o[i, h] = sum_j softmax_j(scale <q[i, h], k[j, h']>) v[j, h'].
+ * q [cap, Hq, d], k and v [cap, Hkv, d]; o [cap, Hq, d] contiguous, of the
+ * same dtype; 1e-30 <= scale <= 1e30.  Both products and the softmax sums are in fp32; the weights
+ * enter the second product rounded to the dtype.  Rows of other sequences,
+ * and rows past the last one, may hold anything.  Within a sequence a key may
+ * be infinite or NaN and touches only the rows that see it; the values of a
+ * sequence have to be finite, because a value of weight zero still enters the
+ * product.  A length above
+ * max_seqlen records RRA_DEVERR_SEQ_TOO_LONG, a decreasing cu_seqlens
+ * RRA_DEVERR_SEQ_NEGATIVE, rows outside [0, cap] RRA_DEVERR_INDEX_RANGE; such
+ * a sequence is not written. */
+RRA_API rra_status rra_attend_prompt(const void* q, long long q_stride, const void* k, long long k_stride,
+                                     const void* v, long long v_stride, const int32_t* cu_seqlens, int B, int cap,
+                                     int max_seqlen, int Hq, int Hkv, int d, float scale, int causal,
+                                     rra_dtype dtype, void* o, void* stream);
+
+/* Attention of the newest nq tokens of each of B sequences over a padded
+ * cache: k_cache and v_cache [B, cap, Hkv, d] contiguous, of which sequence b
+ * uses its first kv_len[b] rows (the new tokens' rows among them, the last
+ * ones).  q [B*nq, Hq, d]; row b*nq + i attends to the keys
+ * j < kv_len[b] - (nq - 1 - i); a row that sees no key gets zeros.
+ * o [B*nq, Hq, d] contiguous, of the same dtype.  1 <= nq <= 64.  Rows from
+ * kv_len[b] on may hold anything; offsets into the cache are 64-bit.  A
+ * kv_len[b] below 0 records RRA_DEVERR_SEQ_NEGATIVE, one above cap
+ * RRA_DEVERR_SEQ_TOO_LONG; that sequence's rows are not written.  Products,
+ * sums and the values' limits as in rra_attend_prompt. */
+RRA_API rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                                    const int32_t* kv_len, int B, int nq, int cap, int Hq, int Hkv, int d,
+                                    float scale, rra_dtype dtype, void* o, void* stream);
+
 /* Bound, in clock cycles, on any one on-chip wait of the tcgen05 attention
  * kernels (0, the initial value: about one second).  A wait that runs out
  * makes the CTA record RRA_DEVERR_WAIT_TIMEOUT, give its own copies and

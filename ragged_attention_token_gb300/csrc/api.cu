@@ -118,6 +118,54 @@ rra_status check_shape(int B, int N, int H, int d) {
     if (_s != RRA_OK) return _s; \
   } while (0)
 
+// int32 arrays the kernels read by 4-byte loads.
+#define RRA_CHECK_I32(p)                                                                              \
+  do {                                                                                                \
+    if ((p) == nullptr) return fail(RRA_ERR_INVALID_ARG, "%s is null", #p);                          \
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(RRA_ERR_MISALIGNED, "%s not 4-byte aligned", #p); \
+  } while (0)
+
+// A row tensor as bytes: `rows` rows of `width` bytes, `stride` bytes apart.
+struct RowSpan {
+  const void* p;
+  long long rows, width, stride;
+};
+
+// No byte belongs to both: disjoint ranges, or rows of one stride that
+// interleave without touching (slices of one wider buffer).
+bool disjoint(const RowSpan& x, const RowSpan& y) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
+  const uintptr_t x1 = x0 + static_cast<uintptr_t>((x.rows - 1) * x.stride + x.width);
+  const uintptr_t y1 = y0 + static_cast<uintptr_t>((y.rows - 1) * y.stride + y.width);
+  if (x1 <= y0 || y1 <= x0) return true;
+  if (x.stride != y.stride) return false;
+  const long long s = x.stride;
+  const long long diff = static_cast<long long>(y0 - x0);   // two's complement difference
+  const long long off = ((diff % s) + s) % s;               // y's first byte within x's row period
+  return off >= x.width && off + y.width <= s;
+}
+
+bool same_rows(const RowSpan& x, const RowSpan& y) {
+  return x.p == y.p && x.stride == y.stride && x.width == y.width;
+}
+
+rra_status check_block_heads(int B, int cap, int Hq, int Hkv, int d, rra_dtype dtype) {
+  if (d != 64 && d != 128) return fail(RRA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  if (B < 1 || B > 65535) return fail(RRA_ERR_INVALID_ARG, "B=%d outside [1, 65535]", B);
+  if (cap < 1) return fail(RRA_ERR_INVALID_ARG, "cap=%d < 1", cap);
+  if (Hkv < 1 || Hq < 1 || Hq > 65535 || Hq % Hkv != 0)
+    return fail(RRA_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d, at most 65535", Hq, Hkv);
+  if (!valid_in(dtype)) return fail(RRA_ERR_INVALID_ARG, "dtype invalid");
+  return RRA_OK;
+}
+
+rra_status check_stride(const char* name, long long stride, int H, int d) {
+  if (stride < static_cast<long long>(H) * d || stride >= (1LL << 36))
+    return fail(RRA_ERR_INVALID_ARG, "%s row stride %lld below H*d or too large", name, stride);
+  if (stride % 8 != 0) return fail(RRA_ERR_MISALIGNED, "%s row stride %lld not a multiple of 8", name, stride);
+  return RRA_OK;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 void workspace_layout(int B, int N, int H, int d, rra_dtype in, size_t off[6], size_t* total) {
@@ -597,6 +645,224 @@ rra_status rra_linear_packed(const void* a, const void* w, const float* bias, co
   return RRA_OK;
 }
 
+rra_status rra_linear_epilogue(const void* a, const void* w, const float* bias, const void* residual,
+                               const int32_t* cu_seqlens, int B, int cap, int K, int N, rra_dtype in_dtype,
+                               rra_activation act, void* c, rra_dtype out_dtype, void* stream) {
+  if (B < 1 || B > 65535) return fail(RRA_ERR_INVALID_ARG, "B=%d outside [1, 65535]", B);
+  if (cap < 1 || cap > 65535 * 128) return fail(RRA_ERR_INVALID_ARG, "cap=%d outside [1, 65535*128]", cap);
+  if (K < 8 || K % 8 != 0 || K > 65536) return fail(RRA_ERR_UNSUPPORTED, "K=%d: a multiple of 8 up to 65536", K);
+  if (N < 8 || N % 8 != 0 || N > 65535 * 128) return fail(RRA_ERR_UNSUPPORTED, "N=%d: a multiple of 8", N);
+  if (!valid_in(in_dtype)) return fail(RRA_ERR_INVALID_ARG, "input dtype invalid");
+  if (!valid_out(out_dtype)) return fail(RRA_ERR_INVALID_ARG, "output dtype invalid");
+  if (act < RRA_ACT_NONE || act > RRA_ACT_SILU) return fail(RRA_ERR_INVALID_ARG, "activation %d unknown", static_cast<int>(act));
+  RRA_CHECK_PTR(a);
+  RRA_CHECK_PTR(w);
+  RRA_CHECK_PTR(c);
+  RRA_CHECK_I32(cu_seqlens);
+  if (bias != nullptr && !aligned16(bias)) return fail(RRA_ERR_MISALIGNED, "bias not 16-byte aligned");
+  if (residual != nullptr && !aligned16(residual)) return fail(RRA_ERR_MISALIGNED, "residual not 16-byte aligned");
+  const long long eo = dtype_bytes(out_dtype);
+  const RowSpan sc{c, cap, N * eo, N * eo}, sa{a, cap, 2LL * K, 2LL * K}, sw{w, N, 2LL * K, 2LL * K};
+  const RowSpan sb{bias, 1, 4LL * N, 4LL * N}, sr{residual, cap, N * eo, N * eo};
+  if (!disjoint(sc, sa) || !disjoint(sc, sw) || (bias != nullptr && !disjoint(sc, sb)))
+    return fail(RRA_ERR_INVALID_ARG, "c overlaps an input");
+  if (residual != nullptr && residual != c && !disjoint(sc, sr))
+    return fail(RRA_ERR_INVALID_ARG, "c overlaps residual without being it");
+  DeviceState* st = nullptr;
+  RRA_TRY(device_state(&st));
+  LinearEpiArgs g{};
+  g.cu = cu_seqlens;
+  g.B = B;
+  g.cap = cap;
+  g.K = K;
+  g.N = N;
+  g.a = a;
+  g.w = w;
+  g.bias = bias;
+  g.residual = residual;
+  g.c = c;
+  g.err = error_word(*st);
+  cudaError_t e = launch_linear_epilogue(g, in_dtype, out_dtype, act, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "linear_epilogue launch");
+  g_launches += 1;
+  return RRA_OK;
+}
+
+rra_status rra_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                            long long v_stride, const int32_t* positions, const int32_t* cu_seqlens, int B, int cap,
+                            int Hq, int Hkv, int d, rra_dtype dtype, const float* q_weight, const float* k_weight,
+                            float eps, const float* inv_freq, int rot, int interleaved, float rope_scale, void* q_out,
+                            long long q_out_stride, void* k_out, long long k_out_stride, void* v_out,
+                            long long v_out_stride, const int32_t* kv_rows, long long kv_out_rows, void* stream) {
+  RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
+  if (rot < 0 || rot > d || rot % 16 != 0)
+    return fail(RRA_ERR_UNSUPPORTED, "rot=%d: a multiple of 16 up to d=%d", rot, d);
+  if (!finite(eps) || eps < 0.f) return fail(RRA_ERR_INVALID_ARG, "eps is negative or not finite");
+  if (!finite(rope_scale)) return fail(RRA_ERR_INVALID_ARG, "rope_scale is not finite");
+  RRA_CHECK_PTR(q);
+  RRA_CHECK_PTR(k);
+  RRA_CHECK_PTR(q_out);
+  RRA_CHECK_PTR(k_out);
+  RRA_CHECK_I32(cu_seqlens);
+  RRA_TRY(check_stride("q", q_stride, Hq, d));
+  RRA_TRY(check_stride("k", k_stride, Hkv, d));
+  RRA_TRY(check_stride("q_out", q_out_stride, Hq, d));
+  RRA_TRY(check_stride("k_out", k_out_stride, Hkv, d));
+  if ((v == nullptr) != (v_out == nullptr)) return fail(RRA_ERR_INVALID_ARG, "v and v_out go together");
+  if (v != nullptr) {
+    RRA_CHECK_PTR(v);
+    RRA_CHECK_PTR(v_out);
+    RRA_TRY(check_stride("v", v_stride, Hkv, d));
+    RRA_TRY(check_stride("v_out", v_out_stride, Hkv, d));
+  }
+  if (rot > 0) {
+    RRA_CHECK_I32(positions);
+    RRA_CHECK_I32(inv_freq);
+  }
+  if (q_weight != nullptr && !aligned16(q_weight)) return fail(RRA_ERR_MISALIGNED, "q_weight not 16-byte aligned");
+  if (k_weight != nullptr && !aligned16(k_weight)) return fail(RRA_ERR_MISALIGNED, "k_weight not 16-byte aligned");
+  if (kv_rows != nullptr) {
+    RRA_CHECK_I32(kv_rows);
+    if (kv_out_rows < 1) return fail(RRA_ERR_INVALID_ARG, "kv_out_rows=%lld < 1", kv_out_rows);
+  }
+  const long long orows = kv_rows != nullptr ? kv_out_rows : cap;
+  const long long wq = 2LL * Hq * d, wk = 2LL * Hkv * d;
+  const RowSpan in[3] = {{q, cap, wq, 2 * q_stride}, {k, cap, wk, 2 * k_stride}, {v, cap, wk, 2 * v_stride}};
+  const RowSpan out[3] = {
+      {q_out, cap, wq, 2 * q_out_stride}, {k_out, orows, wk, 2 * k_out_stride}, {v_out, orows, wk, 2 * v_out_stride}};
+  for (int i = 0; i < 3; ++i) {
+    if (out[i].p == nullptr) continue;
+    for (int j = 0; j < 3; ++j) {
+      if (in[j].p != nullptr) {
+        const bool in_place = i == j && same_rows(out[i], in[j]) && (i == 0 || kv_rows == nullptr);
+        if (!in_place && !disjoint(out[i], in[j])) return fail(RRA_ERR_INVALID_ARG, "an output overlaps an input");
+      }
+      if (j > i && out[j].p != nullptr && !disjoint(out[i], out[j]))
+        return fail(RRA_ERR_INVALID_ARG, "two outputs overlap");
+    }
+  }
+  DeviceState* st = nullptr;
+  RRA_TRY(device_state(&st));
+  NormRopeArgs g{};
+  g.q = q;
+  g.k = k;
+  g.v = v;
+  g.q_out = q_out;
+  g.k_out = k_out;
+  g.v_out = v_out;
+  g.q_stride = q_stride;
+  g.k_stride = k_stride;
+  g.v_stride = v_stride;
+  g.q_out_stride = q_out_stride;
+  g.k_out_stride = k_out_stride;
+  g.v_out_stride = v_out_stride;
+  g.positions = rot > 0 ? positions : nullptr;
+  g.cu = cu_seqlens;
+  g.kv_rows = kv_rows;
+  g.kv_out_rows = orows;
+  g.B = B;
+  g.cap = cap;
+  g.Hq = Hq;
+  g.Hkv = Hkv;
+  g.q_weight = q_weight;
+  g.k_weight = k_weight;
+  g.inv_freq = inv_freq;
+  g.eps = eps;
+  g.rope_scale = rope_scale;
+  g.rot = rot;
+  g.err = error_word(*st);
+  cudaError_t e = launch_qk_norm_rope(g, d, dtype, interleaved != 0, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+  g_launches += 1;
+  return RRA_OK;
+}
+
+rra_status rra_attend_prompt(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                             long long v_stride, const int32_t* cu_seqlens, int B, int cap, int max_seqlen, int Hq,
+                             int Hkv, int d, float scale, int causal, rra_dtype dtype, void* o, void* stream) {
+  RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
+  if (max_seqlen < 1) return fail(RRA_ERR_INVALID_ARG, "max_seqlen=%d < 1", max_seqlen);
+  if (static_cast<long long>(B) * Hq * ((max_seqlen + 127LL) / 128) >= (1LL << 31))
+    return fail(RRA_ERR_UNSUPPORTED, "B * Hq * ceil(max_seqlen / 128) >= 2^31");
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
+  RRA_CHECK_PTR(q);
+  RRA_CHECK_PTR(k);
+  RRA_CHECK_PTR(v);
+  RRA_CHECK_PTR(o);
+  RRA_CHECK_I32(cu_seqlens);
+  RRA_TRY(check_stride("q", q_stride, Hq, d));
+  RRA_TRY(check_stride("k", k_stride, Hkv, d));
+  RRA_TRY(check_stride("v", v_stride, Hkv, d));
+  const long long wq = 2LL * Hq * d, wk = 2LL * Hkv * d;
+  const RowSpan so{o, cap, wq, wq};
+  if (!disjoint(so, {q, cap, wq, 2 * q_stride}) || !disjoint(so, {k, cap, wk, 2 * k_stride}) ||
+      !disjoint(so, {v, cap, wk, 2 * v_stride}))
+    return fail(RRA_ERR_INVALID_ARG, "o overlaps an input");
+  DeviceState* st = nullptr;
+  RRA_TRY(device_state(&st));
+  PromptArgs g{};
+  g.q = q;
+  g.k = k;
+  g.v = v;
+  g.q_stride = q_stride;
+  g.k_stride = k_stride;
+  g.v_stride = v_stride;
+  g.cu = cu_seqlens;
+  g.B = B;
+  g.cap = cap;
+  g.max_seqlen = max_seqlen;
+  g.Hq = Hq;
+  g.Hkv = Hkv;
+  g.scale_log2 = scale * 1.4426950408889634f;
+  g.causal = causal != 0;
+  g.o = o;
+  g.err = error_word(*st);
+  cudaError_t e = launch_attend_prompt(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "attend_prompt launch");
+  g_launches += 1;
+  return RRA_OK;
+}
+
+rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                            const int32_t* kv_len, int B, int nq, int cap, int Hq, int Hkv, int d, float scale,
+                            rra_dtype dtype, void* o, void* stream) {
+  RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
+  if (nq < 1 || nq > 64) return fail(RRA_ERR_UNSUPPORTED, "nq=%d outside [1, 64]", nq);
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
+  RRA_CHECK_PTR(q);
+  RRA_CHECK_PTR(k_cache);
+  RRA_CHECK_PTR(v_cache);
+  RRA_CHECK_PTR(o);
+  RRA_CHECK_I32(kv_len);
+  RRA_TRY(check_stride("q", q_stride, Hq, d));
+  const long long wq = 2LL * Hq * d, wk = 2LL * Hkv * d, rows = static_cast<long long>(B) * nq;
+  const long long krows = static_cast<long long>(B) * cap;
+  const RowSpan so{o, rows, wq, wq};
+  if (!disjoint(so, {q, rows, wq, 2 * q_stride}) || !disjoint(so, {k_cache, krows, wk, wk}) ||
+      !disjoint(so, {v_cache, krows, wk, wk}))
+    return fail(RRA_ERR_INVALID_ARG, "o overlaps an input");
+  DeviceState* st = nullptr;
+  RRA_TRY(device_state(&st));
+  CacheArgs g{};
+  g.q = q;
+  g.k = k_cache;
+  g.v = v_cache;
+  g.q_stride = q_stride;
+  g.kv_len = kv_len;
+  g.B = B;
+  g.nq = nq;
+  g.cap = cap;
+  g.Hq = Hq;
+  g.Hkv = Hkv;
+  g.scale_log2 = scale * 1.4426950408889634f;
+  g.o = o;
+  g.err = error_word(*st);
+  cudaError_t e = launch_attend_cache(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "attend_cache launch");
+  g_launches += 1;
+  return RRA_OK;
+}
+
 rra_status rra_cls_scores(const void* qp, const void* kp, const int32_t* cu_seqlens, const int32_t* src_idx,
                           int B, int N, int H, int d, float scale, rra_dtype in_dtype, float* scores,
                           void* stream) {
@@ -698,7 +964,7 @@ rra_status rra_attend_gather(const void* q, const void* k, const void* v, const 
   RRA_TRY(check_shape(B, N, H, d));
   if (!valid_in(in_dtype)) return fail(RRA_ERR_INVALID_ARG, "input dtype invalid");
   if (!valid_out(out_dtype)) return fail(RRA_ERR_INVALID_ARG, "output dtype invalid");
-  if (!finite(scale)) return fail(RRA_ERR_INVALID_ARG, "scale is not finite");
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
   RRA_CHECK_PTR(q);
   RRA_CHECK_PTR(k);
   RRA_CHECK_PTR(v);

@@ -20,6 +20,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "rra.h")
 RRA_OK, RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED, RRA_ERR_MISALIGNED, RRA_ERR_CUDA, RRA_ERR_DEVICE = range(6)
 RRA_F16, RRA_BF16, RRA_F32 = 0, 1, 2
 ATTEND_TCGEN05, ATTEND_MMA_SYNC, ATTEND_AUTO, ATTEND_TCGEN05_LATENCY = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 DEVERR_NONE, DEVERR_SEQ_TOO_LONG, DEVERR_SEQ_NEGATIVE, DEVERR_INDEX_RANGE, DEVERR_WAIT_TIMEOUT = range(5)
 
 _DTYPE = {torch.float16: RRA_F16, torch.bfloat16: RRA_BF16, torch.float32: RRA_F32}
@@ -28,6 +29,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 _dp = ctypes.POINTER(ctypes.c_double)
 
 _SIGNATURES = {
@@ -68,6 +70,11 @@ _SIGNATURES = {
     "rra_bind_error_word": (_i, [_vp]),
     "rra_read_error_word": (_i, [_vp, ctypes.POINTER(ctypes.c_int32), _i]),
     "rra_set_wait_limit": (ctypes.c_longlong, [ctypes.c_longlong]),
+    "rra_linear_epilogue": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp]),
+    "rra_qk_norm_rope": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _f, _vp, _i,
+                              _i, _f, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp]),
+    "rra_attend_prompt": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _vp, _vp]),
+    "rra_attend_cache": (_i, [_vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
     "rra_status_string": (ctypes.c_char_p, [_i]),
     "rra_last_error_message": (ctypes.c_char_p, []),
     "rra_launch_count": (ctypes.c_uint64, []),
@@ -313,6 +320,109 @@ def pipeline_mapped(keep_h, q_h, k_h, v_h, out_h, workspace, scale: float = 0.12
                                      B, N, H, d, float(scale), _DTYPE[q_h.dtype], out_h.data_ptr(),
                                      _DTYPE[out_h.dtype], _ptr(workspace), _nbytes(workspace),
                                      _stream(stream)))
+
+
+def _typed(t, dtype, name: str, shape=None):
+    """Pointer of a contiguous tensor of the current device with this dtype (and shape), or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    p = _ptr(t)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return p
+
+
+def _rows(t, dtype, name: str, shape):
+    """(pointer, row stride) of a [rows, H, d] tensor whose rows may lie apart (a slice of a wider buffer)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    rows, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: each row must be contiguous")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else H * d)
+
+
+def _cu(cu_seqlens, B: int):
+    if cu_seqlens.numel() < B + 1:
+        raise ValueError(f"cu_seqlens has {cu_seqlens.numel()} entries, fewer than B + 1 = {B + 1}")
+    return _typed(cu_seqlens, torch.int32, "cu_seqlens")
+
+
+def linear_epilogue(a, w, cu_seqlens, B: int, c, bias=None, act: int = ACT_NONE, residual=None, stream=None):
+    """rra_linear_epilogue: c[t] = act(a[t] @ w.T + bias) + residual[t] for the T = cu_seqlens[B] packed rows."""
+    cap, K = a.shape
+    N = w.shape[0]
+    _check(lib().rra_linear_epilogue(_typed(a, a.dtype, "a"), _typed(w, a.dtype, "w", (N, K)),
+                                     _typed(bias, torch.float32, "bias", (N,)),
+                                     _typed(residual, c.dtype, "residual", (cap, N)), _cu(cu_seqlens, B), B, cap, K, N,
+                                     _DTYPE[a.dtype], int(act), _typed(c, c.dtype, "c", (cap, N)), _DTYPE[c.dtype],
+                                     _stream(stream)))
+
+
+def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, rope_scale: float = 1.0, v=None, v_out=None,
+                 kv_rows=None, stream=None):
+    """rra_qk_norm_rope: per-head RMS norm (with a weight) and rotation (with inv_freq) of q [cap, Hq, d] and
+    k [cap, Hkv, d]; k_out / v_out take row t, or row kv_rows[t] of their own rows."""
+    cap, Hq, d = q.shape
+    Hkv = k.shape[1]
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out go together")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    dt = q.dtype
+    out_rows = k_out.shape[0] if kv_rows is not None else cap
+    qp, qs = _rows(q, dt, "q", (cap, Hq, d))
+    kp, ks = _rows(k, dt, "k", (cap, Hkv, d))
+    vp, vs = _rows(v, dt, "v", (cap, Hkv, d)) if v is not None else (None, 0)
+    qo, qos = _rows(q_out, dt, "q_out", (cap, Hq, d))
+    ko, kos = _rows(k_out, dt, "k_out", (out_rows, Hkv, d))
+    vo, vos = _rows(v_out, dt, "v_out", (out_rows, Hkv, d)) if v_out is not None else (None, 0)
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    _check(lib().rra_qk_norm_rope(qp, qs, kp, ks, vp, vs, _typed(positions, torch.int32, "positions", (cap,)),
+                                  _cu(cu_seqlens, B), B, cap, Hq, Hkv, d, _DTYPE[dt],
+                                  _typed(q_weight, torch.float32, "q_weight", (d,)),
+                                  _typed(k_weight, torch.float32, "k_weight", (d,)), float(eps),
+                                  _typed(inv_freq, torch.float32, "inv_freq"), rot, int(bool(interleaved)),
+                                  float(rope_scale), qo, qos, ko, kos, vo, vos,
+                                  _typed(kv_rows, torch.int32, "kv_rows", (cap,)), out_rows, _stream(stream)))
+
+
+def attend_prompt(q, k, v, cu_seqlens, B: int, max_seqlen: int, o, scale: float, causal: bool = True, stream=None):
+    """rra_attend_prompt: attention over B packed sequences, q [cap, Hq, d], k and v [cap, Hkv, d], o [cap, Hq, d]."""
+    cap, Hq, d = q.shape
+    Hkv = k.shape[1]
+    qp, qs = _rows(q, q.dtype, "q", (cap, Hq, d))
+    kp, ks = _rows(k, q.dtype, "k", (cap, Hkv, d))
+    vp, vs = _rows(v, q.dtype, "v", (cap, Hkv, d))
+    _check(lib().rra_attend_prompt(qp, qs, kp, ks, vp, vs, _cu(cu_seqlens, B), B, cap, int(max_seqlen), Hq, Hkv, d,
+                                   float(scale), int(bool(causal)), _DTYPE[q.dtype],
+                                   _typed(o, q.dtype, "o", (cap, Hq, d)), _stream(stream)))
+
+
+def attend_cache(q, k_cache, v_cache, kv_len, o, scale: float, stream=None):
+    """rra_attend_cache: attention of the nq newest tokens of each sequence, q [B*nq, Hq, d], over
+    k_cache and v_cache [B, cap, Hkv, d], of which kv_len [B] rows are in use."""
+    B, cap, Hkv, d = k_cache.shape
+    if B == 0 or q.shape[0] % B:
+        raise ValueError(f"q has {q.shape[0]} rows, no multiple of the cache's {B} sequences")
+    Hq = q.shape[1]
+    qp, qs = _rows(q, q.dtype, "q", (q.shape[0], Hq, d))
+    _check(lib().rra_attend_cache(qp, qs, _typed(k_cache, q.dtype, "k_cache"),
+                                  _typed(v_cache, q.dtype, "v_cache", (B, cap, Hkv, d)),
+                                  _typed(kv_len, torch.int32, "kv_len", (B,)), B, q.shape[0] // B, cap, Hq, Hkv, d,
+                                  float(scale), _DTYPE[q.dtype], _typed(o, q.dtype, "o", (q.shape[0], Hq, d)),
+                                  _stream(stream)))
 
 
 class Plan:

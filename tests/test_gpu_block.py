@@ -1,0 +1,84 @@
+"""The block operators together, as a model uses them (needs a GPU): a layer's attention half over packed prompts
+(projection, norm and rotation in place, attention, projection onto the residual) with its keys and values written into
+a cache, then one more token of every sequence against that cache.  The oracle computes both in fp64 from the
+same weights; the one-token step must agree with the prompt pass over the longer prompts."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as OB
+from ragged_attention_token_gb300 import rra
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,dtype", [(8, 2, 128, torch.bfloat16), (6, 6, 64, torch.float16)])
+def test_prompt_then_one_token(Hq, Hkv, d, dtype):
+    g = torch.Generator().manual_seed(11)
+    C, lens = 384, [150, 1, 33]
+    full = [n + 1 for n in lens]                                     # prompts with the next token appended
+    B, cap_kv, W = len(lens), 200, (Hq + 2 * Hkv) * d
+    w1 = (torch.randn((W, C), generator=g) / np.sqrt(C)).to(dtype)
+    w2 = (torch.randn((C, Hq * d), generator=g) / np.sqrt(Hq * d)).to(dtype)
+    b1 = 0.1 * torch.randn(W, generator=g)
+    nw = 1 + 0.1 * torch.randn((2, d), generator=g)
+    f = (10000.0 ** (-torch.arange(d // 2) / (d // 2))).float()
+    x_full = torch.randn((sum(full), C), generator=g).to(dtype)
+    w1d, w2d, b1d, nwd, fd = w1.cuda(), w2.cuda(), b1.cuda(), nw.cuda(), f.cuda()
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def layer(x, lens, attend, positions, slots, kc, vc):
+        T = x.shape[0]
+        cu = ints(np.concatenate([[0], np.cumsum(lens)]))
+        qkv = torch.empty((T, Hq + 2 * Hkv, d), dtype=dtype, device="cuda")
+        rra.linear_epilogue(x, w1d, cu, len(lens), qkv.view(T, W), bias=b1d)
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        if slots is not None:
+            rra.qk_norm_rope(q, k, positions, cu, len(lens), q, kc, fd, q_weight=nwd[0], k_weight=nwd[1], v=v, v_out=vc,
+                             kv_rows=slots)
+        if slots is None or attend == "prompt":
+            rra.qk_norm_rope(q, k, positions, cu, len(lens), q.clone() if slots is not None else q, k, fd,
+                             q_weight=nwd[0], k_weight=nwd[1])
+        o = torch.empty((T, Hq, d), dtype=dtype, device="cuda")
+        if attend == "prompt":
+            rra.attend_prompt(q, k, v, cu, len(lens), max(lens), o, scale=d ** -0.5)
+        else:
+            rra.attend_cache(q, kc.view(B, cap_kv, Hkv, d), vc.view(B, cap_kv, Hkv, d), attend, o, scale=d ** -0.5)
+        y = x.clone()
+        rra.linear_epilogue(o.view(T, Hq * d), w2d, cu, len(lens), y, residual=y)
+        return y
+
+    kc, vc = (torch.zeros((B * cap_kv, Hkv, d), dtype=dtype, device="cuda") for _ in range(2))
+    at = np.concatenate([[0], np.cumsum(full)])
+    prompt_rows = np.concatenate([np.arange(at[b], at[b] + lens[b]) for b in range(B)])
+    last_rows = at[1:] - 1
+    pos = ints(np.concatenate([np.arange(n) for n in lens]))
+    slots = ints(np.concatenate([b * cap_kv + np.arange(n) for b, n in enumerate(lens)]))
+    rra.get_device_error(clear=True)
+    y_prompt = layer(x_full[prompt_rows].cuda(), lens, "prompt", pos, slots, kc, vc)
+    y_next = layer(x_full[last_rows].cuda(), [1] * B, ints([n + 1 for n in lens]), ints(lens),
+                   ints([b * cap_kv + n for b, n in enumerate(lens)]), kc, vc)
+    y_full = layer(x_full.cuda(), full, "prompt", ints(np.concatenate([np.arange(n) for n in full])), None, None, None)
+    torch.cuda.synchronize()
+    assert rra.get_device_error() == 0
+
+    x64 = x_full.double().numpy()
+    qkv = OB.linear_epilogue(x64, w1.double().numpy(), b1.double().numpy(), "none", None, len(x64)).reshape(-1, Hq + 2 * Hkv, d)
+    p64 = np.concatenate([np.arange(n) for n in full])
+    f64, n64 = f.double().numpy(), nw.double().numpy()
+    q = OB.norm_rope(qkv[:, :Hq], p64, n64[0], 1e-6, f64, False, 1.0)
+    k = OB.norm_rope(qkv[:, Hq:Hq + Hkv], p64, n64[1], 1e-6, f64, False, 1.0)
+    o = np.concatenate([OB.attend_rows(q[at[b]:at[b + 1]], k[at[b]:at[b + 1]], qkv[at[b]:at[b + 1], Hq + Hkv:], d ** -0.5,
+                                       np.arange(full[b]))[0] for b in range(B)])
+    y = OB.linear_epilogue(o.reshape(-1, Hq * d), w2.double().numpy(), None, "none", x64, len(x64))
+    # Four roundings to the type on the way (projection, norm/rotation, weights and output of the attention), each at
+    # most half a step of values of order one to five, through sums whose weights' squares add up to one, and the last
+    # rounding: within 24 half steps of 1 + |y|.
+    u = torch.finfo(dtype).eps / 2
+    for got, rows in ((y_prompt, prompt_rows), (y_next, last_rows), (y_full, np.arange(len(x64)))):
+        err = np.abs(got.cpu().double().numpy() - y[rows])
+        assert np.all(err <= 24 * u * (1 + np.abs(y[rows]))), float(err.max())
