@@ -528,8 +528,8 @@ RRA_API rra_status rra_qk_norm_rope(const void* q, long long q_stride, const voi
                                     long long kv_out_rows, void* stream);
 
 /* Attention over whole prompts: B packed sequences, sequence b in rows
- * cu_seqlens[b] .. cu_seqlens[b+1], of any length up to max_seqlen (which has
- * no upper limit but B * Hq * ceil(max_seqlen / 128) < 2^31).  Row i of a sequence
+ * cu_seqlens[b] .. cu_seqlens[b+1], of any length up to max_seqlen (at
+ * most 2^30).  Row i of a sequence
  * attends to its rows j <= i when `causal` is set, else to all its rows:
  *   o[i, h] = sum_j softmax_j(scale <q[i, h], k[j, h']>) v[j, h'].
  * q [cap, Hq, d], k and v [cap, Hkv, d]; o [cap, Hq, d] contiguous, of the

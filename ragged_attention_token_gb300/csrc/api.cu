@@ -782,8 +782,7 @@ rra_status rra_attend_prompt(const void* q, long long q_stride, const void* k, l
                              int Hkv, int d, float scale, int causal, rra_dtype dtype, void* o, void* stream) {
   RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
   if (max_seqlen < 1) return fail(RRA_ERR_INVALID_ARG, "max_seqlen=%d < 1", max_seqlen);
-  if (static_cast<long long>(B) * Hq * ((max_seqlen + 127LL) / 128) >= (1LL << 31))
-    return fail(RRA_ERR_UNSUPPORTED, "B * Hq * ceil(max_seqlen / 128) >= 2^31");
+  if (max_seqlen > (1 << 30)) return fail(RRA_ERR_UNSUPPORTED, "max_seqlen=%d > 2^30", max_seqlen);
   if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
   RRA_CHECK_PTR(q);
   RRA_CHECK_PTR(k);

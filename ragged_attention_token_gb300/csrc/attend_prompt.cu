@@ -1,63 +1,600 @@
-// Attention over packed prompts.  One warp per (row, query head): lanes hold
-// d/32 elements each, a running maximum and sum over the keys.
+// Attention over packed prompts: TMA tile loads, tcgen05.mma with TMEM
+// accumulators, warp-specialised, persistent.
+//
+// For row i of a sequence and the keys j it sees (j <= i when causal, all of
+// the sequence otherwise): o_i = sum_j 2^(c s_ij - m) v_j / sum_j 2^(c s_ij - m),
+// s = <q_i, k_j>, c = scale log2 e, m a per-row reference.
+//
+// A unit is (sequence, query head, 256 query rows): two tiles of 128 rows (A
+// and B; one TMEM lane per row).  Keys stream in blocks of 128 that both tiles
+// use, so each K/V byte read from L2 serves 256 rows.  Per SM one CTA, its warps:
+//   warps 0-3 / 4-7  softmax of tile A / B, thread r owning row r: the block's
+//            scores from TMEM into registers, their maximum, the weights in
+//            base 2, written over the scores as 16-bit pairs;
+//   warp 8   TMA loads: Q tiles, then K and V blocks through one ring;
+//   warp 9   products, one elected lane: S = Q K^T (128 x 128 x d) and
+//            O += P V (128 x d x 128, P read from TMEM).  While one tile's
+//            softmax runs, the tensor core works for the other tile.
+//
+// The reference of a row is its first block's maximum; it moves (rescaling O in
+// TMEM) only when a later maximum exceeds it by more than 8, so a weight is at
+// most 2^8, and O is touched by the softmax warps in few blocks.  Weights are
+// rounded to the input type for the second product (relative 2^-8 in bf16, 2^-11 in
+// fp16; the size of the output's own rounding and averaging out over the keys);
+// their sum is taken from the unrounded ones.  In fp16 all weights carry a
+// factor 2^7, which cancels, so that only weights below 2^-21 of the largest
+// are subnormal.
+//
+// P overwrites S, and the documented order of two products covers only one
+// accumulator, so the next S of a tile waits until the P V before it has completed.
+//
+// Keys past the end are masked, and the V rows that the last product reads past
+// it are zeroed in shared memory: what the buffer holds there (NaN) reaches no
+// output.  Units are walked longest first: query tiles in descending order,
+// (sequence, head) within; each CTA finds its units by ballots over
+// cu_seqlens, counting only those with rows, in alternating direction from
+// round to round.  Every wait is bounded; a CTA that gives up records
+// RRA_DEVERR_WAIT_TIMEOUT, lets copies and products in flight land, frees its
+// TMEM and returns.
+#include <mutex>
+
 #include "common.cuh"
+#include "tc_ptx.cuh"
+#include "softmax_tc.cuh"
 
 namespace rra {
 namespace {
 
-template <typename T> __device__ __forceinline__ float to_f(T x) { return static_cast<float>(x); }
+constexpr int PT = 128;                      // rows of a tile, keys of a block
+constexpr int P_SOFTMAX_WARPS = 8;
+constexpr int P_LOAD_WARP = 8, P_MMA_WARP = 9;
+constexpr int P_THREADS = 384;               // three warpgroups; warps 10 and 11 only lend their registers
+// Registers: 384 threads start with 168 each; the softmax warpgroups take 216
+// (a row's 128 scores stay in registers), the third gives down to 72:
+// 8 x 216 + 4 x 72 = 12 x 168.
+constexpr int P_REGS_SOFTMAX = 216, P_REGS_OTHER = 72;
+static_assert(8 * P_REGS_SOFTMAX + 4 * P_REGS_OTHER <= 12 * 168, "register split exceeds the launch's registers");
+constexpr uint32_t P_TMEM_COLS = 512;
+constexpr uint32_t P_SUB = PT * 128;         // one 64-element column group of a tile: 128 rows x 128 B
+constexpr float P_MOVE = 8.f;                // log2 units by which a maximum may exceed the reference
 
-template <typename T, int D>
-__global__ void attend_prompt_kernel(const PromptArgs a) {
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y % a.Hq, b = blockIdx.y / a.Hq;
-  const int s0 = a.cu[b], n = a.cu[b + 1] - s0;
-  if (n < 0 || n > a.max_seqlen || s0 < 0 || s0 > a.cap - n) {
-    if (threadIdx.x == 0)
-      record_error(a.err, n < 0 ? RRA_DEVERR_SEQ_NEGATIVE
-                                : (n > a.max_seqlen ? RRA_DEVERR_SEQ_TOO_LONG : RRA_DEVERR_INDEX_RANGE));
-    return;
+template <int D>
+struct PromptCfg {
+  static constexpr uint32_t TILE = (D / 64) * P_SUB;              // a Q tile, a K block or a V block
+  static constexpr int SLOTS = D == 128 ? 5 : 8;                  // K/V ring: 160 / 128 KB
+  static constexpr uint32_t OFF_KV = 2 * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_KV + SLOTS * TILE;
+  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;          // slack to align the base to 1024 B
+  static constexpr uint32_t T_S = 0, T_O = 2 * PT;                // TMEM columns: S/P of A and B, then O of A and B
+};
+
+// Barrier and word offsets from OFF_BAR.
+constexpr uint32_t PB_KV_FULL = 0;      // [8]
+constexpr uint32_t PB_KV_EMPTY = 64;    // [8]
+constexpr uint32_t PB_Q_FULL = 128;     // [2]
+constexpr uint32_t PB_Q_EMPTY = 144;    // [2]
+constexpr uint32_t PB_S_FULL = 160;     // [2] S product done
+constexpr uint32_t PB_P_READY = 176;    // [2] P written (128 arrivals)
+constexpr uint32_t PB_PV_DONE = 192;    // [2] P V product done
+constexpr uint32_t PB_U_FULL = 208;     // [2] unit descriptor written
+constexpr uint32_t PB_U_EMPTY = 224;    // [2] unit finished (softmax warps and the product warp)
+constexpr uint32_t PB_DRAIN = 240;
+constexpr uint32_t PW_TMEM = 248, PW_ABORT = 252;
+constexpr uint32_t P_DESC = 256;        // [2] x 32 bytes: s0, n, q0, h (q0 < 0: no more units)
+
+struct PromptUnit {
+  int s0, n, q0, h;
+  __device__ bool has_b() const { return n - q0 > PT; }
+  // Key blocks of tile w.
+  __device__ int blocks(int w, int causal) const {
+    if (w == 1 && !has_b()) return 0;
+    const int all = (n + PT - 1) / PT;
+    return causal ? min(all, q0 / PT + 1 + w) : all;
   }
-  const int i = blockIdx.x * 4 + warp;
-  if (i >= n) return;
-  const int hk = h / (a.Hq / a.Hkv);
-  const T* q = static_cast<const T*>(a.q) + static_cast<long long>(s0 + i) * a.q_stride + h * D + lane * E;
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_f(q[e]);
-    o[e] = 0.f;
+};
+
+// Walks the non-empty units in order (query tile descending, sequence, head);
+// a warp's lanes look at 32 sequences at a time.  The walk only moves forward.
+struct UnitWalk {
+  int qt;              // current query tile (256 rows), from the highest
+  int b0;              // current group of 32 sequences
+  long long before;    // non-empty units before the group (qt, b0)
+  int lane;
+
+  __device__ int rows_of(const PromptArgs& a, int b, int& s0, int& n, bool record) const {
+    if (b >= a.B) return 0;
+    s0 = __ldg(a.cu + b);
+    n = __ldg(a.cu + b + 1) - s0;
+    if (n < 0 || n > a.max_seqlen || s0 < 0 || s0 > a.cap - n) {
+      if (record)
+        record_error(a.err, n < 0 ? RRA_DEVERR_SEQ_NEGATIVE
+                                  : (n > a.max_seqlen ? RRA_DEVERR_SEQ_TOO_LONG : RRA_DEVERR_INDEX_RANGE));
+      return 0;
+    }
+    return n;
   }
-  const int keys = a.causal ? i + 1 : n;
-  for (int j = 0; j < keys; ++j) {
-    const T* k = static_cast<const T*>(a.k) + static_cast<long long>(s0 + j) * a.k_stride + hk * D + lane * E;
-    const T* v = static_cast<const T*>(a.v) + static_cast<long long>(s0 + j) * a.v_stride + hk * D + lane * E;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += qv[e] * to_f(k[e]);
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float c = mn == -INFINITY ? 1.f : exp2f(m - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    m = mn;
-    l = l * c + p;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f(v[e]);
+
+  // The unit with index `target` (not below any earlier target), or q0 < 0.
+  __device__ PromptUnit find(const PromptArgs& a, long long target, bool record) {
+    PromptUnit u;
+    while (qt >= 0) {
+      int s0 = 0, n = 0;
+      const int rows = rows_of(a, b0 + lane, s0, n, record && qt == 0);
+      const unsigned live = __ballot_sync(0xffffffffu, rows > qt * 2 * PT);
+      const long long here = static_cast<long long>(__popc(live)) * a.Hq;
+      if (target < before + here) {
+        const int k = static_cast<int>((target - before) / a.Hq);      // k-th live sequence of the group
+        const bool mine = ((live >> lane) & 1u) && __popc(live & ((1u << lane) - 1u)) == k;
+        const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        u.s0 = __shfl_sync(0xffffffffu, s0, src);
+        u.n = __shfl_sync(0xffffffffu, n, src);
+        u.q0 = qt * 2 * PT;
+        u.h = static_cast<int>((target - before) % a.Hq);
+        return u;
+      }
+      before += here;
+      b0 += 32;
+      if (b0 >= a.B) {
+        b0 = 0;
+        --qt;
+      }
+    }
+    u.q0 = -1;
+    return u;
   }
-  T* out = static_cast<T*>(a.o) + (static_cast<long long>(s0 + i) * a.Hq + h) * D + lane * E;
-  for (int e = 0; e < E; ++e) out[e] = T(l > 0.f ? o[e] / l : (l == 0.f ? 0.f : l));
+};
+
+// One block of one row: weights from the scores at tS (128 TMEM columns) back
+// over them, 2 per column.  MASK: columns from `lim` on are invisible.
+template <bool BF, int D, bool MASK>
+__device__ __forceinline__ void prompt_softmax(uint32_t tS, uint32_t tO, int lim, bool first, float c2, float& m_ref,
+                                               float& l_run) {
+  float s[PT];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) tmem_ld32_nowait(tS + 32 * g, s + 32 * g);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) tmem_wait_ld32(s + 32 * g);
+  if constexpr (MASK) {
+#pragma unroll
+    for (int i = 0; i < PT; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+  }
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < PT; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx[k] = max3f(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
+  }
+  const float x = max3f(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c2;
+  const bool move = x > m_ref + P_MOVE;
+  if (__any_sync(0xffffffffu, move)) {
+    const float alpha = move ? fast_exp2(m_ref - x) : 1.f;
+    if (move) m_ref = x;
+    l_run *= alpha;
+    if (!first) {
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) {
+        float o[32];
+        tmem_ld32(tO + 32 * g, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_st8(tO + 32 * g + 8 * i, reinterpret_cast<const uint32_t*>(o) + 8 * i);
+      }
+    }
+  }
+  // A row that has seen only -inf scores keeps its reference at -inf: weights 0.
+  const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (BF ? 0.f : 7.f);
+  const uint64_t c2x2 = pack_f2(c2, c2), nm2 = pack_f2(-mu, -mu);
+  uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = 16 * g + 2 * i;
+      float x0, x1;
+      unpack_f2(fma_f2(pack_f2(s[col], s[col + 1]), c2x2, nm2), x0, x1);
+      const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+      acc[i & 1] = add_f2(acc[i & 1], pack_f2(p0, p1));
+      if constexpr (BF) w[i] = pack2<__nv_bfloat162>(p0, p1);
+      else w[i] = pack2<__half2>(p0, p1);
+    }
+    tmem_st8(tS + 8 * g, w);
+  }
+  float a0, a1;
+  unpack_f2(add_f2(acc[0], acc[1]), a0, a1);
+  l_run += a0 + a1;
+  tmem_st_wait();
 }
 
-template <typename T>
-cudaError_t launch_d(const PromptArgs& a, int d, cudaStream_t stream) {
-  const dim3 grid((a.max_seqlen + 3) / 4, a.B * a.Hq);
-  if (d == 64) attend_prompt_kernel<T, 64><<<grid, 128, 0, stream>>>(a);
-  else attend_prompt_kernel<T, 128><<<grid, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+template <typename T, int D>
+__global__ void __launch_bounds__(P_THREADS, 1)
+    attend_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+  using C = PromptCfg<D>;
+  constexpr bool BF = IsBf16<T>::value == 1;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::OFF_BAR;
+  auto bar = [&](uint32_t kind, int i) { return bars + kind + 8 * static_cast<uint32_t>(i); };
+  auto s_q = [&](int w) { return base + static_cast<uint32_t>(w) * C::TILE; };
+  auto s_kv = [&](int i) { return base + C::OFF_KV + static_cast<uint32_t>(i) * C::TILE; };
+  const uint32_t abort_flag = bars + PW_ABORT;
+  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(gbase + C::OFF_BAR + PW_TMEM);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == P_MMA_WARP) {
+    tmem_alloc(bars + PW_TMEM, P_TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(bar(PB_KV_FULL, i), 1);
+      mbar_init(bar(PB_KV_EMPTY, i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(PB_Q_FULL, i), 1);
+      mbar_init(bar(PB_Q_EMPTY, i), 1);
+      mbar_init(bar(PB_S_FULL, i), 1);
+      mbar_init(bar(PB_P_READY, i), PT);
+      mbar_init(bar(PB_PV_DONE, i), 1);
+      mbar_init(bar(PB_U_FULL, i), 1);
+      mbar_init(bar(PB_U_EMPTY, i), P_SOFTMAX_WARPS + 1);
+    }
+    mbar_init(bar(PB_DRAIN, 0), 1);
+    st_shared_u32(abort_flag, 0u);
+    fence_barrier_init();
+    prefetch_tensormap(&map_q);
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool bad = false;
+  // A bounded wait; every lane of the warp leaves with the same `bad`.
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (!mbar_wait_or_abort(b, parity, abort_flag)) bad = true;
+    bad = __any_sync(0xffffffffu, bad);
+    return !bad;
+  };
+  auto read_unit = [&](int i) {
+    const uint32_t d = bars + P_DESC + 32u * static_cast<uint32_t>(i & 1);
+    PromptUnit u;
+    u.s0 = static_cast<int>(ld_shared_u32(d));
+    u.n = static_cast<int>(ld_shared_u32(d + 4));
+    u.q0 = static_cast<int>(ld_shared_u32(d + 8));
+    u.h = static_cast<int>(ld_shared_u32(d + 12));
+    return u;
+  };
+
+  if (warp >= P_SOFTMAX_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P_REGS_OTHER));
+    if (warp == P_LOAD_WARP) {
+      // ------------------------------------------------------------ loads
+      UnitWalk walk{(a.max_seqlen - 1) / (2 * PT), 0, 0, lane};
+      const long long G = gridDim.x, c = blockIdx.x;
+      uint32_t it = 0, nq[2] = {0, 0};
+      const bool recorder = blockIdx.x == 0;
+      for (int i = 0; !bad; ++i) {
+        // Round i of G units, walked forwards and backwards in turn.
+        const PromptUnit u = walk.find(a, i * G + ((i & 1) ? G - 1 - c : c), recorder);
+        if (i >= 2 && !wait(bar(PB_U_EMPTY, i & 1), ((i >> 1) - 1) & 1)) break;
+        if (lane == 0) {
+          const uint32_t d = bars + P_DESC + 32u * static_cast<uint32_t>(i & 1);
+          st_shared_u32(d, static_cast<uint32_t>(u.s0));
+          st_shared_u32(d + 4, static_cast<uint32_t>(u.n));
+          st_shared_u32(d + 8, static_cast<uint32_t>(u.q0));
+          st_shared_u32(d + 12, static_cast<uint32_t>(u.h));
+          mbar_arrive(bar(PB_U_FULL, i & 1));
+        }
+        __syncwarp();
+        if (u.q0 < 0) break;
+        const int hk = u.h / (a.Hq / a.Hkv);
+        const int nb = max(u.blocks(0, a.causal), u.blocks(1, a.causal));
+        auto load_q = [&](int w) {
+          if (nq[w] > 0 && !wait(bar(PB_Q_EMPTY, w), (nq[w] - 1) & 1)) return;
+          ++nq[w];
+          if (lane == 0) {
+            mbar_expect_tx(bar(PB_Q_FULL, w), C::TILE);
+            for (int g = 0; g < D / 64; ++g)
+              tma_load_3d(s_q(w) + g * P_SUB, &map_q, 64 * g, u.h, u.s0 + u.q0 + w * PT, bar(PB_Q_FULL, w));
+          }
+          __syncwarp();
+        };
+        auto load_kv = [&](const CUtensorMap* map, int j) {
+          const int s = static_cast<int>(it % C::SLOTS);
+          if (it >= C::SLOTS && !wait(bar(PB_KV_EMPTY, s), (it / C::SLOTS - 1) & 1)) return;
+          ++it;
+          if (lane == 0) {
+            mbar_expect_tx(bar(PB_KV_FULL, s), C::TILE);
+            for (int g = 0; g < D / 64; ++g)
+              tma_load_3d(s_kv(s) + g * P_SUB, map, 64 * g, hk, u.s0 + j * PT, bar(PB_KV_FULL, s));
+          }
+          __syncwarp();
+        };
+        load_q(0);
+        if (!bad) load_kv(&map_k, 0);
+        if (!bad && u.has_b()) load_q(1);
+        if (!bad) load_kv(&map_v, 0);
+        for (int j = 1; j < nb && !bad; ++j) {
+          load_kv(&map_k, j);
+          if (!bad) load_kv(&map_v, j);
+        }
+      }
+    } else if (warp == P_MMA_WARP) {
+      // ------------------------------------------------------------ products
+      const uint32_t idesc_s = idesc_f16(BF ? 1u : 0u, 0, PT, PT);
+      const uint32_t idesc_pv = idesc_f16(BF ? 1u : 0u, 1, PT, D);
+      uint32_t kv0 = 0;                       // ring index of the unit's K block 0; K j at kv0 + 2j, V j one after
+      uint32_t nq_a = 0, nq_b = 0, npv_a = 0, npv_b = 0;   // Q tiles and P V products of each tile so far
+      auto kv_slot = [&](uint32_t idx) { return static_cast<int>(idx % C::SLOTS); };
+      auto kv_wait = [&](uint32_t idx) { return wait(bar(PB_KV_FULL, kv_slot(idx)), (idx / C::SLOTS) & 1); };
+      // S of tile w with the K block at ring index idx; the P V product before it on this tile has completed.
+      auto issue_s = [&](int w, uint32_t idx, bool last) {
+        tc_fence_after();
+        const uint32_t sk = s_kv(kv_slot(idx));
+        const bool leader = elect_one();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * P_SUB + (kk % 4) * 32;
+          const uint64_t da = sdesc(s_q(w) + off, 16, 1024), db = sdesc(sk + off, 16, 1024);
+          if (leader) umma_f16(tmem + C::T_S + w * PT, da, db, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        if (leader) {
+          umma_commit(bar(PB_S_FULL, w));
+          if (last) umma_commit(bar(PB_Q_EMPTY, w));
+        }
+        __syncwarp();
+      };
+      auto release = [&](uint32_t idx) {
+        if (elect_one()) umma_commit(bar(PB_KV_EMPTY, kv_slot(idx)));
+        __syncwarp();
+      };
+      // First S of tile w of a unit: its Q tile landed, the tile's last P V product done.
+      auto first_s = [&](int w, uint32_t idx, bool last) {
+        if (!wait(bar(PB_Q_FULL, w), (w ? nq_b : nq_a) & 1)) return;
+        ++(w ? nq_b : nq_a);
+        const uint32_t npv = w ? npv_b : npv_a;
+        if (npv > 0 && !wait(bar(PB_PV_DONE, w), (npv - 1) & 1)) return;
+        issue_s(w, idx, last);
+      };
+      PromptUnit u{0, 0, -1, 0};
+      bool a_started = false;                 // tile A's first S was issued during the previous unit
+      if (wait(bar(PB_U_FULL, 0), 0)) u = read_unit(0);
+      for (int i = 0; !bad && u.q0 >= 0; ++i) {
+        const int nba = u.blocks(0, a.causal), nbb = u.blocks(1, a.causal), nb = max(nba, nbb);
+        PromptUnit next;
+        next.q0 = -2;                         // not read yet
+        if (!a_started) {
+          if (!kv_wait(kv0)) break;
+          first_s(0, kv0, nba == 1);
+          if (bad) break;
+        }
+        a_started = false;
+        if (nbb > 0) {
+          first_s(1, kv0, nbb == 1);
+          if (bad) break;
+        }
+        release(kv0);
+        for (int j = 0; j < nb && !bad; ++j) {
+          const uint32_t vi = kv0 + 2 * j + 1, ki = vi + 1;
+          if (!kv_wait(vi)) break;
+          const int valid = min(PT, u.n - j * PT);                // keys of the block
+          const int ksteps = (valid + 15) / 16;
+          const uint32_t sv = s_kv(kv_slot(vi));
+          if (valid < PT) {
+            // V rows [valid, 16 ksteps): zeros, whatever lies behind the sequence.
+            for (int z = lane; z < (16 * ksteps - valid) * 8 * (D / 64); z += 32) {
+              const int g = z / ((16 * ksteps - valid) * 8), r = z % ((16 * ksteps - valid) * 8);
+              st_shared_v4(sv + g * P_SUB + valid * 128 + r * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            const int nbw = w == 0 ? nba : nbb;
+            if (j < nbw) {
+              uint32_t& npv = w ? npv_b : npv_a;
+              if (!wait(bar(PB_P_READY, w), npv & 1)) break;
+              tc_fence_after();
+              const bool leader = elect_one();
+#pragma unroll 1
+              for (int kk = 0; kk < ksteps; ++kk) {
+                const uint64_t db = sdesc(sv + kk * 2048, P_SUB, 1024);
+                if (leader)
+                  umma_f16_tmem_a(tmem + C::T_O + w * D, tmem + C::T_S + w * PT + kk * 8, db, idesc_pv,
+                                  (j > 0 || kk > 0) ? 1u : 0u);
+              }
+              if (leader) umma_commit(bar(PB_PV_DONE, w));
+              __syncwarp();
+              ++npv;
+              if (j + 1 < nbw) {
+                if (!kv_wait(ki)) break;
+                if (!wait(bar(PB_PV_DONE, w), (npv - 1) & 1)) break;
+                issue_s(w, ki, j + 2 == nbw);
+              }
+            }
+            if (w == 0 && nbb > 0 && j == nbb - 1) {
+              // Tile A has no more products in this unit: its first S of the
+              // next unit goes ahead of tile B's last P V.
+              if (!wait(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
+              next = read_unit(i + 1);
+              if (next.q0 >= 0) {
+                if (!kv_wait(kv0 + 2 * nb)) break;
+                first_s(0, kv0 + 2 * nb, next.blocks(0, a.causal) == 1);
+                if (bad) break;
+                a_started = true;
+              }
+            }
+          }
+          if (bad) break;
+          release(vi);
+          if (j + 1 < nb) release(ki);
+        }
+        if (bad) break;
+        kv0 += 2 * static_cast<uint32_t>(nb);
+        if (next.q0 == -2) {
+          if (!wait(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
+          next = read_unit(i + 1);
+        }
+        if (lane == 0) mbar_arrive(bar(PB_U_EMPTY, i & 1));
+        __syncwarp();
+        u = next;
+      }
+      if (!bad) {
+        if (elect_one()) umma_commit(bar(PB_DRAIN, 0));
+        __syncwarp();
+        wait(bar(PB_DRAIN, 0), 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P_REGS_SOFTMAX));
+    const int w = warp >> 2, row = tid & (PT - 1);
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::T_S + w * PT, tO = tmem + lane_off + C::T_O + w * D;
+    uint32_t count = 0;                     // blocks of this tile so far
+    for (int i = 0;; ++i) {
+      if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
+      const PromptUnit u = read_unit(i);
+      if (u.q0 < 0) break;
+      const int nbw = u.blocks(w, a.causal);
+      float m_ref = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < nbw; ++j) {
+        if (!wait(bar(PB_S_FULL, w), count & 1)) break;
+        ++count;
+        tc_fence_after();
+        if (j + 1 < nbw) {
+          prompt_softmax<BF, D, false>(tS, tO, PT, j == 0, a.scale_log2, m_ref, l_run);
+        } else {
+          // The last block: the sequence's end, and the diagonal when causal.
+          int lim = u.n - j * PT;
+          if (a.causal) lim = min(lim, u.q0 + w * PT + row - j * PT + 1);
+          prompt_softmax<BF, D, true>(tS, tO, lim, j == 0, a.scale_log2, m_ref, l_run);
+        }
+        tc_fence_before();
+        mbar_arrive(bar(PB_P_READY, w));
+      }
+      if (bad) break;
+      if (nbw > 0) {
+        if (!wait(bar(PB_PV_DONE, w), (count - 1) & 1)) break;
+        tc_fence_after();
+        const int r = u.q0 + w * PT + row;
+        const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
+        T* out = static_cast<T*>(a.o) + (static_cast<long long>(u.s0 + r) * a.Hq + u.h) * D;
+#pragma unroll
+        for (int g = 0; g < D / 16; ++g) {
+          float o[16];
+          tmem_ld16(tO + 16 * g, o);
+          if (r < u.n) store16<T>(out + 16 * g, o, inv);
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(PB_U_EMPTY, i & 1));
+    }
+  }
+  if (bad && lane == 0) {
+    st_shared_u32(abort_flag, 1u);
+    record_error(a.err, RRA_DEVERR_WAIT_TIMEOUT);
+  }
+
+  // Teardown: after an abort, copies and products still in flight get a
+  // bounded grace period (~1 ms) to land before the TMEM is released.
+  tc_fence_before();
+  __syncthreads();
+  if (warp == P_MMA_WARP) {
+    if (lane == 0 && ld_shared_volatile_u32(abort_flag) != 0u) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 2000000LL) {
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, P_TMEM_COLS);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 prompt_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// 3-D map over a [rows, H, d] tensor with rows `stride` elements apart: box =
+// 128 rows of 64 elements of one head, 128-byte swizzle.
+cudaError_t make_map_rows(CUtensorMap* map, const void* ptr, int rows, int H, int d, long long stride, bool bf16) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, 1, PT};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = prompt_encode_fn()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+  using C = PromptCfg<D>;
+  auto kernel = attend_prompt_kernel<T, D>;
+  constexpr int kMaxDevices = 64;
+  static bool attr_set[kMaxDevices] = {};
+  static std::mutex m;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(m);
+    if (!attr_set[dev]) {
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess)
+        return e;
+      attr_set[dev] = true;
+    }
+  }
+  const bool bf16 = IsBf16<T>::value == 1;
+  CUtensorMap mq, mk, mv;
+  if ((e = make_map_rows(&mq, a.q, a.cap, a.Hq, D, a.q_stride, bf16)) != cudaSuccess) return e;
+  if ((e = make_map_rows(&mk, a.k, a.cap, a.Hkv, D, a.k_stride, bf16)) != cudaSuccess) return e;
+  if ((e = make_map_rows(&mv, a.v, a.cap, a.Hkv, D, a.v_stride, bf16)) != cudaSuccess) return e;
+  const long long units = static_cast<long long>(a.B) * a.Hq * ((a.max_seqlen + 2LL * PT - 1) / (2 * PT));
+  const int grid = static_cast<int>(units < num_sms ? units : num_sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(P_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_prompt(const PromptArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream) {
-  return dt == RRA_BF16 ? launch_d<__nv_bfloat16>(a, d, stream) : launch_d<__half>(a, d, stream);
+  if (prompt_encode_fn() == nullptr) return cudaErrorNotSupported;
+  if (dt == RRA_BF16)
+    return d == 64 ? launch_d<__nv_bfloat16, 64>(a, num_sms, stream) : launch_d<__nv_bfloat16, 128>(a, num_sms, stream);
+  return d == 64 ? launch_d<__half, 64>(a, num_sms, stream) : launch_d<__half, 128>(a, num_sms, stream);
 }
 
 }  // namespace rra

@@ -65,16 +65,12 @@ PROMPT = dict(q=0x1000000, qs=2560, k=0x1000000 + 2048 * 2, ks=2560, v=0x1000000
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(d=32), UNS), (dict(S=0), INV), (dict(B=65535, Hq=16384, S=1 << 20), UNS), (dict(Hq=3), INV), (dict(B=0), INV),
+    (dict(d=32), UNS), (dict(S=0), INV), (dict(S=(1 << 30) + 1), UNS), (dict(Hq=3), INV), (dict(B=0), INV),
     (dict(cap=0), INV), (dict(scale=NAN), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV),
     (dict(scale=float("inf")), INV), (dict(dt=rra.RRA_F32), INV), (dict(q=None), INV), (dict(o=None), INV),
     (dict(cu=None), INV), (dict(cu=0x302), MIS), (dict(v=0x1000008), MIS), (dict(ks=2556), MIS), (dict(vs=128), INV),
     (dict(o=0x1000000), INV), (dict(o=0x1000000 + 64 * 2560 * 2 - 640), INV)])
 def test_attend_prompt_refusals(L, kw, want):
-    # B=65535, S=2^20 keeps B*Hq*tiles past 2^31 for Hq = 16384 (a multiple of Hkv = 2)
-    kw = dict(kw)
-    if kw.get("Hq") == 16384:
-        kw.update(qs=16384 * 128)
     assert _call(L.rra_attend_prompt, PROMPT, kw) == want
 
 
