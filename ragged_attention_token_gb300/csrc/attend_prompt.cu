@@ -12,7 +12,8 @@
 //            scores from TMEM into registers, their maximum, the weights in
 //            base 2, written over the scores as 16-bit pairs;
 //   warp 8   TMA loads: Q tiles, then K and V blocks through one ring;
-//   warp 9   products, one elected lane: S = Q K^T (128 x 128 x d) and
+//   warp 10  zeroes the V rows behind a sequence's end in its last block;
+//   warp 9   products, one thread: S = Q K^T (128 x 128 x d) and
 //            O += P V (128 x d x 128, P read from TMEM).  While one tile's
 //            softmax runs, the tensor core works for the other tile.
 //
@@ -47,8 +48,8 @@ namespace {
 
 constexpr int PT = 128;                      // rows of a tile, keys of a block
 constexpr int P_SOFTMAX_WARPS = 8;
-constexpr int P_LOAD_WARP = 8, P_MMA_WARP = 9;
-constexpr int P_THREADS = 384;               // three warpgroups; warps 10 and 11 only lend their registers
+constexpr int P_LOAD_WARP = 8, P_MMA_WARP = 9, P_TAIL_WARP = 10;
+constexpr int P_THREADS = 384;               // three warpgroups; warp 11 only lends its registers
 // Registers: 384 threads start with 168 each; the softmax warpgroups take 216
 // (a row's 128 scores stay in registers), the third gives down to 72:
 // 8 x 216 + 4 x 72 = 12 x 168.
@@ -64,8 +65,12 @@ struct PromptCfg {
   static constexpr int SLOTS = D == 128 ? 5 : 8;                  // K/V ring: 160 / 128 KB
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_KV + SLOTS * TILE;
-  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;          // slack to align the base to 1024 B
-  static constexpr uint32_t T_S = 0, T_O = 2 * PT;                // TMEM columns: S/P of A and B, then O of A and B
+  static constexpr uint32_t SMEM = OFF_BAR + 512;
+  // TMEM columns: S of A and B, O of A and B; P over S, or, where there is
+  // room (d = 64), beside it: then the next S need not wait for this P V, and
+  // goes as soon as the scores are in registers (32 heads, 8192 rows, not causal: 594 -> 547 us).
+  static constexpr bool OWN_P = D == 64;
+  static constexpr uint32_t T_S = 0, T_O = 2 * PT, T_P = OWN_P ? T_O + 2 * D : T_S, P_STEP = OWN_P ? PT / 2 : PT;
 };
 
 // Barrier and word offsets from OFF_BAR.
@@ -74,13 +79,15 @@ constexpr uint32_t PB_KV_EMPTY = 64;    // [8]
 constexpr uint32_t PB_Q_FULL = 128;     // [2]
 constexpr uint32_t PB_Q_EMPTY = 144;    // [2]
 constexpr uint32_t PB_S_FULL = 160;     // [2] S product done
-constexpr uint32_t PB_P_READY = 176;    // [2] P written (128 arrivals)
+constexpr uint32_t PB_P_READY = 176;    // [2] P written (one arrival per softmax warp of the tile)
 constexpr uint32_t PB_PV_DONE = 192;    // [2] P V product done
 constexpr uint32_t PB_U_FULL = 208;     // [2] unit descriptor written
-constexpr uint32_t PB_U_EMPTY = 224;    // [2] unit finished (softmax warps and the product warp)
+constexpr uint32_t PB_U_EMPTY = 224;    // [2] unit finished (softmax, product and tail warps)
 constexpr uint32_t PB_DRAIN = 240;
 constexpr uint32_t PW_TMEM = 248, PW_ABORT = 252;
 constexpr uint32_t P_DESC = 256;        // [2] x 32 bytes: s0, n, q0, h (q0 < 0: no more units)
+constexpr uint32_t PB_S_READ = 320;     // [2] the scores are in registers (one arrival per softmax warp of the tile)
+constexpr uint32_t PB_TAIL = 336;       // [2] a V block's tail to zero; zeroed
 
 struct PromptUnit {
   int s0, n, q0, h;
@@ -144,12 +151,10 @@ struct UnitWalk {
   }
 };
 
-// One block of one row: weights from the scores at tS (128 TMEM columns) back
-// over them, 2 per column.  MASK: columns from `lim` on are invisible.
-template <bool BF, int D, bool MASK>
-__device__ __forceinline__ void prompt_softmax(uint32_t tS, uint32_t tO, int lim, bool first, float c2, float& m_ref,
-                                               float& l_run) {
-  float s[PT];
+// The row's 128 scores into registers (columns from `lim` on invisible when
+// MASK) and their maximum.
+template <bool MASK>
+__device__ __forceinline__ float prompt_scores(uint32_t tS, int lim, float (&s)[PT]) {
 #pragma unroll
   for (int g = 0; g < 4; ++g) tmem_ld32_nowait(tS + 32 * g, s + 32 * g);
 #pragma unroll
@@ -164,30 +169,33 @@ __device__ __forceinline__ void prompt_softmax(uint32_t tS, uint32_t tO, int lim
 #pragma unroll
     for (int k = 0; k < 4; ++k) mx[k] = max3f(mx[k], s[i + 2 * k], s[i + 2 * k + 1]);
   }
-  const float x = max3f(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c2;
-  const bool move = x > m_ref + P_MOVE;
-  if (__any_sync(0xffffffffu, move)) {
-    const float alpha = move ? fast_exp2(m_ref - x) : 1.f;
-    if (move) m_ref = x;
-    l_run *= alpha;
-    if (!first) {
+  return max3f(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+}
+
+// The row's D columns of O times alpha.
+template <int D>
+__device__ __forceinline__ void prompt_rescale(uint32_t tO, float alpha) {
 #pragma unroll
-      for (int g = 0; g < D / 32; ++g) {
-        float o[32];
-        tmem_ld32(tO + 32 * g, o);
+  for (int g = 0; g < D / 16; ++g) {
+    float o[16];
+    tmem_ld16(tO + 16 * g, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= alpha;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_st8(tO + 32 * g + 8 * i, reinterpret_cast<const uint32_t*>(o) + 8 * i);
-      }
-    }
+    for (int i = 0; i < 16; ++i) o[i] *= alpha;
+    tmem_st8(tO + 16 * g, reinterpret_cast<const uint32_t*>(o));
+    tmem_st8(tO + 16 * g + 8, reinterpret_cast<const uint32_t*>(o) + 8);
   }
+}
+
+// The weights of the row's scores to tP, two per TMEM column, against the
+// reference m_ref; returns their sum.
+template <bool BF>
+__device__ __forceinline__ float prompt_weights(uint32_t tP, const float (&s)[PT], float c2, float m_ref) {
   // A row that has seen only -inf scores keeps its reference at -inf: weights 0.
   const float mu = (m_ref == -INFINITY ? 0.f : m_ref) - (BF ? 0.f : 7.f);
   const uint64_t c2x2 = pack_f2(c2, c2), nm2 = pack_f2(-mu, -mu);
   uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
+  for (int g = 0; g < PT / 16; ++g) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -199,12 +207,11 @@ __device__ __forceinline__ void prompt_softmax(uint32_t tS, uint32_t tO, int lim
       if constexpr (BF) w[i] = pack2<__nv_bfloat162>(p0, p1);
       else w[i] = pack2<__half2>(p0, p1);
     }
-    tmem_st8(tS + 8 * g, w);
+    tmem_st8(tP + 8 * g, w);
   }
   float a0, a1;
   unpack_f2(add_f2(acc[0], acc[1]), a0, a1);
-  l_run += a0 + a1;
-  tmem_st_wait();
+  return a0 + a1;
 }
 
 template <typename T, int D>
@@ -213,16 +220,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                          const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
   using C = PromptCfg<D>;
   constexpr bool BF = IsBf16<T>::value == 1;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* gbase = smem_raw + (base - raw);
+  extern __shared__ __align__(1024) uint8_t smem_prompt[];   // the swizzled tiles start 1024-byte aligned
+  const uint32_t base = smem_u32(smem_prompt);
   const uint32_t bars = base + C::OFF_BAR;
   auto bar = [&](uint32_t kind, int i) { return bars + kind + 8 * static_cast<uint32_t>(i); };
   auto s_q = [&](int w) { return base + static_cast<uint32_t>(w) * C::TILE; };
   auto s_kv = [&](int i) { return base + C::OFF_KV + static_cast<uint32_t>(i) * C::TILE; };
   const uint32_t abort_flag = bars + PW_ABORT;
-  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(gbase + C::OFF_BAR + PW_TMEM);
+  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_prompt + C::OFF_BAR + PW_TMEM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (warp == P_MMA_WARP) {
@@ -238,10 +243,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       mbar_init(bar(PB_Q_FULL, i), 1);
       mbar_init(bar(PB_Q_EMPTY, i), 1);
       mbar_init(bar(PB_S_FULL, i), 1);
-      mbar_init(bar(PB_P_READY, i), PT);
+      mbar_init(bar(PB_P_READY, i), P_SOFTMAX_WARPS / 2);
       mbar_init(bar(PB_PV_DONE, i), 1);
       mbar_init(bar(PB_U_FULL, i), 1);
-      mbar_init(bar(PB_U_EMPTY, i), P_SOFTMAX_WARPS + 1);
+      mbar_init(bar(PB_U_EMPTY, i), P_SOFTMAX_WARPS + 2);
+      mbar_init(bar(PB_TAIL, i), 1);
+      mbar_init(bar(PB_S_READ, i), P_SOFTMAX_WARPS / 2);
     }
     mbar_init(bar(PB_DRAIN, 0), 1);
     st_shared_u32(abort_flag, 0u);
@@ -326,132 +333,166 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           if (!bad) load_kv(&map_v, j);
         }
       }
+    } else if (warp == P_TAIL_WARP) {
+      // ------------------------------------------------------------ tails
+      // V rows [keys, 16 ceil(keys / 16)) of a unit's last block: zeros,
+      // whatever lies behind the sequence.  The product thread hands the
+      // block over once it has landed and gets it back before its P V.
+      uint32_t kv0 = 0, done = 0;
+      for (int i = 0;; ++i) {
+        if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
+        const PromptUnit u = read_unit(i);
+        if (u.q0 < 0) break;
+        const int nb = max(u.blocks(0, a.causal), u.blocks(1, a.causal));
+        const int keys = min(PT, u.n - (nb - 1) * PT), pad = -keys & 15;
+        kv0 += 2 * static_cast<uint32_t>(nb);
+        if (pad > 0) {
+          if (!wait(bar(PB_TAIL, 0), done & 1)) break;
+          ++done;
+          const uint32_t sv = s_kv(static_cast<int>((kv0 - 1) % C::SLOTS)) + keys * 128;
+          for (int z = lane; z < pad * 8 * (D / 64); z += 32) {
+            const int g = z / (pad * 8), r = z % (pad * 8);
+            st_shared_v4(sv + g * P_SUB + r * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (pad > 0) mbar_arrive(bar(PB_TAIL, 1));
+          mbar_arrive(bar(PB_U_EMPTY, i & 1));
+        }
+      }
     } else if (warp == P_MMA_WARP) {
       // ------------------------------------------------------------ products
-      const uint32_t idesc_s = idesc_f16(BF ? 1u : 0u, 0, PT, PT);
-      const uint32_t idesc_pv = idesc_f16(BF ? 1u : 0u, 1, PT, D);
-      uint32_t kv0 = 0;                       // ring index of the unit's K block 0; K j at kv0 + 2j, V j one after
-      uint32_t nq_a = 0, nq_b = 0, npv_a = 0, npv_b = 0;   // Q tiles and P V products of each tile so far
-      auto kv_slot = [&](uint32_t idx) { return static_cast<int>(idx % C::SLOTS); };
-      auto kv_wait = [&](uint32_t idx) { return wait(bar(PB_KV_FULL, kv_slot(idx)), (idx / C::SLOTS) & 1); };
-      // S of tile w with the K block at ring index idx; the P V product before it on this tile has completed.
-      auto issue_s = [&](int w, uint32_t idx, bool last) {
-        tc_fence_after();
-        const uint32_t sk = s_kv(kv_slot(idx));
-        const bool leader = elect_one();
+      // One thread does all of it: issuing from a branch inside each step cost
+      // 95 to 150 cycles a product (against 64 of the tensor core).
+      if (elect_one()) {
+        auto wait1 = [&](uint32_t b, uint32_t parity) {
+          if (!mbar_wait_or_abort(b, parity, abort_flag)) bad = true;
+          return !bad;
+        };
+        const uint32_t idesc_s = idesc_f16(BF ? 1u : 0u, 0, PT, PT);
+        const uint32_t idesc_pv = idesc_f16(BF ? 1u : 0u, 1, PT, D);
+        const uint64_t dq0 = sdesc(s_q(0), 16, 1024), dk0 = sdesc(s_kv(0), 16, 1024), dv0 = sdesc(s_kv(0), P_SUB, 1024);
+        uint32_t kv0 = 0;                       // ring index of the unit's K block 0; K j at kv0 + 2j, V j one after
+        // Q tiles, S products, P V products of each tile and tails so far.
+        uint32_t nq_a = 0, nq_b = 0, ns_a = 0, ns_b = 0, npv_a = 0, npv_b = 0, ntail = 0;
+        auto kv_slot = [&](uint32_t idx) { return static_cast<int>(idx % C::SLOTS); };
+        auto kv_wait = [&](uint32_t idx) { return wait1(bar(PB_KV_FULL, kv_slot(idx)), (idx / C::SLOTS) & 1); };
+        // S of tile w with the K block at ring index idx.
+        auto issue_s = [&](int w, uint32_t idx, bool last) {
+          tc_fence_after();
+          const uint64_t dq = dq0 + static_cast<uint32_t>(w) * (C::TILE >> 4);
+          const uint64_t dk = dk0 + static_cast<uint32_t>(kv_slot(idx)) * (C::TILE >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * P_SUB + (kk % 4) * 32;
-          const uint64_t da = sdesc(s_q(w) + off, 16, 1024), db = sdesc(sk + off, 16, 1024);
-          if (leader) umma_f16(tmem + C::T_S + w * PT, da, db, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        if (leader) {
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * P_SUB + (kk % 4) * 32) >> 4;
+            umma_f16(tmem + C::T_S + w * PT, dq + off, dk + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
           umma_commit(bar(PB_S_FULL, w));
           if (last) umma_commit(bar(PB_Q_EMPTY, w));
-        }
-        __syncwarp();
-      };
-      auto release = [&](uint32_t idx) {
-        if (elect_one()) umma_commit(bar(PB_KV_EMPTY, kv_slot(idx)));
-        __syncwarp();
-      };
-      // First S of tile w of a unit: its Q tile landed, the tile's last P V product done.
-      auto first_s = [&](int w, uint32_t idx, bool last) {
-        if (!wait(bar(PB_Q_FULL, w), (w ? nq_b : nq_a) & 1)) return;
-        ++(w ? nq_b : nq_a);
-        const uint32_t npv = w ? npv_b : npv_a;
-        if (npv > 0 && !wait(bar(PB_PV_DONE, w), (npv - 1) & 1)) return;
-        issue_s(w, idx, last);
-      };
-      PromptUnit u{0, 0, -1, 0};
-      bool a_started = false;                 // tile A's first S was issued during the previous unit
-      if (wait(bar(PB_U_FULL, 0), 0)) u = read_unit(0);
-      for (int i = 0; !bad && u.q0 >= 0; ++i) {
-        const int nba = u.blocks(0, a.causal), nbb = u.blocks(1, a.causal), nb = max(nba, nbb);
-        PromptUnit next;
-        next.q0 = -2;                         // not read yet
-        if (!a_started) {
-          if (!kv_wait(kv0)) break;
-          first_s(0, kv0, nba == 1);
-          if (bad) break;
-        }
-        a_started = false;
-        if (nbb > 0) {
-          first_s(1, kv0, nbb == 1);
-          if (bad) break;
-        }
-        release(kv0);
-        for (int j = 0; j < nb && !bad; ++j) {
-          const uint32_t vi = kv0 + 2 * j + 1, ki = vi + 1;
-          if (!kv_wait(vi)) break;
-          const int valid = min(PT, u.n - j * PT);                // keys of the block
-          const int ksteps = (valid + 15) / 16;
-          const uint32_t sv = s_kv(kv_slot(vi));
-          if (valid < PT) {
-            // V rows [valid, 16 ksteps): zeros, whatever lies behind the sequence.
-            for (int z = lane; z < (16 * ksteps - valid) * 8 * (D / 64); z += 32) {
-              const int g = z / ((16 * ksteps - valid) * 8), r = z % ((16 * ksteps - valid) * 8);
-              st_shared_v4(sv + g * P_SUB + valid * 128 + r * 16, 0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async();
-            __syncwarp();
+        };
+        auto release = [&](uint32_t idx) { umma_commit(bar(PB_KV_EMPTY, kv_slot(idx))); };
+        // The S columns of tile w are free: P V done with the P over them, or (own P) the scores read.
+        auto s_free = [&](int w) {
+          const uint32_t n = C::OWN_P ? (w ? ns_b : ns_a) : (w ? npv_b : npv_a);
+          return n == 0 || wait1(bar(C::OWN_P ? PB_S_READ : PB_PV_DONE, w), (n - 1) & 1);
+        };
+        // S of tile w of block j of a unit (block 0: its Q tile has landed).
+        auto next_s = [&](int w, int j, uint32_t idx, bool last) {
+          if (j == 0) {
+            if (!wait1(bar(PB_Q_FULL, w), (w ? nq_b : nq_a) & 1)) return false;
+            ++(w ? nq_b : nq_a);
           }
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w) {
-            const int nbw = w == 0 ? nba : nbb;
-            if (j < nbw) {
-              uint32_t& npv = w ? npv_b : npv_a;
-              if (!wait(bar(PB_P_READY, w), npv & 1)) break;
-              tc_fence_after();
-              const bool leader = elect_one();
-#pragma unroll 1
-              for (int kk = 0; kk < ksteps; ++kk) {
-                const uint64_t db = sdesc(sv + kk * 2048, P_SUB, 1024);
-                if (leader)
-                  umma_f16_tmem_a(tmem + C::T_O + w * D, tmem + C::T_S + w * PT + kk * 8, db, idesc_pv,
-                                  (j > 0 || kk > 0) ? 1u : 0u);
-              }
-              if (leader) umma_commit(bar(PB_PV_DONE, w));
-              __syncwarp();
-              ++npv;
-              if (j + 1 < nbw) {
-                if (!kv_wait(ki)) break;
-                if (!wait(bar(PB_PV_DONE, w), (npv - 1) & 1)) break;
-                issue_s(w, ki, j + 2 == nbw);
+          if (!kv_wait(idx) || !s_free(w)) return false;
+          ++(w ? ns_b : ns_a);
+          issue_s(w, idx, last);
+          return true;
+        };
+        // O (+)= P V of tile w for block j.
+        auto next_pv = [&](int w, int j, int ksteps, uint32_t vi) {
+          if (!wait1(bar(PB_P_READY, w), (w ? npv_b : npv_a) & 1)) return false;
+          ++(w ? npv_b : npv_a);
+          tc_fence_after();
+          const uint64_t dv = dv0 + static_cast<uint32_t>(kv_slot(vi)) * (C::TILE >> 4);
+          const uint32_t to = tmem + C::T_O + w * D, tp = tmem + C::T_P + w * C::P_STEP;
+#pragma unroll
+          for (int kk = 0; kk < PT / 16; ++kk) {
+            if (kk < ksteps) umma_f16_tmem_a(to, tp + kk * 8, dv + kk * (2048 >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(bar(PB_PV_DONE, w));
+          return true;
+        };
+        PromptUnit u{0, 0, -1, 0};
+        int started = 0;                        // tiles (bits) whose first S was issued during the previous unit
+        if (wait1(bar(PB_U_FULL, 0), 0)) u = read_unit(0);
+        for (int i = 0; !bad && u.q0 >= 0; ++i) {
+          const int nba = u.blocks(0, a.causal), nbb = u.blocks(1, a.causal), nb = max(nba, nbb);
+          PromptUnit next{0, 0, -2, 0};         // not read yet
+          if (!(started & 1) && !next_s(0, 0, kv0, nba == 1)) break;
+          if (nbb > 0 && !(started & 2) && !next_s(1, 0, kv0, nbb == 1)) break;
+          started = 0;
+          release(kv0);
+          for (int j = 0; j < nb && !bad; ++j) {
+            const uint32_t vi = kv0 + 2 * j + 1, ki = vi + 1;
+            if (!kv_wait(vi)) break;
+            const int keys = min(PT, u.n - j * PT), ksteps = (keys + 15) / 16;
+            if (keys & 15) {
+              mbar_arrive(bar(PB_TAIL, 0));
+              if (!wait1(bar(PB_TAIL, 1), ntail & 1)) break;
+              ++ntail;
+            }
+            // With the next block's S ahead of this block's P V (own P), or right behind it.
+            if constexpr (C::OWN_P) {
+              if (j + 1 < nba && !next_s(0, j + 1, ki, j + 2 == nba)) break;
+              if (j + 1 < nbb && !next_s(1, j + 1, ki, j + 2 == nbb)) break;
+              if (j + 1 < nb) release(ki);
+            } else {
+              if (j < nba) {
+                if (!next_pv(0, j, ksteps, vi)) break;
+                if (j + 1 < nba && !next_s(0, j + 1, ki, j + 2 == nba)) break;
               }
             }
-            if (w == 0 && nbb > 0 && j == nbb - 1) {
-              // Tile A has no more products in this unit: its first S of the
-              // next unit goes ahead of tile B's last P V.
-              if (!wait(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
+            if (j == nb - 1) {
+              // The next unit's first S goes ahead of this unit's last P V: tile A's when
+              // its products are all issued (P over S) or its scores read (own P).
+              if (!wait1(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
               next = read_unit(i + 1);
               if (next.q0 >= 0) {
-                if (!kv_wait(kv0 + 2 * nb)) break;
-                first_s(0, kv0 + 2 * nb, next.blocks(0, a.causal) == 1);
-                if (bad) break;
-                a_started = true;
+                const uint32_t k0 = kv0 + 2 * nb;
+                if (C::OWN_P || nbb > 0) {
+                  if (!next_s(0, 0, k0, next.blocks(0, a.causal) == 1)) break;
+                  started |= 1;
+                }
+                if (C::OWN_P && next.has_b()) {
+                  if (!next_s(1, 0, k0, next.blocks(1, a.causal) == 1)) break;
+                  started |= 2;
+                }
               }
             }
+            if constexpr (C::OWN_P) {
+              if (j < nba && !next_pv(0, j, ksteps, vi)) break;
+              if (j < nbb && !next_pv(1, j, ksteps, vi)) break;
+            } else {
+              if (j < nbb) {
+                if (!next_pv(1, j, ksteps, vi)) break;
+                if (j + 1 < nbb && !next_s(1, j + 1, ki, j + 2 == nbb)) break;
+              }
+              if (j + 1 < nb) release(ki);
+            }
+            release(vi);
           }
           if (bad) break;
-          release(vi);
-          if (j + 1 < nb) release(ki);
+          kv0 += 2 * static_cast<uint32_t>(nb);
+          mbar_arrive(bar(PB_U_EMPTY, i & 1));
+          u = next;
         }
-        if (bad) break;
-        kv0 += 2 * static_cast<uint32_t>(nb);
-        if (next.q0 == -2) {
-          if (!wait(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
-          next = read_unit(i + 1);
+        if (!bad) {
+          umma_commit(bar(PB_DRAIN, 0));
+          wait1(bar(PB_DRAIN, 0), 0);
         }
-        if (lane == 0) mbar_arrive(bar(PB_U_EMPTY, i & 1));
-        __syncwarp();
-        u = next;
       }
-      if (!bad) {
-        if (elect_one()) umma_commit(bar(PB_DRAIN, 0));
-        __syncwarp();
-        wait(bar(PB_DRAIN, 0), 0);
-      }
+      bad = __any_sync(0xffffffffu, bad);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -459,6 +500,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const int w = warp >> 2, row = tid & (PT - 1);
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::T_S + w * PT, tO = tmem + lane_off + C::T_O + w * D;
+    const uint32_t tP = tmem + lane_off + C::T_P + w * C::P_STEP;
     uint32_t count = 0;                     // blocks of this tile so far
     for (int i = 0;; ++i) {
       if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
@@ -468,18 +510,38 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       float m_ref = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nbw; ++j) {
         if (!wait(bar(PB_S_FULL, w), count & 1)) break;
-        ++count;
         tc_fence_after();
+        float s[PT], mx;
         if (j + 1 < nbw) {
-          prompt_softmax<BF, D, false>(tS, tO, PT, j == 0, a.scale_log2, m_ref, l_run);
+          mx = prompt_scores<false>(tS, PT, s);
         } else {
           // The last block: the sequence's end, and the diagonal when causal.
           int lim = u.n - j * PT;
           if (a.causal) lim = min(lim, u.q0 + w * PT + row - j * PT + 1);
-          prompt_softmax<BF, D, true>(tS, tO, lim, j == 0, a.scale_log2, m_ref, l_run);
+          mx = prompt_scores<true>(tS, lim, s);
         }
+        if constexpr (C::OWN_P) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PB_S_READ, w));
+          // P and O are free once the P V product before this one is done.
+          if (count > 0 && !wait(bar(PB_PV_DONE, w), (count - 1) & 1)) break;
+          tc_fence_after();
+        }
+        ++count;
+        const float x = mx * a.scale_log2;
+        const bool move = x > m_ref + P_MOVE;
+        if (__any_sync(0xffffffffu, move)) {
+          const float alpha = move ? fast_exp2(m_ref - x) : 1.f;
+          if (move) m_ref = x;
+          l_run *= alpha;
+          if (j > 0) prompt_rescale<D>(tO, alpha);
+        }
+        l_run += prompt_weights<BF>(tP, s, a.scale_log2, m_ref);
+        tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar(PB_P_READY, w));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PB_P_READY, w));
       }
       if (bad) break;
       if (nbw > 0) {
