@@ -1,64 +1,613 @@
-// Linear layer with bias, activation and residual: 32 x 32 output tiles,
-// operands staged in shared memory as fp32, one output element per thread.
+// Linear layer with its whole epilogue: c = act(a W^T + bias) + residual over
+// the T = cu_seqlens[B] packed rows (T read on the device), a [cap, K] and
+// W [N, K] both K-major.
+//
+// Two kernels.
+//
+// linear_pair_kernel: tcgen05 on pairs of SMs (cta_group::2).  A pair owns a
+// tile of 256 rows x LN columns (LN = 256, 128 or 64): each CTA holds 128 of the rows
+// and half of the W rows, and the pair's one product per 16-wide K step reads
+// both halves, so an SM's shared memory serves 8 KB of operands per 256 x 256 x 16
+// product instead of the 12 KB of a 128 x 256 x 16 one on a single SM, half as
+// much per multiply-add: on one SM shared memory bandwidth holds the products
+// at two thirds of the tensor rate.  Persistent, per CTA: warp 0 streams K
+// chunks of 64 (16 + 16 KB) through a six-stage TMA ring, both CTAs' copies counted
+// on the leader's barrier; one thread of the leader's warp 1 issues the products into one of
+// two 256-column TMEM accumulators, so the next tile's products run while warps 2-9 of both
+// CTAs drain the last one: bias, activation and residual in fp32, one
+// rounding, through 4 KB of shared memory per warp to whole 128-byte row
+// pieces.  LN is chosen on the device, where T is known: the width whose
+// rounds over the pairs take the least time.
+//
+// linear_few_kernel: a handful of rows (one token of each sequence).  The work
+// is one read of W, so W goes from global memory straight into mma.sync operand
+// registers, 16 bytes a lane, eight warps splitting K of 16 W rows, the sums joined
+// in shared memory.  The K order inside a 32-wide step is the one in which the 16-byte
+// loads arrive, the same for both operands (a dot product does not mind).
+//
+// Every wait is bounded; a CTA that gives up tells its peer, records
+// RRA_DEVERR_WAIT_TIMEOUT, lets copies and products in flight land, frees its
+// TMEM and returns.
+#include <mutex>
+
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace rra {
 namespace {
 
-__device__ __forceinline__ float activate(float x, int act) {
-  switch (act) {
-    case RRA_ACT_RELU: return x < 0.f ? 0.f : x;
-    case RRA_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-    case RRA_ACT_GELU_TANH: return 0.5f * x * (1.f + tanhf(0.79788456080286536f * (x + 0.044715f * x * x * x)));
-    case RRA_ACT_SILU: return x / (1.f + expf(-x));
-    default: return x;
+constexpr int LM = 128;                                  // rows of a CTA's half tile
+constexpr int LN_MAX = 256;                              // columns of a tile
+constexpr int LK = 64;                                   // K per stage (one 128-byte swizzled row)
+constexpr int L_STAGES = 6;
+constexpr int L_EPI_WARPS = 8;                           // warps 2-9
+constexpr int L_THREADS = 64 + 32 * L_EPI_WARPS;
+constexpr uint32_t L_A_BYTES = LM * 128;
+constexpr uint32_t L_W_BYTES = LN_MAX / 2 * 128;
+constexpr uint32_t L_STAGE_BYTES = L_A_BYTES + L_W_BYTES;
+constexpr uint32_t L_OUT_BYTES = 32 * 128;               // output staging of one epilogue warp
+constexpr uint32_t L_OFF_OUT = L_STAGES * L_STAGE_BYTES;
+constexpr uint32_t L_OFF_BAR = L_OFF_OUT + L_EPI_WARPS * L_OUT_BYTES;
+constexpr uint32_t LB_FULL = 0;                          // [L_STAGES] (the leader's: both CTAs' copies)
+constexpr uint32_t LB_EMPTY = 64;                        // [L_STAGES] (each CTA's own)
+constexpr uint32_t LB_ACC_FULL = 128;                    // [2] (each CTA's own)
+constexpr uint32_t LB_ACC_EMPTY = 144;                   // [2] (the leader's: one arrival per epilogue warp of both)
+constexpr uint32_t LW_TMEM = 160, LW_ABORT = 164;
+constexpr uint32_t L_SMEM = L_OFF_BAR + 256;
+constexpr uint32_t L_TMEM_COLS = 512;
+
+// --------------------------------------------------------- pair-of-CTAs PTX
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// The address of this shared-memory location in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once every product issued so far has completed.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// ------------------------------------------------------------------ epilogue
+
+__device__ __forceinline__ float act_gelu(float x) { return 0.5f * x * (1.f + erff(x * 0.70710678118654752f)); }
+__device__ __forceinline__ float act_gelu_tanh(float x) {
+  return 0.5f * x * (1.f + tanhf(0.79788456080286536f * fmaf(0.044715f * x * x, x, x)));
+}
+__device__ __forceinline__ float act_silu(float x) { return x / (1.f + __expf(-x)); }
+
+template <int E>
+__device__ __forceinline__ void activate(float (&v)[E], int act) {
+  if (act == RRA_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+  } else if (act == RRA_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = act_gelu(v[i]);
+  } else if (act == RRA_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = act_gelu_tanh(v[i]);
+  } else if (act == RRA_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = act_silu(v[i]);
   }
+}
+
+// A 16-byte chunk of outputs as floats, and back (one rounding).
+template <typename T> struct Chunk;
+template <> struct Chunk<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void add(float* v, uint4 x) {
+    v[0] += __uint_as_float(x.x);
+    v[1] += __uint_as_float(x.y);
+    v[2] += __uint_as_float(x.z);
+    v[3] += __uint_as_float(x.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <> struct Chunk<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void add(float* v, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] += __uint_as_float(w[i] << 16);
+      v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Chunk<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void add(float* v, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] += f.x;
+      v[2 * i + 1] += f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 t = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Columns of a tile: the width whose rounds over `pairs` pairs cost least, a
+// tile of LN columns counted as LN + 64 (its A half is loaded whatever its width).
+__device__ __forceinline__ int tile_columns(int T, int N, int pairs) {
+  const long long mt = (T + 2 * LM - 1) / (2 * LM);
+  int best = LN_MAX;
+  long long cost = -1;
+#pragma unroll
+  for (int ln = LN_MAX; ln >= 64; ln /= 2) {
+    const long long tiles = mt * ((N + ln - 1) / ln), c = (tiles + pairs - 1) / pairs * (ln + 64);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = ln;
+    }
+  }
+  return best;
 }
 
 template <typename Tin, typename Tout>
-__global__ void linear_epilogue_kernel(const LinearEpiArgs a, int act) {
-  __shared__ float sa[32][33], sw[32][33];
-  const int T = a.cu[a.B];
-  const int t0 = blockIdx.y * 32, n0 = blockIdx.x * 32, x = threadIdx.x, y = threadIdx.y;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w128,
+                       const __grid_constant__ CUtensorMap map_w64, const __grid_constant__ CUtensorMap map_w32,
+                       const LinearEpiArgs a, int act) {
+  extern __shared__ __align__(1024) uint8_t smem_linear[];
+  const uint32_t base = smem_u32(smem_linear);
+  auto s_a = [&](int s) { return base + static_cast<uint32_t>(s) * L_STAGE_BYTES; };
+  auto s_w = [&](int s) { return base + static_cast<uint32_t>(s) * L_STAGE_BYTES + L_A_BYTES; };
+  const uint32_t bars = base + L_OFF_BAR;
+  auto bar = [&](uint32_t kind, int i) { return bars + kind + 8 * static_cast<uint32_t>(i); };
+  const uint32_t abort_flag = bars + LW_ABORT;
+  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_linear + L_OFF_BAR + LW_TMEM);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bars + LW_TMEM),
+                 "r"(L_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int s = 0; s < L_STAGES; ++s) {
+      mbar_init(bar(LB_FULL, s), 1);
+      mbar_init(bar(LB_EMPTY, s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(LB_ACC_FULL, b), 1);
+      mbar_init(bar(LB_ACC_EMPTY, b), 2 * L_EPI_WARPS);
+    }
+    st_shared_u32(abort_flag, 0u);
+    fence_barrier_init();
+    prefetch_tensormap(&map_a);
+    prefetch_tensormap(&map_w128);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();                                    // both CTAs' barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int T = __ldg(a.cu + a.B);
+  bool bad = false;
   if (T < 0 || T > a.cap) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && x == 0 && y == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
+    if (blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
+  } else {
+    const int pairs = static_cast<int>(gridDim.x) / 2, pair = static_cast<int>(blockIdx.x) / 2;
+    const int ln = tile_columns(T, a.N, pairs);
+    const int nt = (a.N + ln - 1) / ln;
+    const long long tiles = static_cast<long long>((T + 2 * LM - 1) / (2 * LM)) * nt;   // row tiles outermost
+    const int kchunks = (a.K + LK - 1) / LK;
+    if (warp == 0) {
+      // ------------------------------------------------------------ loads
+      const CUtensorMap* mw = ln == 256 ? &map_w128 : (ln == 128 ? &map_w64 : &map_w32);
+      const uint32_t bytes = 2 * (L_A_BYTES + static_cast<uint32_t>(ln / 2) * 128u);
+      uint32_t it = 0;
+      if (elect_one()) {
+        for (long long t = pair; t < tiles && !bad; t += pairs) {
+          const int m0 = static_cast<int>(t / nt) * 2 * LM + static_cast<int>(rank) * LM;
+          const int n0 = static_cast<int>(t % nt) * ln + static_cast<int>(rank) * (ln / 2);
+          for (int kc = 0; kc < kchunks; ++kc, ++it) {
+            const int s = static_cast<int>(it % L_STAGES);
+            if (it >= L_STAGES && !mbar_wait_or_abort(bar(LB_EMPTY, s), (it / L_STAGES - 1) & 1, abort_flag)) {
+              bad = true;
+              break;
+            }
+            if (rank == 0) mbar_expect_tx(bar(LB_FULL, s), bytes);
+            const uint32_t full = map_rank(bar(LB_FULL, s), 0);
+            tma_load_2d_pair(s_a(s), &map_a, kc * LK, m0, full);    // rows past cap, columns past K: zeros
+            tma_load_2d_pair(s_w(s), mw, kc * LK, n0, full);
+          }
+        }
+      }
+      bad = __any_sync(0xffffffffu, bad);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ products
+      if (rank == 0 && elect_one()) {
+        const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, ln);
+        const uint64_t da0 = sdesc(s_a(0), 16, 1024), dw0 = sdesc(s_w(0), 16, 1024);
+        uint32_t it = 0, i = 0;
+        for (long long t = pair; t < tiles && !bad; t += pairs, ++i) {
+          const int b = i & 1;
+          if (i >= 2 && !mbar_wait_or_abort(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag)) {
+            bad = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t acc = tmem + static_cast<uint32_t>(b) * LN_MAX;
+          for (int kc = 0; kc < kchunks; ++kc, ++it) {
+            const uint32_t s = it % L_STAGES;
+            if (!mbar_wait_or_abort(bar(LB_FULL, static_cast<int>(s)), (it / L_STAGES) & 1, abort_flag)) {
+              bad = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t off = s * (L_STAGE_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < LK / 16; ++kk)
+              umma_f16_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+            umma_commit_pair(bar(LB_EMPTY, static_cast<int>(s)));
+          }
+          if (!bad) umma_commit_pair(bar(LB_ACC_FULL, b));
+        }
+      }
+      bad = __any_sync(0xffffffffu, bad);
+    } else {
+      // ------------------------------------------------------------ epilogue
+      using Ch = Chunk<Tout>;
+      constexpr int CPP = 8 * Ch::N;                     // columns of a 128-byte piece
+      const int quad = warp & 3, half = (warp - 2) >> 2; // TMEM lane quadrant; which pieces
+      const uint32_t stg = base + L_OFF_OUT + static_cast<uint32_t>(warp - 2) * L_OUT_BYTES;
+      const uint32_t acc_empty[2] = {map_rank(bar(LB_ACC_EMPTY, 0), 0), map_rank(bar(LB_ACC_EMPTY, 1), 0)};
+      uint32_t i = 0;
+      for (long long t = pair; t < tiles; t += pairs, ++i) {
+        const int b = i & 1;
+        if (!mbar_wait_or_abort(bar(LB_ACC_FULL, b), (i >> 1) & 1, abort_flag)) bad = true;
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad) break;
+        tc_fence_after();
+        const int m0 = static_cast<int>(t / nt) * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
+        const int n0 = static_cast<int>(t % nt) * ln;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(b) * LN_MAX;
+        const int cc = lane & 7;                         // this lane's 16-byte chunk of a row piece
+#pragma unroll 1
+        for (int p = half; p * CPP < ln; p += 2) {
+          const int col0 = n0 + p * CPP;
+          if (col0 >= a.N || m0 >= T) break;
+          const bool col_ok = col0 + cc * Ch::N < a.N;   // N is a multiple of 8: chunks are whole
+          auto at = [&](int r) { return static_cast<size_t>(m0 + r) * a.N + col0 + cc * Ch::N; };
+          uint4 res[8];
+          if (a.residual != nullptr) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int rr = 4 * r + (lane >> 3);
+              res[r] = make_uint4(0u, 0u, 0u, 0u);
+              if (col_ok && m0 + rr < T)
+                res[r] = *reinterpret_cast<const uint4*>(static_cast<const Tout*>(a.residual) + at(rr));
+            }
+          }
+          float v[CPP];
+#pragma unroll
+          for (int q = 0; q < CPP / 32; ++q) tmem_ld32(taddr + p * CPP + q * 32, v + q * 32);
+          if (a.bias != nullptr) {
+            const float4* b4 = reinterpret_cast<const float4*>(a.bias + col0);
+#pragma unroll
+            for (int j = 0; j < CPP / 4; ++j) {
+              if (col0 + 4 * j < a.N) {
+                const float4 bb = __ldg(b4 + j);
+                v[4 * j] += bb.x;
+                v[4 * j + 1] += bb.y;
+                v[4 * j + 2] += bb.z;
+                v[4 * j + 3] += bb.w;
+              }
+            }
+          }
+          activate(v, act);
+          if (a.residual != nullptr) {
+            // The residual turns from row pieces into rows through the staging rows.
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int rr = 4 * r + (lane >> 3);
+              st_shared_v4(stg + rr * 128 + ((cc ^ (rr & 7)) << 4), res[r].x, res[r].y, res[r].z, res[r].w);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) Ch::add(v + j * Ch::N, ld_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4)));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 w = Ch::pack(v + j * Ch::N);
+            st_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4), w.x, w.y, w.z, w.w);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int rr = 4 * r + (lane >> 3);
+            const uint4 w = ld_shared_v4(stg + rr * 128 + ((cc ^ (rr & 7)) << 4));
+            if (col_ok && m0 + rr < T) *reinterpret_cast<uint4*>(static_cast<Tout*>(a.c) + at(rr)) = w;
+          }
+          __syncwarp();                                  // read back before the next piece is written
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty[b]);
+      }
+    }
+    if (bad && lane == 0) {
+      st_shared_u32(abort_flag, 1u);
+      st_cluster_u32(map_rank(abort_flag, rank ^ 1u), 1u);
+      record_error(a.err, RRA_DEVERR_WAIT_TIMEOUT);
+    }
+  }
+
+  // Teardown: after an abort, copies and products still in flight get a
+  // bounded grace period (~1 ms) to land before the TMEM is released.
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && ld_shared_volatile_u32(abort_flag) != 0u) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000LL) {
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();                                    // the peer's copies, arrivals and products are done too
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L_TMEM_COLS) : "memory");
+}
+
+// ------------------------------------------------------------------ few rows
+
+constexpr int FEW_WARPS = 8;
+constexpr int FEW_UNROLL = 4;     // 32-wide K steps in flight per warp
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// NT: groups of 8 rows of a.  One CTA: 16 columns of c.
+template <typename Tin, typename Tout, int NT>
+__global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const LinearEpiArgs a, int act) {
+  __shared__ float part[FEW_WARPS][16][NT * 8 + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int n0 = static_cast<int>(blockIdx.x) * 16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int T = __ldg(a.cu + a.B);
+  if (T < 0 || T > a.cap) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
     return;
   }
-  if (t0 >= T) return;
-  const Tin* pa = static_cast<const Tin*>(a.a);
-  const Tin* pw = static_cast<const Tin*>(a.w);
-  float acc = 0.f;
-  for (int k0 = 0; k0 < a.K; k0 += 32) {
-    const int k = k0 + x;
-    sa[y][x] = (t0 + y < T && k < a.K) ? static_cast<float>(pa[static_cast<size_t>(t0 + y) * a.K + k]) : 0.f;
-    sw[y][x] = (n0 + y < a.N && k < a.K) ? static_cast<float>(pw[static_cast<size_t>(n0 + y) * a.K + k]) : 0.f;
-    __syncthreads();
-    for (int j = 0; j < 32; ++j) acc = fmaf(sa[y][j], sw[x][j], acc);
-    __syncthreads();
+  if (T == 0) return;
+  const Tin* W = static_cast<const Tin*>(a.w);
+  const Tin* X = static_cast<const Tin*>(a.a);
+  // Rows past N or T repeat the last one: their results are not stored.
+  const Tin* w0 = W + static_cast<size_t>(min(n0 + g, a.N - 1)) * a.K;
+  const Tin* w1 = W + static_cast<size_t>(min(n0 + g + 8, a.N - 1)) * a.K;
+  const Tin* x[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) x[t] = X + static_cast<size_t>(min(8 * t + g, T - 1)) * a.K;
+  float d[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+  const int steps = (a.K + 31) / 32;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int s0 = warp * FEW_UNROLL; s0 < steps; s0 += FEW_WARPS * FEW_UNROLL) {
+    uint4 wa[FEW_UNROLL], wb[FEW_UNROLL], xv[FEW_UNROLL][NT];
+#pragma unroll
+    for (int i = 0; i < FEW_UNROLL; ++i) {
+      const int k = (s0 + i) * 32 + q * 8;               // K is a multiple of 8: chunks are whole
+      const bool ok = k < a.K;
+      wa[i] = ok ? ld_stream16(w0 + k) : zero;
+      wb[i] = ok ? ld_stream16(w1 + k) : zero;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) xv[i][t] = ok ? *reinterpret_cast<const uint4*>(x[t] + k) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < FEW_UNROLL; ++i) {
+      const uint32_t lo[4] = {wa[i].x, wb[i].x, wa[i].y, wb[i].y}, hi[4] = {wa[i].z, wb[i].z, wa[i].w, wb[i].w};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_16816(d[t], lo, xv[i][t].x, xv[i][t].y, Tin());
+        mma_16816(d[t], hi, xv[i][t].z, xv[i][t].w, Tin());
+      }
+    }
   }
-  const int t = t0 + y, n = n0 + x;
-  if (t >= T || n >= a.N) return;
-  if (a.bias != nullptr) acc += a.bias[n];
-  acc = activate(acc, act);
-  const size_t at = static_cast<size_t>(t) * a.N + n;
-  if (a.residual != nullptr) acc += static_cast<float>(static_cast<const Tout*>(a.residual)[at]);
-  static_cast<Tout*>(a.c)[at] = Tout(acc);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    part[warp][g][8 * t + 2 * q] = d[t][0];
+    part[warp][g][8 * t + 2 * q + 1] = d[t][1];
+    part[warp][g + 8][8 * t + 2 * q] = d[t][2];
+    part[warp][g + 8][8 * t + 2 * q + 1] = d[t][3];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 16 * NT * 8; e += 32 * FEW_WARPS) {
+    const int j = e & 15, t = e >> 4, n = n0 + j;
+    if (t >= T || n >= a.N) continue;
+    float v[1] = {0.f};
+#pragma unroll
+    for (int w = 0; w < FEW_WARPS; ++w) v[0] += part[w][j][t];
+    if (a.bias != nullptr) v[0] += __ldg(a.bias + n);
+    activate(v, act);
+    const size_t at = static_cast<size_t>(t) * a.N + n;
+    if (a.residual != nullptr) v[0] += static_cast<float>(static_cast<const Tout*>(a.residual)[at]);
+    static_cast<Tout*>(a.c)[at] = static_cast<Tout>(v[0]);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 linear_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// 2-D map over a row-major [rows, K] matrix: box = 64 columns x box_rows rows,
+// 128-byte swizzle (the canonical K-major operand layout).
+cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, long long rows, int K, bool bf16, uint32_t box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
+  cuuint32_t box[2] = {LK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = linear_encode_fn()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                                  const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Launched as a programmatic dependent: the set-up overlaps the tail of the
+// kernel before it in the stream, whose completion the kernels wait for
+// before touching global memory.
+cudaLaunchConfig_t dependent_config(cudaLaunchAttribute* attr, int grid, int threads, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <typename Tin, typename Tout>
+cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
+  if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
+  auto kernel = linear_pair_kernel<Tin, Tout>;
+  constexpr int kMaxDevices = 64;
+  static bool attr_set[kMaxDevices] = {};
+  static std::mutex m;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(m);
+    if (!attr_set[dev]) {
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L_SMEM)) != cudaSuccess)
+        return e;
+      attr_set[dev] = true;
+    }
+  }
+  const bool bf16 = IsBf16<Tin>::value == 1;
+  CUtensorMap ma, mw[3];
+  if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, LM)) != cudaSuccess) return e;
+  for (int i = 0; i < 3; ++i)
+    if ((e = make_map_2d(&mw[i], a.w, a.N, a.K, bf16, 128u >> i)) != cudaSuccess) return e;
+  const long long most = ((a.cap + 2LL * LM - 1) / (2 * LM)) * ((a.N + 63LL) / 64);   // tiles if every row is in use
+  const int pairs = static_cast<int>(most < num_sms / 2 ? most : num_sms / 2);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = dependent_config(&attr, 2 * (pairs > 0 ? pairs : 1), L_THREADS, L_SMEM, stream);
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mw[0], mw[1], mw[2], a, act);
+}
+
+template <typename Tin, typename Tout, int NT>
+cudaError_t launch_few(const LinearEpiArgs& a, int act, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = dependent_config(&attr, (a.N + 15) / 16, 32 * FEW_WARPS, 0, stream);
+  return cudaLaunchKernelEx(&cfg, linear_few_kernel<Tin, Tout, NT>, a, act);
+}
+
+template <typename Tin, typename Tout>
+cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
+  if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
+  if (a.cap <= 16) return launch_few<Tin, Tout, 2>(a, act, stream);
+  if (a.cap <= 32) return launch_few<Tin, Tout, 4>(a, act, stream);
+  return launch_pair<Tin, Tout>(a, act, num_sms, stream);
 }
 
 template <typename Tin>
-cudaError_t launch_in(const LinearEpiArgs& a, rra_dtype out, int act, cudaStream_t stream) {
-  const dim3 grid((a.N + 31) / 32, (a.cap + 31) / 32), block(32, 32);
-  if (out == RRA_BF16) linear_epilogue_kernel<Tin, __nv_bfloat16><<<grid, block, 0, stream>>>(a, act);
-  else if (out == RRA_F16) linear_epilogue_kernel<Tin, __half><<<grid, block, 0, stream>>>(a, act);
-  else linear_epilogue_kernel<Tin, float><<<grid, block, 0, stream>>>(a, act);
-  return cudaGetLastError();
+cudaError_t launch_in(const LinearEpiArgs& a, rra_dtype out, int act, int num_sms, cudaStream_t stream) {
+  if (out == RRA_BF16) return launch_typed<Tin, __nv_bfloat16>(a, act, num_sms, stream);
+  if (out == RRA_F16) return launch_typed<Tin, __half>(a, act, num_sms, stream);
+  return launch_typed<Tin, float>(a, act, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_epilogue(const LinearEpiArgs& a, rra_dtype in, rra_dtype out, rra_activation act,
                                    int num_sms, cudaStream_t stream) {
-  return in == RRA_BF16 ? launch_in<__nv_bfloat16>(a, out, act, stream) : launch_in<__half>(a, out, act, stream);
+  return in == RRA_BF16 ? launch_in<__nv_bfloat16>(a, out, act, num_sms, stream)
+                        : launch_in<__half>(a, out, act, num_sms, stream);
 }
 
 }  // namespace rra
