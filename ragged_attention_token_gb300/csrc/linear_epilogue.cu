@@ -103,11 +103,32 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
 
 // ------------------------------------------------------------------ epilogue
 
-__device__ __forceinline__ float act_gelu(float x) { return 0.5f * x * (1.f + erff(x * 0.70710678118654752f)); }
-__device__ __forceinline__ float act_gelu_tanh(float x) {
-  return 0.5f * x * (1.f + tanhf(0.79788456080286536f * fmaf(0.044715f * x * x, x, x)));
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ float act_silu(float x) { return x / (1.f + __expf(-x)); }
+// 1 / (1 + e^-x): within a few 2^-23 of its value; 0 where e^-x overflows.
+__device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.f + __expf(-x)); }
+// x/2 (1 + erf(x / sqrt 2)) by Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26: erfc(z) = (a1 t + ... + a5 t^5) e^{-z^2}, t = 1 / (1 + p z), z >= 0,
+// within 1.5e-7.  For x < 0 the result is x erfc(|z|) / 2, with no cancellation.
+// (With erff the epilogue of a K = 384 layer took 2.5 times as long as its products.)
+__device__ __forceinline__ float act_gelu(float x) {
+  const float z = fabsf(x) * 0.70710678118654752f;
+  const float t = fast_rcp(fmaf(0.3275911f, z, 1.f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f) * t;
+  const float h = 0.5f * q * __expf(-z * z);   // erfc(|z|) / 2
+  return x * (x < 0.f ? h : 1.f - h);
+}
+// (1 + tanh u) / 2 = 1 / (1 + e^{-2u}).
+__device__ __forceinline__ float act_gelu_tanh(float x) {
+  return x * fast_sigmoid(1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
+}
+__device__ __forceinline__ float act_silu(float x) { return x * fast_sigmoid(x); }
 
 template <int E>
 __device__ __forceinline__ void activate(float (&v)[E], int act) {
@@ -331,13 +352,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           auto at = [&](int r) { return static_cast<size_t>(m0 + r) * a.N + col0 + cc * Ch::N; };
           uint4 res[8];
           if (a.residual != nullptr) {
+            // Past T or N: some element that is in use, for outputs that are not stored.
+            const Tout* from = static_cast<const Tout*>(a.residual) + (col_ok ? col0 + cc * Ch::N : 0);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int rr = 4 * r + (lane >> 3);
-              res[r] = make_uint4(0u, 0u, 0u, 0u);
-              if (col_ok && m0 + rr < T)
-                res[r] = *reinterpret_cast<const uint4*>(static_cast<const Tout*>(a.residual) + at(rr));
-            }
+            for (int r = 0; r < 8; ++r)
+              res[r] = *reinterpret_cast<const uint4*>(from + static_cast<size_t>(min(m0 + 4 * r + (lane >> 3), T - 1)) * a.N);
           }
           float v[CPP];
 #pragma unroll
@@ -346,13 +365,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
             const float4* b4 = reinterpret_cast<const float4*>(a.bias + col0);
 #pragma unroll
             for (int j = 0; j < CPP / 4; ++j) {
-              if (col0 + 4 * j < a.N) {
-                const float4 bb = __ldg(b4 + j);
-                v[4 * j] += bb.x;
-                v[4 * j + 1] += bb.y;
-                v[4 * j + 2] += bb.z;
-                v[4 * j + 3] += bb.w;
-              }
+              // Past N: the last columns' bias, for outputs that are not stored (a guard would put the loads in a row).
+              const float4 bb = __ldg(b4 + min(j, (a.N - col0) / 4 - 1));
+              v[4 * j] += bb.x;
+              v[4 * j + 1] += bb.y;
+              v[4 * j + 2] += bb.z;
+              v[4 * j + 3] += bb.w;
             }
           }
           activate(v, act);
@@ -412,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
 // ------------------------------------------------------------------ few rows
 
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_UNROLL = 4;     // 32-wide K steps in flight per warp
+constexpr int FEW_UNROLL = 8;     // 32-wide K steps in flight per warp (few rows: 16 KB a warp)
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
   asm volatile(
@@ -426,11 +444,19 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Both loads are volatile so that they stay ahead of the products: left to
+// the compiler they sank to their uses and a warp had one step in flight.
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
@@ -458,26 +484,31 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   float d[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+  // Steps of 32 in K, U at a time and a warp's share in turn; U shrinks as
+  // the rows of a take more registers.
+  constexpr int U = NT == 1 ? FEW_UNROLL : (NT == 2 ? FEW_UNROLL / 2 : FEW_UNROLL / 4);
   const int steps = (a.K + 31) / 32;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int s0 = warp * FEW_UNROLL; s0 < steps; s0 += FEW_WARPS * FEW_UNROLL) {
-    uint4 wa[FEW_UNROLL], wb[FEW_UNROLL], xv[FEW_UNROLL][NT];
+  for (int s0 = warp * U; s0 < steps; s0 += FEW_WARPS * U) {
+    uint4 wa[U], wb[U], xv[U][NT];
 #pragma unroll
-    for (int i = 0; i < FEW_UNROLL; ++i) {
-      const int k = (s0 + i) * 32 + q * 8;               // K is a multiple of 8: chunks are whole
-      const bool ok = k < a.K;
-      wa[i] = ok ? ld_stream16(w0 + k) : zero;
-      wb[i] = ok ? ld_stream16(w1 + k) : zero;
+    for (int i = 0; i < U; ++i) {
+      // K is a multiple of 8: chunks are whole; past K the last one is loaded and counts as zero.
+      const int k = min((s0 + i) * 32 + q * 8, a.K - 8);
+      wa[i] = ld_stream16(w0 + k);
+      wb[i] = ld_stream16(w1 + k);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) xv[i][t] = ok ? *reinterpret_cast<const uint4*>(x[t] + k) : zero;
+      for (int t = 0; t < NT; ++t) xv[i][t] = ld16(x[t] + k);
     }
 #pragma unroll
-    for (int i = 0; i < FEW_UNROLL; ++i) {
-      const uint32_t lo[4] = {wa[i].x, wb[i].x, wa[i].y, wb[i].y}, hi[4] = {wa[i].z, wb[i].z, wa[i].w, wb[i].w};
+    for (int i = 0; i < U; ++i) {
+      const bool in = (s0 + i) * 32 + q * 8 < a.K;
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u), va = in ? wa[i] : z, vb = in ? wb[i] : z;
+      const uint32_t lo[4] = {va.x, vb.x, va.y, vb.y}, hi[4] = {va.z, vb.z, va.w, vb.w};
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        mma_16816(d[t], lo, xv[i][t].x, xv[i][t].y, Tin());
-        mma_16816(d[t], hi, xv[i][t].z, xv[i][t].w, Tin());
+        const uint4 vx = in ? xv[i][t] : z;
+        mma_16816(d[t], lo, vx.x, vx.y, Tin());
+        mma_16816(d[t], hi, vx.z, vx.w, Tin());
       }
     }
   }
