@@ -20,8 +20,8 @@
 // rounds over the pairs take the least time.
 //
 // linear_few_kernel: a handful of rows (one token of each sequence).  The work
-// is one read of W, so W goes from global memory straight into mma.sync operand
-// registers, 16 bytes a lane, eight warps splitting K of 16 W rows, the sums joined
+// is one read of W, so W goes in 16-byte chunks into the mma.sync operands of the
+// lane that copied them, eight warps splitting K of 16 W rows, the sums joined
 // in shared memory.  The K order inside a 32-wide step is the one in which the 16-byte
 // loads arrive, the same for both operands (a dot product does not mind).
 //
@@ -39,20 +39,19 @@ namespace {
 constexpr int LM = 128;                                  // rows of a CTA's half tile
 constexpr int LN_MAX = 256;                              // columns of a tile
 constexpr int LK = 64;                                   // K per stage (one 128-byte swizzled row)
-constexpr int L_STAGES = 6;
+constexpr int L_MAX_STAGES = 9;                          // ring: 6 stages at LN = 256, 8 at 128, 9 at 64
 constexpr int L_EPI_WARPS = 8;                           // warps 2-9
 constexpr int L_THREADS = 64 + 32 * L_EPI_WARPS;
 constexpr uint32_t L_A_BYTES = LM * 128;
-constexpr uint32_t L_W_BYTES = LN_MAX / 2 * 128;
-constexpr uint32_t L_STAGE_BYTES = L_A_BYTES + L_W_BYTES;
+constexpr uint32_t L_RING_BYTES = 6 * (L_A_BYTES + LN_MAX / 2 * 128);   // 192 KB
 constexpr uint32_t L_OUT_BYTES = 32 * 128;               // output staging of one epilogue warp
-constexpr uint32_t L_OFF_OUT = L_STAGES * L_STAGE_BYTES;
+constexpr uint32_t L_OFF_OUT = L_RING_BYTES;
 constexpr uint32_t L_OFF_BAR = L_OFF_OUT + L_EPI_WARPS * L_OUT_BYTES;
-constexpr uint32_t LB_FULL = 0;                          // [L_STAGES] (the leader's: both CTAs' copies)
-constexpr uint32_t LB_EMPTY = 64;                        // [L_STAGES] (each CTA's own)
-constexpr uint32_t LB_ACC_FULL = 128;                    // [2] (each CTA's own)
-constexpr uint32_t LB_ACC_EMPTY = 144;                   // [2] (the leader's: one arrival per epilogue warp of both)
-constexpr uint32_t LW_TMEM = 160, LW_ABORT = 164;
+constexpr uint32_t LB_FULL = 0;                          // [stages] (the leader's: both CTAs' copies)
+constexpr uint32_t LB_EMPTY = 80;                        // [stages] (each CTA's own)
+constexpr uint32_t LB_ACC_FULL = 160;                    // [2] (each CTA's own)
+constexpr uint32_t LB_ACC_EMPTY = 176;                   // [2] (the leader's: one arrival per epilogue warp of both)
+constexpr uint32_t LW_TMEM = 192, LW_ABORT = 196;
 constexpr uint32_t L_SMEM = L_OFF_BAR + 256;
 constexpr uint32_t L_TMEM_COLS = 512;
 
@@ -94,8 +93,12 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// Arrival on a barrier of the pair's leader.  It publishes no memory (what it
+// orders are this warp's TMEM reads, by the tcgen05 fence before it), so it
+// releases at CTA scope: at cluster scope it waited for the warp's global
+// stores, 1800 cycles a tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
@@ -227,10 +230,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
                        const LinearEpiArgs a, int act) {
   extern __shared__ __align__(1024) uint8_t smem_linear[];
   const uint32_t base = smem_u32(smem_linear);
-  auto s_a = [&](int s) { return base + static_cast<uint32_t>(s) * L_STAGE_BYTES; };
-  auto s_w = [&](int s) { return base + static_cast<uint32_t>(s) * L_STAGE_BYTES + L_A_BYTES; };
   const uint32_t bars = base + L_OFF_BAR;
-  auto bar = [&](uint32_t kind, int i) { return bars + kind + 8 * static_cast<uint32_t>(i); };
+  auto bar = [&](uint32_t kind, uint32_t i) { return bars + kind + 8 * i; };
   const uint32_t abort_flag = bars + LW_ABORT;
   const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_linear + L_OFF_BAR + LW_TMEM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -243,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int s = 0; s < L_STAGES; ++s) {
+    for (int s = 0; s < L_MAX_STAGES; ++s) {
       mbar_init(bar(LB_FULL, s), 1);
       mbar_init(bar(LB_EMPTY, s), 1);
     }
@@ -272,25 +273,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     const int nt = (a.N + ln - 1) / ln;
     const long long tiles = static_cast<long long>((T + 2 * LM - 1) / (2 * LM)) * nt;   // row tiles outermost
     const int kchunks = (a.K + LK - 1) / LK;
+    const uint32_t stage_bytes = L_A_BYTES + static_cast<uint32_t>(ln / 2) * 128u;   // A rows, then W rows
+    const uint32_t stages = L_RING_BYTES / stage_bytes;
     if (warp == 0) {
       // ------------------------------------------------------------ loads
       const CUtensorMap* mw = ln == 256 ? &map_w128 : (ln == 128 ? &map_w64 : &map_w32);
-      const uint32_t bytes = 2 * (L_A_BYTES + static_cast<uint32_t>(ln / 2) * 128u);
-      uint32_t it = 0;
+      uint32_t s = 0, lap = 0;                           // ring position: stage and times round
       if (elect_one()) {
         for (long long t = pair; t < tiles && !bad; t += pairs) {
           const int m0 = static_cast<int>(t / nt) * 2 * LM + static_cast<int>(rank) * LM;
           const int n0 = static_cast<int>(t % nt) * ln + static_cast<int>(rank) * (ln / 2);
-          for (int kc = 0; kc < kchunks; ++kc, ++it) {
-            const int s = static_cast<int>(it % L_STAGES);
-            if (it >= L_STAGES && !mbar_wait_or_abort(bar(LB_EMPTY, s), (it / L_STAGES - 1) & 1, abort_flag)) {
+          for (int kc = 0; kc < kchunks; ++kc) {
+            if (lap > 0 && !mbar_wait_or_abort(bar(LB_EMPTY, s), (lap - 1) & 1, abort_flag)) {
               bad = true;
               break;
             }
-            if (rank == 0) mbar_expect_tx(bar(LB_FULL, s), bytes);
-            const uint32_t full = map_rank(bar(LB_FULL, s), 0);
-            tma_load_2d_pair(s_a(s), &map_a, kc * LK, m0, full);    // rows past cap, columns past K: zeros
-            tma_load_2d_pair(s_w(s), mw, kc * LK, n0, full);
+            if (rank == 0) mbar_expect_tx(bar(LB_FULL, s), 2 * stage_bytes);
+            const uint32_t full = map_rank(bar(LB_FULL, s), 0), dst = base + s * stage_bytes;
+            tma_load_2d_pair(dst, &map_a, kc * LK, m0, full);       // rows past cap, columns past K: zeros
+            tma_load_2d_pair(dst + L_A_BYTES, mw, kc * LK, n0, full);
+            if (++s == stages) {
+              s = 0;
+              ++lap;
+            }
           }
         }
       }
@@ -299,28 +304,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
       // ------------------------------------------------------------ products
       if (rank == 0 && elect_one()) {
         const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, ln);
-        const uint64_t da0 = sdesc(s_a(0), 16, 1024), dw0 = sdesc(s_w(0), 16, 1024);
-        uint32_t it = 0, i = 0;
+        const uint64_t da0 = sdesc(base, 16, 1024), dw0 = sdesc(base + L_A_BYTES, 16, 1024);
+        uint32_t s = 0, lap = 0, i = 0;
         for (long long t = pair; t < tiles && !bad; t += pairs, ++i) {
-          const int b = i & 1;
+          const uint32_t b = i & 1;
           if (i >= 2 && !mbar_wait_or_abort(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag)) {
             bad = true;
             break;
           }
           tc_fence_after();
           const uint32_t acc = tmem + static_cast<uint32_t>(b) * LN_MAX;
-          for (int kc = 0; kc < kchunks; ++kc, ++it) {
-            const uint32_t s = it % L_STAGES;
-            if (!mbar_wait_or_abort(bar(LB_FULL, static_cast<int>(s)), (it / L_STAGES) & 1, abort_flag)) {
+          for (int kc = 0; kc < kchunks; ++kc) {
+            if (!mbar_wait_or_abort(bar(LB_FULL, s), lap & 1, abort_flag)) {
               bad = true;
               break;
             }
             tc_fence_after();
-            const uint64_t off = s * (L_STAGE_BYTES >> 4);
+            const uint64_t off = s * (stage_bytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < LK / 16; ++kk)
               umma_f16_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
-            umma_commit_pair(bar(LB_EMPTY, static_cast<int>(s)));
+            umma_commit_pair(bar(LB_EMPTY, s));
+            if (++s == stages) {
+              s = 0;
+              ++lap;
+            }
           }
           if (!bad) umma_commit_pair(bar(LB_ACC_FULL, b));
         }
@@ -334,8 +342,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
       const uint32_t stg = base + L_OFF_OUT + static_cast<uint32_t>(warp - 2) * L_OUT_BYTES;
       const uint32_t acc_empty[2] = {map_rank(bar(LB_ACC_EMPTY, 0), 0), map_rank(bar(LB_ACC_EMPTY, 1), 0)};
       uint32_t i = 0;
+      // This lane's columns of the bias of piece p (of the tile at column n0): lane, and lane + 32 of a 64-column piece.
+      float bias0 = 0.f, bias1 = 0.f;
+      auto load_bias = [&](int col0) {
+        if (a.bias == nullptr || col0 >= a.N) return;
+        bias0 = __ldg(a.bias + min(col0 + lane, a.N - 1));
+        if (CPP > 32) bias1 = __ldg(a.bias + min(col0 + 32 + lane, a.N - 1));
+      };
       for (long long t = pair; t < tiles; t += pairs, ++i) {
-        const int b = i & 1;
+        const uint32_t b = i & 1;
+        load_bias(static_cast<int>(t % nt) * ln + half * CPP);
         if (!mbar_wait_or_abort(bar(LB_ACC_FULL, b), (i >> 1) & 1, abort_flag)) bad = true;
         bad = __any_sync(0xffffffffu, bad);
         if (bad) break;
@@ -344,10 +360,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         const int n0 = static_cast<int>(t % nt) * ln;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(b) * LN_MAX;
         const int cc = lane & 7;                         // this lane's 16-byte chunk of a row piece
+        const int cols = m0 < T ? min(ln, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
 #pragma unroll 1
-        for (int p = half; p * CPP < ln; p += 2) {
+        for (int p = half; p * CPP < cols; p += 2) {
           const int col0 = n0 + p * CPP;
-          if (col0 >= a.N || m0 >= T) break;
           const bool col_ok = col0 + cc * Ch::N < a.N;   // N is a multiple of 8: chunks are whole
           auto at = [&](int r) { return static_cast<size_t>(m0 + r) * a.N + col0 + cc * Ch::N; };
           uint4 res[8];
@@ -361,17 +377,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           float v[CPP];
 #pragma unroll
           for (int q = 0; q < CPP / 32; ++q) tmem_ld32(taddr + p * CPP + q * 32, v + q * 32);
+          if ((p + 2) * CPP >= cols) {
+            // This warp's share of the accumulator is in registers: the products of tile i + 2 may overwrite it.
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty[b]);
+          }
           if (a.bias != nullptr) {
-            const float4* b4 = reinterpret_cast<const float4*>(a.bias + col0);
+            // From a column per lane to every lane through the staging rows (16
+            // broadcast loads from global memory came one after another: 3600 cycles a piece).
+            st_shared_u32(stg + lane * 4, __float_as_uint(bias0));
+            if (CPP > 32) st_shared_u32(stg + 128 + lane * 4, __float_as_uint(bias1));
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < CPP / 4; ++j) {
-              // Past N: the last columns' bias, for outputs that are not stored (a guard would put the loads in a row).
-              const float4 bb = __ldg(b4 + min(j, (a.N - col0) / 4 - 1));
-              v[4 * j] += bb.x;
-              v[4 * j + 1] += bb.y;
-              v[4 * j + 2] += bb.z;
-              v[4 * j + 3] += bb.w;
+              const uint4 bb = ld_shared_v4(stg + 16 * j);
+              v[4 * j] += __uint_as_float(bb.x);
+              v[4 * j + 1] += __uint_as_float(bb.y);
+              v[4 * j + 2] += __uint_as_float(bb.z);
+              v[4 * j + 3] += __uint_as_float(bb.w);
             }
+            __syncwarp();
+            load_bias(n0 + (p + 2) * CPP);
           }
           activate(v, act);
           if (a.residual != nullptr) {
@@ -399,9 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           }
           __syncwarp();                                  // read back before the next piece is written
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty[b]);
+        if (half * CPP >= cols && lane == 0) mbar_arrive_cluster(acc_empty[b]);   // no piece for this warp
       }
     }
     if (bad && lane == 0) {
@@ -430,7 +455,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
 // ------------------------------------------------------------------ few rows
 
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_UNROLL = 8;     // 32-wide K steps in flight per warp (few rows: 16 KB a warp)
+// Steps of 32 in K in flight per warp: about 96 KB a CTA, two CTAs an SM.
+template <int NT> struct FewCfg {
+  static constexpr int U = NT == 1 ? 8 : (NT == 2 ? 6 : 4);
+  static constexpr int SMEM = U * (2 + NT) * FEW_WARPS * 32 * 16;
+};
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
   asm volatile(
@@ -444,26 +473,16 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Both loads are volatile so that they stay ahead of the products: left to
-// the compiler they sank to their uses and a warp had one step in flight.
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // NT: groups of 8 rows of a.  One CTA: 16 columns of c.
 template <typename Tin, typename Tout, int NT>
 __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const LinearEpiArgs a, int act) {
+  constexpr int U = FewCfg<NT>::U;
   __shared__ float part[FEW_WARPS][16][NT * 8 + 1];
+  extern __shared__ __align__(16) uint8_t smem_few[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int n0 = static_cast<int>(blockIdx.x) * 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -484,32 +503,43 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   float d[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
-  // Steps of 32 in K, U at a time and a warp's share in turn; U shrinks as
-  // the rows of a take more registers.
-  constexpr int U = NT == 1 ? FEW_UNROLL : (NT == 2 ? FEW_UNROLL / 2 : FEW_UNROLL / 4);
-  const int steps = (a.K + 31) / 32;
-  for (int s0 = warp * U; s0 < steps; s0 += FEW_WARPS * U) {
-    uint4 wa[U], wb[U], xv[U][NT];
+  // Steps of 32 in K, taken by the warps in turn.  Each lane copies its own
+  // chunks into its own slots of shared memory and reads them back, U steps
+  // later: no other lane waits for them, and the copies in flight need no
+  // registers (as register loads the compiler kept one step in flight).
+  const uint32_t slot = smem_u32(smem_few) + static_cast<uint32_t>(threadIdx.x) * 16u;
+  auto chunk = [&](int u, int j) { return slot + static_cast<uint32_t>((u * (2 + NT) + j) * FEW_WARPS * 32) * 16u; };
+  const int steps = (a.K + 31) / 32, mine = (steps - warp + FEW_WARPS - 1) / FEW_WARPS;
+  auto fetch = [&](int i, int u) {
+    // K is a multiple of 8: chunks are whole; past K the last one is copied and counts as zero.
+    const int k = min((warp + i * FEW_WARPS) * 32 + q * 8, a.K - 8);
+    cp_async16(chunk(u, 0), w0 + k);
+    cp_async16(chunk(u, 1), w1 + k);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      // K is a multiple of 8: chunks are whole; past K the last one is loaded and counts as zero.
-      const int k = min((s0 + i) * 32 + q * 8, a.K - 8);
-      wa[i] = ld_stream16(w0 + k);
-      wb[i] = ld_stream16(w1 + k);
+    for (int t = 0; t < NT; ++t) cp_async16(chunk(u, 2 + t), x[t] + k);
+  };
 #pragma unroll
-      for (int t = 0; t < NT; ++t) xv[i][t] = ld16(x[t] + k);
-    }
+  for (int i = 0; i < U; ++i) {
+    if (i < mine) fetch(i, i);
+    cp_async_commit();
+  }
+  int u = 0;
+  for (int i = 0; i < mine; ++i) {
+    cp_async_wait<U - 1>();
+    const bool in = (warp + i * FEW_WARPS) * 32 + q * 8 < a.K;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 va = in ? ld_shared_v4(chunk(u, 0)) : z, vb = in ? ld_shared_v4(chunk(u, 1)) : z;
+    uint4 vx[NT];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const bool in = (s0 + i) * 32 + q * 8 < a.K;
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u), va = in ? wa[i] : z, vb = in ? wb[i] : z;
-      const uint32_t lo[4] = {va.x, vb.x, va.y, vb.y}, hi[4] = {va.z, vb.z, va.w, vb.w};
+    for (int t = 0; t < NT; ++t) vx[t] = in ? ld_shared_v4(chunk(u, 2 + t)) : z;
+    if (i + U < mine) fetch(i + U, u);
+    cp_async_commit();
+    if (++u == U) u = 0;
+    const uint32_t lo[4] = {va.x, vb.x, va.y, vb.y}, hi[4] = {va.z, vb.z, va.w, vb.w};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 vx = in ? xv[i][t] : z;
-        mma_16816(d[t], lo, vx.x, vx.y, Tin());
-        mma_16816(d[t], hi, vx.z, vx.w, Tin());
-      }
+    for (int t = 0; t < NT; ++t) {
+      mma_16816(d[t], lo, vx[t].x, vx[t].y, Tin());
+      mma_16816(d[t], hi, vx[t].z, vx[t].w, Tin());
     }
   }
 #pragma unroll
@@ -580,10 +610,9 @@ cudaLaunchConfig_t dependent_config(cudaLaunchAttribute* attr, int grid, int thr
   return cfg;
 }
 
-template <typename Tin, typename Tout>
-cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
-  if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
-  auto kernel = linear_pair_kernel<Tin, Tout>;
+// Once per device and kernel (the template arguments name the kernel): its dynamic shared memory.
+template <typename Tin, typename Tout, int NT, typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
   constexpr int kMaxDevices = 64;
   static bool attr_set[kMaxDevices] = {};
   static std::mutex m;
@@ -591,14 +620,21 @@ cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(m);
-    if (!attr_set[dev]) {
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L_SMEM)) != cudaSuccess)
-        return e;
-      attr_set[dev] = true;
-    }
+  std::lock_guard<std::mutex> lock(m);
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
   }
+  return cudaSuccess;
+}
+
+template <typename Tin, typename Tout>
+cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
+  if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
+  auto kernel = linear_pair_kernel<Tin, Tout>;
+  cudaError_t e = allow_smem<Tin, Tout, 0>(kernel, L_SMEM);
+  if (e != cudaSuccess) return e;
   const bool bf16 = IsBf16<Tin>::value == 1;
   CUtensorMap ma, mw[3];
   if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, LM)) != cudaSuccess) return e;
@@ -613,9 +649,12 @@ cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream
 
 template <typename Tin, typename Tout, int NT>
 cudaError_t launch_few(const LinearEpiArgs& a, int act, cudaStream_t stream) {
+  auto kernel = linear_few_kernel<Tin, Tout, NT>;
+  if (cudaError_t e = allow_smem<Tin, Tout, NT>(kernel, FewCfg<NT>::SMEM); e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = dependent_config(&attr, (a.N + 15) / 16, 32 * FEW_WARPS, 0, stream);
-  return cudaLaunchKernelEx(&cfg, linear_few_kernel<Tin, Tout, NT>, a, act);
+  const cudaLaunchConfig_t cfg =
+      dependent_config(&attr, (a.N + 15) / 16, 32 * FEW_WARPS, FewCfg<NT>::SMEM, stream);
+  return cudaLaunchKernelEx(&cfg, kernel, a, act);
 }
 
 template <typename Tin, typename Tout>
