@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   if (T == 0) return;
   const Tin* W = static_cast<const Tin*>(a.w);
   const Tin* X = static_cast<const Tin*>(a.a);
-  // Rows past N or T repeat the last one: their results are not stored.
+  // Rows past N repeat the last one, rows past T are zeros: their results are not stored.
   const Tin* w0 = W + static_cast<size_t>(min(n0 + g, a.N - 1)) * a.K;
   const Tin* w1 = W + static_cast<size_t>(min(n0 + g + 8, a.N - 1)) * a.K;
   const Tin* x[NT];
@@ -509,14 +509,24 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   // registers (as register loads the compiler kept one step in flight).
   const uint32_t slot = smem_u32(smem_few) + static_cast<uint32_t>(threadIdx.x) * 16u;
   auto chunk = [&](int u, int j) { return slot + static_cast<uint32_t>((u * (2 + NT) + j) * FEW_WARPS * 32) * 16u; };
-  const int steps = (a.K + 31) / 32, mine = (steps - warp + FEW_WARPS - 1) / FEW_WARPS;
+  // A warp takes pairs of steps (whole 128-byte lines of W), starting at a
+  // place that differs from CTA to CTA: all CTAs read the same rows of a, and
+  // in step they would all ask one L2 line at a time.
+  const int units = (a.K + 63) / 64, mine = 2 * ((units - warp + FEW_WARPS - 1) / FEW_WARPS);
+  const int turn = mine > 0 ? 2 * (static_cast<int>(blockIdx.x) % (mine / 2)) : 0;
+  auto k_of = [&](int i) {
+    int j = i + turn;
+    if (j >= mine) j -= mine;
+    return (warp + (j >> 1) * FEW_WARPS) * 64 + (j & 1) * 32 + q * 8;
+  };
   auto fetch = [&](int i, int u) {
     // K is a multiple of 8: chunks are whole; past K the last one is copied and counts as zero.
-    const int k = min((warp + i * FEW_WARPS) * 32 + q * 8, a.K - 8);
+    const int k = min(k_of(i), a.K - 8);
     cp_async16(chunk(u, 0), w0 + k);
     cp_async16(chunk(u, 1), w1 + k);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) cp_async16(chunk(u, 2 + t), x[t] + k);
+    for (int t = 0; t < NT; ++t)
+      if (8 * t + g < T) cp_async16(chunk(u, 2 + t), x[t] + k);
   };
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -526,12 +536,12 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   int u = 0;
   for (int i = 0; i < mine; ++i) {
     cp_async_wait<U - 1>();
-    const bool in = (warp + i * FEW_WARPS) * 32 + q * 8 < a.K;
+    const bool in = k_of(i) < a.K;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     const uint4 va = in ? ld_shared_v4(chunk(u, 0)) : z, vb = in ? ld_shared_v4(chunk(u, 1)) : z;
     uint4 vx[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) vx[t] = in ? ld_shared_v4(chunk(u, 2 + t)) : z;
+    for (int t = 0; t < NT; ++t) vx[t] = in && 8 * t + g < T ? ld_shared_v4(chunk(u, 2 + t)) : z;
     if (i + U < mine) fetch(i + U, u);
     cp_async_commit();
     if (++u == U) u = 0;
