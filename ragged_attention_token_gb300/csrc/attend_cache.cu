@@ -43,8 +43,9 @@ struct CacheCfg {
   static constexpr int STAGES = C_RING / (2 * TILE);      // 3 at d = 128, 6 at d = 64
   // Partial results of a warp, over its ring once its keys are done: O [16][D], then m [16], l [16] (fp32).
   static constexpr int PART = (C_ROWS * D + 2 * C_ROWS) * 4;
+  static constexpr int CTA_PART = C_RING / 2;             // the CTA's joined result, behind warp 0's
   static constexpr int SMEM = C_WARPS * C_RING;
-  static_assert(PART <= C_RING, "partial results live in the ring");
+  static_assert(PART <= CTA_PART, "both lie in warp 0's ring");
 };
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
@@ -76,10 +77,20 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+// Reads of another CTA's shared memory, between the two cluster barriers
+// (nothing is written there then, so they need no order among themselves).
+__device__ __forceinline__ float ld_cluster(uint32_t cluster_addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
   return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -88,13 +99,14 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * C_WARPS, 2) attend_cache_kernel(const CacheArgs a, int nsplit, int row_blocks) {
+__global__ void __launch_bounds__(32 * C_WARPS, 2)
+    attend_cache_kernel(const CacheArgs a, int cluster, int min_chunks, int row_blocks) {
   using C = CacheCfg<D>;
   constexpr bool BF = IsBf16<T>::value == 1;
   extern __shared__ __align__(128) uint8_t smem_cache[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int split = static_cast<int>(blockIdx.x) % nsplit;         // = the CTA's rank in its cluster
-  const int unit = static_cast<int>(blockIdx.x) / nsplit;
+  const int split = static_cast<int>(blockIdx.x) % cluster;        // = the CTA's rank in its cluster
+  const int unit = static_cast<int>(blockIdx.x) / cluster;
   const int rb = unit % row_blocks, hk = unit / row_blocks % a.Hkv, b = unit / row_blocks / a.Hkv;
   const int G = a.Hq / a.Hkv;
   const int rows = min(C_ROWS, a.nq * G - rb * C_ROWS);            // row r: token r / G, head hk * G + r % G (r from rb * 16)
@@ -108,7 +120,12 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2) attend_cache_kernel(const Cac
   // Keys that row r of the unit sees: its first `sees(r)` ones (not above zero: none).
   auto sees = [&](int r) { return len - (a.nq - 1 - (rb * C_ROWS + r) / G); };
   const int keys = valid ? max(0, sees(rows - 1)) : 0;
-  const int chunks = (keys + CK - 1) / CK, stride = nsplit * C_WARPS, first = split * C_WARPS + warp;
+  const int chunks = (keys + CK - 1) / CK;
+  // The CTAs that share the keys: no more than give each warp its min_chunks
+  // (the host knows only the cache's capacity); the others of the cluster leave.
+  const int nsplit = min(cluster, max(1, chunks / (C_WARPS * min_chunks)));
+  if (split >= nsplit) return;
+  const int stride = nsplit * C_WARPS, first = split * C_WARPS + warp;
   const int mine = first < chunks ? (chunks - first + stride - 1) / stride : 0;
 
   // Copies of this warp's i-th chunk into stage s, 16-byte pieces, 128-byte
@@ -244,89 +261,152 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2) attend_cache_kernel(const Cac
       part[C_ROWS * D + C_ROWS + r] = l_run[x];
     }
   }
-  if (nsplit > 1) asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-  else __syncthreads();
+  __syncthreads();
 
-  // The cluster's CTAs take pairs of output elements in turn; each pair reads
-  // all partial results in the same order.
-  const uint32_t part0 = smem_u32(smem_cache);
-  for (int e = split * blockDim.x + threadIdx.x; valid && e < rows * (D / 2); e += nsplit * blockDim.x) {
-    const int r = e / (D / 2), c = 2 * (e % (D / 2));
-    float top = -INFINITY;
-    for (int p = 0; p < stride; ++p) {
-      const uint32_t at = map_rank(part0 + static_cast<uint32_t>(p % C_WARPS) * C_RING, static_cast<uint32_t>(p / C_WARPS));
-      top = fmaxf(top, ld_cluster_f32(at + 4u * static_cast<uint32_t>(C_ROWS * D + r)));
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, y0 = 0.f, y1 = 0.f;
-    for (int p = 0; p < stride; ++p) {
-      const uint32_t at = map_rank(part0 + static_cast<uint32_t>(p % C_WARPS) * C_RING, static_cast<uint32_t>(p / C_WARPS));
-      const float w = fast_exp2(ld_cluster_f32(at + 4u * static_cast<uint32_t>(C_ROWS * D + r)) - ref);
-      sum = fmaf(w, ld_cluster_f32(at + 4u * static_cast<uint32_t>(C_ROWS * D + C_ROWS + r)), sum);
-      y0 = fmaf(w, ld_cluster_f32(at + 4u * static_cast<uint32_t>(r * D + c)), y0);
-      y1 = fmaf(w, ld_cluster_f32(at + 4u * static_cast<uint32_t>(r * D + c + 1)), y1);
-    }
+  // Four neighbouring outputs of row r as T.
+  auto store = [&](int r, int c, float4 y, float sum) {
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     const int rr = rb * C_ROWS + r;
     T* out = static_cast<T*>(a.o) + ((static_cast<long long>(b) * a.nq + rr / G) * a.Hq + hk * G + rr % G) * D + c;
-    const uint32_t w = BF ? pack2<__nv_bfloat162>(y0 * inv, y1 * inv) : pack2<__half2>(y0 * inv, y1 * inv);
-    *reinterpret_cast<uint32_t*>(out) = w;
+    uint2 w;
+    w.x = BF ? pack2<__nv_bfloat162>(y.x * inv, y.y * inv) : pack2<__half2>(y.x * inv, y.y * inv);
+    w.y = BF ? pack2<__nv_bfloat162>(y.z * inv, y.w * inv) : pack2<__half2>(y.z * inv, y.w * inv);
+    *reinterpret_cast<uint2*>(out) = w;
+  };
+  constexpr int QUADS = D / 4;
+  // The CTA's warps joined: O, reference and sum of each row.
+  float* joined = reinterpret_cast<float*>(smem_cache + C::CTA_PART);
+  for (int e = threadIdx.x; valid && e < rows * QUADS; e += 32 * C_WARPS) {
+    const int r = e / QUADS, c = 4 * (e % QUADS);
+    float m[C_WARPS], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < C_WARPS; ++w) {
+      m[w] = reinterpret_cast<const float*>(smem_cache + w * C_RING)[C_ROWS * D + r];
+      top = fmaxf(top, m[w]);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < C_WARPS; ++w) {
+      const float* p = reinterpret_cast<const float*>(smem_cache + w * C_RING);
+      const float f = fast_exp2(m[w] - ref);
+      const float4 v = *reinterpret_cast<const float4*>(p + r * D + c);
+      sum = fmaf(f, p[C_ROWS * D + C_ROWS + r], sum);
+      y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+    }
+    if (nsplit == 1) {
+      store(r, c, y, sum);
+    } else {
+      *reinterpret_cast<float4*>(joined + r * D + c) = y;
+      if (c == 0) {
+        joined[C_ROWS * D + r] = top;
+        joined[C_ROWS * D + C_ROWS + r] = sum;
+      }
+    }
   }
-  // No CTA leaves while another may still read its partial results.
-  if (nsplit > 1) asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+  if (nsplit == 1) return;
+  cluster_sync_all();                       // (a CTA that left counts as arrived)
+  // The cluster's CTAs joined, each CTA a share of the outputs, in rank order.
+  const uint32_t mine_at = smem_u32(joined);
+  for (int e = split * 32 * C_WARPS + threadIdx.x; valid && e < rows * QUADS; e += nsplit * 32 * C_WARPS) {
+    const int r = e / QUADS, c = 4 * (e % QUADS);
+    float m[C_MAX_SPLIT], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < C_MAX_SPLIT; ++p) {
+      m[p] = p < nsplit ? ld_cluster(map_rank(mine_at, p) + 4u * static_cast<uint32_t>(C_ROWS * D + r)) : -INFINITY;
+    }
+#pragma unroll
+    for (int p = 0; p < C_MAX_SPLIT; ++p) top = fmaxf(top, m[p]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < nsplit; ++p) {
+      const uint32_t at = map_rank(mine_at, p);
+      const float4 v = ld_cluster4(at + 4u * static_cast<uint32_t>(r * D + c));
+      const float lp = ld_cluster(at + 4u * static_cast<uint32_t>(C_ROWS * D + C_ROWS + r));
+      const float f = fast_exp2(ld_cluster(at + 4u * static_cast<uint32_t>(C_ROWS * D + r)) - ref);
+      sum = fmaf(f, lp, sum);
+      y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+    }
+    store(r, c, y, sum);
+  }
+  cluster_sync_all();                       // no CTA leaves while another may still read its result
 }
 
+// The CTAs a cluster may have here, 16 or 8 (set up once per device and kernel).
 template <typename T, int D>
-cudaError_t launch_d(const CacheArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t cluster_limit(int* most) {
   using C = CacheCfg<D>;
   auto kernel = attend_cache_kernel<T, D>;
   constexpr int kMaxDevices = 64;
-  static int max_split[kMaxDevices] = {};                 // 0: not yet set up
+  static int limit[kMaxDevices] = {};
   static std::mutex m;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(m);
+  if (limit[dev] == 0) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+    int clusters = 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C_MAX_SPLIT;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(C_MAX_SPLIT);
+    cfg.blockDim = dim3(32 * C_WARPS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      clusters = 0;
+    }
+    limit[dev] = clusters > 0 ? C_MAX_SPLIT : C_MAX_SPLIT / 2;
+  }
+  *most = limit[dev];
+  return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const CacheArgs& a, int num_sms, cudaStream_t stream) {
+  const int row_blocks = (a.nq * (a.Hq / a.Hkv) + C_ROWS - 1) / C_ROWS;
+  const long long units = static_cast<long long>(a.B) * a.Hkv * row_blocks;
+  int most = 0;
+  cudaError_t e = cluster_limit<T, D>(&most);
+  if (e != cudaSuccess) return e;
+  // Few units: split them until the CTAs fill the SMs once (two at a time),
+  // leaving a warp four chunks.  A second round of such small CTAs costs more than
+  // it evens out (4 x 4096 keys, 8 heads: 8 CTAs a unit 11.5 us, 16 25.7 us).  Units
+  // that nearly fill them over a long cache: up to four CTAs with at least 32 chunks a
+  // warp even out sequences of different lengths (32 x up to 16384 keys, 8 heads: 1 CTA
+  // a unit 167 us, 4 155 us, 16 216 us).  More units even out by themselves (48 x 1000 keys,
+  // 12 heads, in a cache of 32768: 1 CTA a unit 26 us, 2 40 us).
+  const int chunks = (a.cap - 1) / CK + 1;
+  int cluster = 1, min_chunks = 4;
+  while (2 * cluster <= most && units * 2 * cluster <= 2LL * num_sms && chunks >= 2 * cluster * C_WARPS * min_chunks)
+    cluster *= 2;
+  while (cluster < 4 && units <= 2LL * num_sms && chunks >= 2 * cluster * C_WARPS * 32) {
+    cluster *= 2;
+    min_chunks = 32;
+  }
+  if (units * cluster >= (1LL << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
   cfg.blockDim = dim3(32 * C_WARPS);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = CacheCfg<D>::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
-  int most;
-  {
-    std::lock_guard<std::mutex> lock(m);
-    if (max_split[dev] == 0) {
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
-      // Clusters of 16 where the device takes them, else of 8 (which every device of this kind does).
-      int clusters = 0;
-      attr[0].val.clusterDim.x = C_MAX_SPLIT;
-      cfg.gridDim = dim3(C_MAX_SPLIT);
-      cfg.numAttrs = 1;
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        clusters = 0;
-      }
-      max_split[dev] = clusters > 0 ? C_MAX_SPLIT : C_MAX_SPLIT / 2;
-    }
-    most = max_split[dev];
-  }
-  const int row_blocks = (a.nq * (a.Hq / a.Hkv) + C_ROWS - 1) / C_ROWS;
-  const long long units = static_cast<long long>(a.B) * a.Hkv * row_blocks;
-  // Split until the CTAs fill the SMs four times over (two at a time), so that
-  // sequences of very different lengths even out, but leave a warp four chunks.
-  int nsplit = 1;
-  while (nsplit < most && units * nsplit < 8LL * num_sms && (a.cap + CK - 1) / CK >= 2 * nsplit * C_WARPS * 4) nsplit *= 2;
-  if (units * nsplit >= (1LL << 31)) return cudaErrorInvalidValue;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(nsplit);
-  cfg.gridDim = dim3(static_cast<unsigned>(units * nsplit));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, nsplit, row_blocks);
+  return cudaLaunchKernelEx(&cfg, attend_cache_kernel<T, D>, a, cluster, min_chunks, row_blocks);
 }
 
 }  // namespace
