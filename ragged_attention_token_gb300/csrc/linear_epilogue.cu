@@ -54,6 +54,11 @@ constexpr uint32_t LB_ACC_EMPTY = 176;                   // [2] (the leader's: o
 constexpr uint32_t LW_TMEM = 192, LW_ABORT = 196;
 constexpr uint32_t L_SMEM = L_OFF_BAR + 256;
 constexpr uint32_t L_TMEM_COLS = 512;
+// fp32 outputs: the tensor cores' additions truncate, which after K = 8192 has
+// cost 1e-5 of the sum, so a tile is computed in parts of 8 chunks (K = 512),
+// added in registers by the epilogue warps (which hold 128 columns of a tile):
+// 7e-7.  16-bit outputs are rounded at 2^-9 and keep one sum.
+constexpr int L_PART = 8, LN_PARTS = 128;
 
 // --------------------------------------------------------- pair-of-CTAs PTX
 
@@ -208,12 +213,11 @@ template <> struct Chunk<__half> {
 
 // Columns of a tile: the width whose rounds over `pairs` pairs cost least, a
 // tile of LN columns counted as LN + 64 (its A half is loaded whatever its width).
-__device__ __forceinline__ int tile_columns(int T, int N, int pairs) {
+__device__ __forceinline__ int tile_columns(int T, int N, int pairs, int most) {
   const long long mt = (T + 2 * LM - 1) / (2 * LM);
-  int best = LN_MAX;
+  int best = most;
   long long cost = -1;
-#pragma unroll
-  for (int ln = LN_MAX; ln >= 64; ln /= 2) {
+  for (int ln = most; ln >= 64; ln /= 2) {
     const long long tiles = mt * ((N + ln - 1) / ln), c = (tiles + pairs - 1) / pairs * (ln + 64);
     if (cost < 0 || c < cost) {
       cost = c;
@@ -223,11 +227,25 @@ __device__ __forceinline__ int tile_columns(int T, int N, int pairs) {
   return best;
 }
 
+// Tile t of the grid of mt x nt: bands of 8 row tiles, column by column within
+// a band, so that the pairs at work together share their rows of a and of W
+// (8 x 9.5 tiles at 76 pairs).  With whole rows of tiles in order, every
+// row tile read all of W again: 8192 x 4096 x 16384 took 780 us under load.
+constexpr int L_BAND = 8;
+__device__ __forceinline__ void tile_at(long long t, int mt, int nt, int& m, int& n) {
+  const int band = static_cast<int>(t / (static_cast<long long>(L_BAND) * nt));
+  const int rows = min(L_BAND, mt - band * L_BAND);
+  const int r = static_cast<int>(t - static_cast<long long>(band) * L_BAND * nt);
+  m = band * L_BAND + r % rows;
+  n = r / rows;
+}
+
 template <typename Tin, typename Tout>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w128,
                        const __grid_constant__ CUtensorMap map_w64, const __grid_constant__ CUtensorMap map_w32,
                        const LinearEpiArgs a, int act) {
+  constexpr bool PARTS = sizeof(Tout) == 4;
   extern __shared__ __align__(1024) uint8_t smem_linear[];
   const uint32_t base = smem_u32(smem_linear);
   const uint32_t bars = base + L_OFF_BAR;
@@ -269,10 +287,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     if (blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
   } else {
     const int pairs = static_cast<int>(gridDim.x) / 2, pair = static_cast<int>(blockIdx.x) / 2;
-    const int ln = tile_columns(T, a.N, pairs);
-    const int nt = (a.N + ln - 1) / ln;
-    const long long tiles = static_cast<long long>((T + 2 * LM - 1) / (2 * LM)) * nt;   // row tiles outermost
     const int kchunks = (a.K + LK - 1) / LK;
+    const int parts = PARTS ? (kchunks + L_PART - 1) / L_PART : 1;
+    const int ln = tile_columns(T, a.N, pairs, parts > 1 ? LN_PARTS : LN_MAX);
+    const int nt = (a.N + ln - 1) / ln;
+    const int mt = (T + 2 * LM - 1) / (2 * LM);
+    const long long tiles = static_cast<long long>(mt) * nt;
     const uint32_t stage_bytes = L_A_BYTES + static_cast<uint32_t>(ln / 2) * 128u;   // A rows, then W rows
     const uint32_t stages = L_RING_BYTES / stage_bytes;
     if (warp == 0) {
@@ -281,8 +301,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
       uint32_t s = 0, lap = 0;                           // ring position: stage and times round
       if (elect_one()) {
         for (long long t = pair; t < tiles && !bad; t += pairs) {
-          const int m0 = static_cast<int>(t / nt) * 2 * LM + static_cast<int>(rank) * LM;
-          const int n0 = static_cast<int>(t % nt) * ln + static_cast<int>(rank) * (ln / 2);
+          int m0, n0;
+          tile_at(t, mt, nt, m0, n0);
+          m0 = m0 * 2 * LM + static_cast<int>(rank) * LM;
+          n0 = n0 * ln + static_cast<int>(rank) * (ln / 2);
           for (int kc = 0; kc < kchunks; ++kc) {
             if (lap > 0 && !mbar_wait_or_abort(bar(LB_EMPTY, s), (lap - 1) & 1, abort_flag)) {
               bad = true;
@@ -306,31 +328,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, ln);
         const uint64_t da0 = sdesc(base, 16, 1024), dw0 = sdesc(base + L_A_BYTES, 16, 1024);
         uint32_t s = 0, lap = 0, i = 0;
-        for (long long t = pair; t < tiles && !bad; t += pairs, ++i) {
-          const uint32_t b = i & 1;
-          if (i >= 2 && !mbar_wait_or_abort(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag)) {
-            bad = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t acc = tmem + static_cast<uint32_t>(b) * LN_MAX;
-          for (int kc = 0; kc < kchunks; ++kc) {
-            if (!mbar_wait_or_abort(bar(LB_FULL, s), lap & 1, abort_flag)) {
+        for (long long t = pair; t < tiles && !bad; t += pairs) {
+          for (int part = 0; part < parts && !bad; ++part, ++i) {
+            const uint32_t b = i & 1;
+            if (i >= 2 && !mbar_wait_or_abort(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag)) {
               bad = true;
               break;
             }
             tc_fence_after();
-            const uint64_t off = s * (stage_bytes >> 4);
+            const uint32_t acc = tmem + b * LN_MAX;
+            const int k_from = part * L_PART, k_to = PARTS ? min(kchunks, k_from + L_PART) : kchunks;
+            for (int kc = k_from; kc < k_to; ++kc) {
+              if (!mbar_wait_or_abort(bar(LB_FULL, s), lap & 1, abort_flag)) {
+                bad = true;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t off = s * (stage_bytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < LK / 16; ++kk)
-              umma_f16_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
-            umma_commit_pair(bar(LB_EMPTY, s));
-            if (++s == stages) {
-              s = 0;
-              ++lap;
+              for (int kk = 0; kk < LK / 16; ++kk)
+                umma_f16_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, (kc > k_from || kk > 0) ? 1u : 0u);
+              umma_commit_pair(bar(LB_EMPTY, s));
+              if (++s == stages) {
+                s = 0;
+                ++lap;
+              }
             }
+            if (!bad) umma_commit_pair(bar(LB_ACC_FULL, b));
           }
-          if (!bad) umma_commit_pair(bar(LB_ACC_FULL, b));
         }
       }
       bad = __any_sync(0xffffffffu, bad);
@@ -350,17 +375,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         if (CPP > 32) bias1 = __ldg(a.bias + min(col0 + 32 + lane, a.N - 1));
       };
       for (long long t = pair; t < tiles; t += pairs, ++i) {
+        int m0, n0;
+        tile_at(t, mt, nt, m0, n0);
+        m0 = m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
+        n0 *= ln;
+        load_bias(n0 + half * CPP);
+        const int cols = m0 < T ? min(ln, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
+        // The tile's partial products, into registers: the sum of those before the last, fp32 outputs only.
+        constexpr int SUMS = PARTS ? LN_PARTS / CPP / 2 : 1;
+        float sum[SUMS][CPP];
+        for (int part = 0; part + 1 < parts && !bad; ++part, ++i) {
+          if (!mbar_wait_or_abort(bar(LB_ACC_FULL, i & 1), (i >> 1) & 1, abort_flag)) bad = true;
+          bad = __any_sync(0xffffffffu, bad);
+          if (bad) break;
+          tc_fence_after();
+          if constexpr (PARTS) {
+#pragma unroll
+            for (int y = 0; y < SUMS; ++y) {
+              if ((half + 2 * y) * CPP < cols) {
+                float v[CPP];
+                tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + (i & 1) * LN_MAX + (half + 2 * y) * CPP, v);
+#pragma unroll
+                for (int k = 0; k < CPP; ++k) sum[y][k] = part == 0 ? v[k] : sum[y][k] + v[k];
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty[i & 1]);
+        }
+        if (bad) break;
         const uint32_t b = i & 1;
-        load_bias(static_cast<int>(t % nt) * ln + half * CPP);
         if (!mbar_wait_or_abort(bar(LB_ACC_FULL, b), (i >> 1) & 1, abort_flag)) bad = true;
         bad = __any_sync(0xffffffffu, bad);
         if (bad) break;
         tc_fence_after();
-        const int m0 = static_cast<int>(t / nt) * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
-        const int n0 = static_cast<int>(t % nt) * ln;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(b) * LN_MAX;
         const int cc = lane & 7;                         // this lane's 16-byte chunk of a row piece
-        const int cols = m0 < T ? min(ln, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
 #pragma unroll 1
         for (int p = half; p * CPP < cols; p += 2) {
           const int col0 = n0 + p * CPP;
@@ -377,6 +428,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           float v[CPP];
 #pragma unroll
           for (int q = 0; q < CPP / 32; ++q) tmem_ld32(taddr + p * CPP + q * 32, v + q * 32);
+          if constexpr (PARTS) {
+            if (parts > 1) {
+#pragma unroll
+              for (int y = 0; y < SUMS; ++y) {
+                if (p == half + 2 * y) {
+#pragma unroll
+                  for (int k = 0; k < CPP; ++k) v[k] += sum[y][k];
+                }
+              }
+            }
+          }
           if ((p + 2) * CPP >= cols) {
             // This warp's share of the accumulator is in registers: the products of tile i + 2 may overwrite it.
             tc_fence_before();
@@ -454,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
 
 // ------------------------------------------------------------------ few rows
 
-constexpr int FEW_WARPS = 8;
+constexpr int FEW_WARPS = 8, FEW_PART = 4;
 // Steps of 32 in K in flight per warp: about 96 KB a CTA, two CTAs an SM.
 template <int NT> struct FewCfg {
   static constexpr int U = NT == 1 ? 8 : (NT == 2 ? 6 : 4);
@@ -500,9 +562,13 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   const Tin* x[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) x[t] = X + static_cast<size_t>(min(8 * t + g, T - 1)) * a.K;
-  float d[NT][4];
+  // Sums of the products, in parts of FEW_PART steps (see L_PART) added up in sum.
+  float d[NT][4], sum[NT][4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[t][j] = sum[t][j] = 0.f;
+  }
   // Steps of 32 in K, taken by the warps in turn.  Each lane copies its own
   // chunks into its own slots of shared memory and reads them back, U steps
   // later: no other lane waits for them, and the copies in flight need no
@@ -551,13 +617,23 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
       mma_16816(d[t], lo, vx[t].x, vx[t].y, Tin());
       mma_16816(d[t], hi, vx[t].z, vx[t].w, Tin());
     }
+    if (i % FEW_PART == FEW_PART - 1 || i + 1 == mine) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[t][j] += d[t][j];
+          d[t][j] = 0.f;
+        }
+      }
+    }
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    part[warp][g][8 * t + 2 * q] = d[t][0];
-    part[warp][g][8 * t + 2 * q + 1] = d[t][1];
-    part[warp][g + 8][8 * t + 2 * q] = d[t][2];
-    part[warp][g + 8][8 * t + 2 * q + 1] = d[t][3];
+    part[warp][g][8 * t + 2 * q] = sum[t][0];
+    part[warp][g][8 * t + 2 * q + 1] = sum[t][1];
+    part[warp][g + 8][8 * t + 2 * q] = sum[t][2];
+    part[warp][g + 8][8 * t + 2 * q + 1] = sum[t][3];
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 16 * NT * 8; e += 32 * FEW_WARPS) {

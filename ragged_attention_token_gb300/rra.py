@@ -322,51 +322,66 @@ def pipeline_mapped(keep_h, q_h, k_h, v_h, out_h, workspace, scale: float = 0.12
                                      _stream(stream)))
 
 
-def _typed(t, dtype, name: str, shape=None):
-    """Pointer of a contiguous tensor of the current device with this dtype (and shape), or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
+def _refuse(t, dtype, name: str, shape) -> None:
+    """Why `t` is not a tensor of this dtype and shape on the current device."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    p = _ptr(t)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return p
-
-
-def _rows(t, dtype, name: str, shape):
-    """(pointer, row stride) of a [rows, H, d] tensor whose rows may lie apart (a slice of a wider buffer)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    rows, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    raise ValueError(f"{name} is on {t.device}, not on the current device" if t.is_contiguous()
+                     else f"{name}: expected a contiguous tensor on the current device")
+
+
+def _typed(t, dtype, name: str, shape, dev: int):
+    """Pointer of a contiguous tensor with this dtype and shape (None: any) on device `dev`, or None.
+
+    The block operators' smallest calls take a few microseconds on the GPU, so
+    a tensor costs one line of attribute reads here."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or (shape is not None and t.shape != shape) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, name, shape)
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name: str, shape, dev: int):
+    """(pointer, row stride) of a [rows, H, d] tensor whose rows may lie apart (a slice of a wider buffer)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, name, shape)
+    rows, H, d = shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (H > 1 and s1 != d):
         raise ValueError(f"{name}: each row must be contiguous")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else H * d)
+    return t.data_ptr(), (s0 if rows > 1 else H * d)
 
 
-def _cu(cu_seqlens, B: int):
+def _cu(cu_seqlens, B: int, dev: int):
     if cu_seqlens.numel() < B + 1:
         raise ValueError(f"cu_seqlens has {cu_seqlens.numel()} entries, fewer than B + 1 = {B + 1}")
-    return _typed(cu_seqlens, torch.int32, "cu_seqlens")
+    return _typed(cu_seqlens, torch.int32, "cu_seqlens", None, dev)
+
+
+def _device(t) -> int:
+    """The current device, which `t` has to be on (-1, no device, for a host tensor)."""
+    return torch.cuda.current_device() if t.is_cuda else -2
+
+
+def _on(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def linear_epilogue(a, w, cu_seqlens, B: int, c, bias=None, act: int = ACT_NONE, residual=None, stream=None):
     """rra_linear_epilogue: c[t] = act(a[t] @ w.T + bias) + residual[t] for the T = cu_seqlens[B] packed rows."""
+    dev, dt, out = _device(a), a.dtype, c.dtype
     cap, K = a.shape
     N = w.shape[0]
-    _check(lib().rra_linear_epilogue(_typed(a, a.dtype, "a"), _typed(w, a.dtype, "w", (N, K)),
-                                     _typed(bias, torch.float32, "bias", (N,)),
-                                     _typed(residual, c.dtype, "residual", (cap, N)), _cu(cu_seqlens, B), B, cap, K, N,
-                                     _DTYPE[a.dtype], int(act), _typed(c, c.dtype, "c", (cap, N)), _DTYPE[c.dtype],
-                                     _stream(stream)))
+    _check(lib().rra_linear_epilogue(_typed(a, dt, "a", None, dev), _typed(w, dt, "w", (N, K), dev),
+                                     _typed(bias, torch.float32, "bias", (N,), dev),
+                                     _typed(residual, out, "residual", (cap, N), dev), _cu(cu_seqlens, B, dev), B, cap,
+                                     K, N, _DTYPE[dt], act, _typed(c, out, "c", (cap, N), dev), _DTYPE[out],
+                                     _on(stream, dev)))
 
 
 def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=None, q_weight=None, k_weight=None,
@@ -374,55 +389,61 @@ def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=Non
                  kv_rows=None, stream=None):
     """rra_qk_norm_rope: per-head RMS norm (with a weight) and rotation (with inv_freq) of q [cap, Hq, d] and
     k [cap, Hkv, d]; k_out / v_out take row t, or row kv_rows[t] of their own rows."""
+    dev, dt = _device(q), q.dtype
     cap, Hq, d = q.shape
     Hkv = k.shape[1]
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out go together")
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    dt = q.dtype
     out_rows = k_out.shape[0] if kv_rows is not None else cap
-    qp, qs = _rows(q, dt, "q", (cap, Hq, d))
-    kp, ks = _rows(k, dt, "k", (cap, Hkv, d))
-    vp, vs = _rows(v, dt, "v", (cap, Hkv, d)) if v is not None else (None, 0)
-    qo, qos = _rows(q_out, dt, "q_out", (cap, Hq, d))
-    ko, kos = _rows(k_out, dt, "k_out", (out_rows, Hkv, d))
-    vo, vos = _rows(v_out, dt, "v_out", (out_rows, Hkv, d)) if v_out is not None else (None, 0)
-    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
-    _check(lib().rra_qk_norm_rope(qp, qs, kp, ks, vp, vs, _typed(positions, torch.int32, "positions", (cap,)),
-                                  _cu(cu_seqlens, B), B, cap, Hq, Hkv, d, _DTYPE[dt],
-                                  _typed(q_weight, torch.float32, "q_weight", (d,)),
-                                  _typed(k_weight, torch.float32, "k_weight", (d,)), float(eps),
-                                  _typed(inv_freq, torch.float32, "inv_freq"), rot, int(bool(interleaved)),
-                                  float(rope_scale), qo, qos, ko, kos, vo, vos,
-                                  _typed(kv_rows, torch.int32, "kv_rows", (cap,)), out_rows, _stream(stream)))
+    qp, qs = _rows(q, dt, "q", (cap, Hq, d), dev)
+    kp, ks = _rows(k, dt, "k", (cap, Hkv, d), dev)
+    qo, qos = _rows(q_out, dt, "q_out", (cap, Hq, d), dev)
+    ko, kos = _rows(k_out, dt, "k_out", (out_rows, Hkv, d), dev)
+    vp = vo = None
+    vs = vos = rot = 0
+    if v is not None:
+        vp, vs = _rows(v, dt, "v", (cap, Hkv, d), dev)
+        vo, vos = _rows(v_out, dt, "v_out", (out_rows, Hkv, d), dev)
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+    f32 = torch.float32
+    _check(lib().rra_qk_norm_rope(qp, qs, kp, ks, vp, vs, _typed(positions, torch.int32, "positions", (cap,), dev),
+                                  _cu(cu_seqlens, B, dev), B, cap, Hq, Hkv, d, _DTYPE[dt],
+                                  _typed(q_weight, f32, "q_weight", (d,), dev),
+                                  _typed(k_weight, f32, "k_weight", (d,), dev), eps,
+                                  _typed(inv_freq, f32, "inv_freq", None, dev), rot, 1 if interleaved else 0,
+                                  rope_scale, qo, qos, ko, kos, vo, vos,
+                                  _typed(kv_rows, torch.int32, "kv_rows", (cap,), dev), out_rows, _on(stream, dev)))
 
 
 def attend_prompt(q, k, v, cu_seqlens, B: int, max_seqlen: int, o, scale: float, causal: bool = True, stream=None):
     """rra_attend_prompt: attention over B packed sequences, q [cap, Hq, d], k and v [cap, Hkv, d], o [cap, Hq, d]."""
-    cap, Hq, d = q.shape
+    dev, dt, shape = _device(q), q.dtype, q.shape
+    cap, Hq, d = shape
     Hkv = k.shape[1]
-    qp, qs = _rows(q, q.dtype, "q", (cap, Hq, d))
-    kp, ks = _rows(k, q.dtype, "k", (cap, Hkv, d))
-    vp, vs = _rows(v, q.dtype, "v", (cap, Hkv, d))
-    _check(lib().rra_attend_prompt(qp, qs, kp, ks, vp, vs, _cu(cu_seqlens, B), B, cap, int(max_seqlen), Hq, Hkv, d,
-                                   float(scale), int(bool(causal)), _DTYPE[q.dtype],
-                                   _typed(o, q.dtype, "o", (cap, Hq, d)), _stream(stream)))
+    qp, qs = _rows(q, dt, "q", shape, dev)
+    kp, ks = _rows(k, dt, "k", (cap, Hkv, d), dev)
+    vp, vs = _rows(v, dt, "v", (cap, Hkv, d), dev)
+    _check(lib().rra_attend_prompt(qp, qs, kp, ks, vp, vs, _cu(cu_seqlens, B, dev), B, cap, max_seqlen, Hq, Hkv, d,
+                                   scale, 1 if causal else 0, _DTYPE[dt], _typed(o, dt, "o", shape, dev),
+                                   _on(stream, dev)))
 
 
 def attend_cache(q, k_cache, v_cache, kv_len, o, scale: float, stream=None):
     """rra_attend_cache: attention of the nq newest tokens of each sequence, q [B*nq, Hq, d], over
     k_cache and v_cache [B, cap, Hkv, d], of which kv_len [B] rows are in use."""
-    B, cap, Hkv, d = k_cache.shape
-    if B == 0 or q.shape[0] % B:
-        raise ValueError(f"q has {q.shape[0]} rows, no multiple of the cache's {B} sequences")
-    Hq = q.shape[1]
-    qp, qs = _rows(q, q.dtype, "q", (q.shape[0], Hq, d))
-    _check(lib().rra_attend_cache(qp, qs, _typed(k_cache, q.dtype, "k_cache"),
-                                  _typed(v_cache, q.dtype, "v_cache", (B, cap, Hkv, d)),
-                                  _typed(kv_len, torch.int32, "kv_len", (B,)), B, q.shape[0] // B, cap, Hq, Hkv, d,
-                                  float(scale), _DTYPE[q.dtype], _typed(o, q.dtype, "o", (q.shape[0], Hq, d)),
-                                  _stream(stream)))
+    dev, dt, shape = _device(q), q.dtype, k_cache.shape
+    B, cap, Hkv, d = shape
+    rows, Hq, _ = q.shape
+    if B == 0 or rows % B:
+        raise ValueError(f"q has {rows} rows, no multiple of the cache's {B} sequences")
+    qp, qs = _rows(q, dt, "q", (rows, Hq, d), dev)
+    _check(lib().rra_attend_cache(qp, qs, _typed(k_cache, dt, "k_cache", None, dev),
+                                  _typed(v_cache, dt, "v_cache", shape, dev),
+                                  _typed(kv_len, torch.int32, "kv_len", (B,), dev), B, rows // B, cap, Hq, Hkv, d,
+                                  scale, _DTYPE[dt], _typed(o, dt, "o", (rows, Hq, d), dev), _on(stream, dev)))
 
 
 class Plan:
