@@ -5,9 +5,11 @@
 // the sequence otherwise): o_i = sum_j 2^(c s_ij - m) v_j / sum_j 2^(c s_ij - m),
 // s = <q_i, k_j>, c = scale log2 e, m a per-row reference.
 //
-// A unit is (sequence, query head, 256 query rows): two tiles of 128 rows (A
-// and B; one TMEM lane per row).  Keys stream in blocks of 128 that both tiles
-// use, so each K/V byte read from L2 serves 256 rows.  Per SM one CTA, its warps:
+// A unit is two tiles of 128 query rows (A and B; one TMEM lane per row) that read
+// the same keys: the same rows of two query heads of one key/value head, where
+// the heads of a group are even in number (both tiles then see the same blocks, and neither
+// ever works alone), else 256 rows of one head.  Keys stream in blocks of 128 that
+// both tiles use, so each K/V byte read from L2 serves 256 rows.  Per SM one CTA, its warps:
 //   warps 0-3 / 4-7  softmax of tile A / B, thread r owning row r: the block's
 //            scores from TMEM into registers, their maximum, the weights in
 //            base 2, written over the scores as 16-bit pairs;
@@ -62,9 +64,10 @@ constexpr float P_MOVE = 8.f;                // log2 units by which a maximum ma
 template <int D>
 struct PromptCfg {
   static constexpr uint32_t TILE = (D / 64) * P_SUB;              // a Q tile, a K block or a V block
-  static constexpr int SLOTS = D == 128 ? 5 : 8;                  // K/V ring: 160 / 128 KB
+  static constexpr int SLOTS = D == 128 ? 4 : 8;                  // K/V ring: 128 KB
   static constexpr uint32_t OFF_KV = 2 * TILE;
-  static constexpr uint32_t OFF_BAR = OFF_KV + SLOTS * TILE;
+  static constexpr uint32_t OFF_OUT = OFF_KV + SLOTS * TILE;      // output staging, 4 KB a softmax warp
+  static constexpr uint32_t OFF_BAR = OFF_OUT + P_SOFTMAX_WARPS * 4096;
   static constexpr uint32_t SMEM = OFF_BAR + 512;
   // TMEM columns: S of A and B, O of A and B; P over S, or, where there is
   // room (d = 64), beside it: then the next S need not wait for this P V, and
@@ -89,21 +92,32 @@ constexpr uint32_t P_DESC = 256;        // [2] x 32 bytes: s0, n, q0, h (q0 < 0:
 constexpr uint32_t PB_S_READ = 320;     // [2] the scores are in registers (one arrival per softmax warp of the tile)
 constexpr uint32_t PB_TAIL = 336;       // [2] a V block's tail to zero; zeroed
 
+// How units are made up: `heads` query heads and `rows` rows (2 and 128, or 1 and 256).
+struct UnitShape {
+  int heads, rows;
+};
+
 struct PromptUnit {
   int s0, n, q0, h;
-  __device__ bool has_b() const { return n - q0 > PT; }
+  // First row and head of tile w.
+  __device__ int row0(int w, const UnitShape& us) const { return us.heads == 2 ? q0 : q0 + w * PT; }
+  __device__ int head(int w, const UnitShape& us) const { return us.heads == 2 ? h + w : h; }
+  __device__ bool has_b(const UnitShape& us) const { return us.heads == 2 || n - q0 > PT; }
   // Key blocks of tile w.
-  __device__ int blocks(int w, int causal) const {
-    if (w == 1 && !has_b()) return 0;
+  __device__ int blocks(int w, const UnitShape& us, int causal) const {
+    if (w == 1 && !has_b(us)) return 0;
     const int all = (n + PT - 1) / PT;
-    return causal ? min(all, q0 / PT + 1 + w) : all;
+    return causal ? min(all, row0(w, us) / PT + 1) : all;
   }
 };
+
+__host__ __device__ inline UnitShape prompt_shape(int group) { return group % 2 == 0 ? UnitShape{2, PT} : UnitShape{1, 2 * PT}; }
 
 // Walks the non-empty units in order (query tile descending, sequence, head);
 // a warp's lanes look at 32 sequences at a time.  The walk only moves forward.
 struct UnitWalk {
-  int qt;              // current query tile (256 rows), from the highest
+  UnitShape us;
+  int qt;              // current query tile (us.rows rows), from the highest
   int b0;              // current group of 32 sequences
   long long before;    // non-empty units before the group (qt, b0)
   int lane;
@@ -127,16 +141,17 @@ struct UnitWalk {
     while (qt >= 0) {
       int s0 = 0, n = 0;
       const int rows = rows_of(a, b0 + lane, s0, n, record && qt == 0);
-      const unsigned live = __ballot_sync(0xffffffffu, rows > qt * 2 * PT);
-      const long long here = static_cast<long long>(__popc(live)) * a.Hq;
+      const unsigned live = __ballot_sync(0xffffffffu, rows > qt * us.rows);
+      const int per = a.Hq / us.heads;
+      const long long here = static_cast<long long>(__popc(live)) * per;
       if (target < before + here) {
-        const int k = static_cast<int>((target - before) / a.Hq);      // k-th live sequence of the group
+        const int k = static_cast<int>((target - before) / per);       // k-th live sequence of the group
         const bool mine = ((live >> lane) & 1u) && __popc(live & ((1u << lane) - 1u)) == k;
         const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         u.s0 = __shfl_sync(0xffffffffu, s0, src);
         u.n = __shfl_sync(0xffffffffu, n, src);
-        u.q0 = qt * 2 * PT;
-        u.h = static_cast<int>((target - before) % a.Hq);
+        u.q0 = qt * us.rows;
+        u.h = static_cast<int>((target - before) % per) * us.heads;
         return u;
       }
       before += here;
@@ -262,6 +277,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const UnitShape us = prompt_shape(a.Hq / a.Hkv);
   bool bad = false;
   // A bounded wait; every lane of the warp leaves with the same `bad`.
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -283,7 +299,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P_REGS_OTHER));
     if (warp == P_LOAD_WARP) {
       // ------------------------------------------------------------ loads
-      UnitWalk walk{(a.max_seqlen - 1) / (2 * PT), 0, 0, lane};
+      UnitWalk walk{us, (a.max_seqlen - 1) / us.rows, 0, 0, lane};
       const long long G = gridDim.x, c = blockIdx.x;
       uint32_t it = 0, nq[2] = {0, 0};
       const bool recorder = blockIdx.x == 0;
@@ -302,14 +318,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         __syncwarp();
         if (u.q0 < 0) break;
         const int hk = u.h / (a.Hq / a.Hkv);
-        const int nb = max(u.blocks(0, a.causal), u.blocks(1, a.causal));
+        const int nb = max(u.blocks(0, us, a.causal), u.blocks(1, us, a.causal));
         auto load_q = [&](int w) {
           if (nq[w] > 0 && !wait(bar(PB_Q_EMPTY, w), (nq[w] - 1) & 1)) return;
           ++nq[w];
           if (lane == 0) {
             mbar_expect_tx(bar(PB_Q_FULL, w), C::TILE);
             for (int g = 0; g < D / 64; ++g)
-              tma_load_3d(s_q(w) + g * P_SUB, &map_q, 64 * g, u.h, u.s0 + u.q0 + w * PT, bar(PB_Q_FULL, w));
+              tma_load_3d(s_q(w) + g * P_SUB, &map_q, 64 * g, u.head(w, us), u.s0 + u.row0(w, us), bar(PB_Q_FULL, w));
           }
           __syncwarp();
         };
@@ -326,7 +342,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         };
         load_q(0);
         if (!bad) load_kv(&map_k, 0);
-        if (!bad && u.has_b()) load_q(1);
+        if (!bad && u.has_b(us)) load_q(1);
         if (!bad) load_kv(&map_v, 0);
         for (int j = 1; j < nb && !bad; ++j) {
           load_kv(&map_k, j);
@@ -343,7 +359,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
         const PromptUnit u = read_unit(i);
         if (u.q0 < 0) break;
-        const int nb = max(u.blocks(0, a.causal), u.blocks(1, a.causal));
+        const int nb = max(u.blocks(0, us, a.causal), u.blocks(1, us, a.causal));
         const int keys = min(PT, u.n - (nb - 1) * PT), pad = -keys & 15;
         kv0 += 2 * static_cast<uint32_t>(nb);
         if (pad > 0) {
@@ -427,7 +443,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         int started = 0;                        // tiles (bits) whose first S was issued during the previous unit
         if (wait1(bar(PB_U_FULL, 0), 0)) u = read_unit(0);
         for (int i = 0; !bad && u.q0 >= 0; ++i) {
-          const int nba = u.blocks(0, a.causal), nbb = u.blocks(1, a.causal), nb = max(nba, nbb);
+          const int nba = u.blocks(0, us, a.causal), nbb = u.blocks(1, us, a.causal), nb = max(nba, nbb);
           PromptUnit next{0, 0, -2, 0};         // not read yet
           if (!(started & 1) && !next_s(0, 0, kv0, nba == 1)) break;
           if (nbb > 0 && !(started & 2) && !next_s(1, 0, kv0, nbb == 1)) break;
@@ -461,11 +477,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               if (next.q0 >= 0) {
                 const uint32_t k0 = kv0 + 2 * nb;
                 if (C::OWN_P || nbb > 0) {
-                  if (!next_s(0, 0, k0, next.blocks(0, a.causal) == 1)) break;
+                  if (!next_s(0, 0, k0, next.blocks(0, us, a.causal) == 1)) break;
                   started |= 1;
                 }
-                if (C::OWN_P && next.has_b()) {
-                  if (!next_s(1, 0, k0, next.blocks(1, a.causal) == 1)) break;
+                if (C::OWN_P && next.has_b(us)) {
+                  if (!next_s(1, 0, k0, next.blocks(1, us, a.causal) == 1)) break;
                   started |= 2;
                 }
               }
@@ -506,7 +522,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
       const PromptUnit u = read_unit(i);
       if (u.q0 < 0) break;
-      const int nbw = u.blocks(w, a.causal);
+      const int nbw = u.blocks(w, us, a.causal);
       float m_ref = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nbw; ++j) {
         if (!wait(bar(PB_S_FULL, w), count & 1)) break;
@@ -517,7 +533,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         } else {
           // The last block: the sequence's end, and the diagonal when causal.
           int lim = u.n - j * PT;
-          if (a.causal) lim = min(lim, u.q0 + w * PT + row - j * PT + 1);
+          if (a.causal) lim = min(lim, u.row0(w, us) + row - j * PT + 1);
           mx = prompt_scores<true>(tS, lim, s);
         }
         if constexpr (C::OWN_P) {
@@ -547,14 +563,37 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       if (nbw > 0) {
         if (!wait(bar(PB_PV_DONE, w), (count - 1) & 1)) break;
         tc_fence_after();
-        const int r = u.q0 + w * PT + row;
         const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
-        T* out = static_cast<T*>(a.o) + (static_cast<long long>(u.s0 + r) * a.Hq + u.h) * D;
+        // 64 columns at a time through the warp's 4 KB of staging (rows of
+        // 128 bytes, 16-byte chunks swizzled): whole row pieces leave, four to an
+        // instruction.  Stored straight from the registers, a row a lane, the
+        // epilogue held the tile for 4000 cycles.
+        const uint32_t stg = base + C::OFF_OUT + static_cast<uint32_t>(warp) * 4096u;
+        const int r0 = u.row0(w, us) + (warp & 3) * 32;
 #pragma unroll
-        for (int g = 0; g < D / 16; ++g) {
-          float o[16];
-          tmem_ld16(tO + 16 * g, o);
-          if (r < u.n) store16<T>(out + 16 * g, o, inv);
+        for (int g = 0; g < D / 64; ++g) {
+          float o[64];
+          tmem_ld32_nowait(tO + 64 * g, o);
+          tmem_ld32_nowait(tO + 64 * g + 32, o + 32);
+          tmem_wait_ld32(o);
+          tmem_wait_ld32(o + 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pack2<Tout2<T>>(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+            st_shared_v4(stg + lane * 128 + ((k ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + (lane >> 3), cc = lane & 7;
+            const uint4 v = ld_shared_v4(stg + rr * 128 + ((cc ^ (rr & 7)) << 4));
+            if (r0 + rr < u.n)
+              *reinterpret_cast<uint4*>(static_cast<T*>(a.o) +
+                                        (static_cast<long long>(u.s0 + r0 + rr) * a.Hq + u.head(w, us)) * D + 64 * g + 8 * cc) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       }
@@ -635,7 +674,8 @@ cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if ((e = make_map_rows(&mq, a.q, a.cap, a.Hq, D, a.q_stride, bf16)) != cudaSuccess) return e;
   if ((e = make_map_rows(&mk, a.k, a.cap, a.Hkv, D, a.k_stride, bf16)) != cudaSuccess) return e;
   if ((e = make_map_rows(&mv, a.v, a.cap, a.Hkv, D, a.v_stride, bf16)) != cudaSuccess) return e;
-  const long long units = static_cast<long long>(a.B) * a.Hq * ((a.max_seqlen + 2LL * PT - 1) / (2 * PT));
+  const UnitShape us = prompt_shape(a.Hq / a.Hkv);
+  const long long units = static_cast<long long>(a.B) * (a.Hq / us.heads) * ((a.max_seqlen - 1) / us.rows + 1);
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
