@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2)
   const int rb = unit % row_blocks, hk = unit / row_blocks % a.Hkv, b = unit / row_blocks / a.Hkv;
   const int G = a.Hq / a.Hkv;
   const int rows = min(C_ROWS, a.nq * G - rb * C_ROWS);            // row r: token r / G, head hk * G + r % G (r from rb * 16)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependent_launch();
   const int len = __ldg(a.kv_len + b);
   const bool valid = len >= 0 && len <= a.cap;
   if (!valid && split == 0 && rb == 0 && hk == 0 && threadIdx.x == 0)

@@ -6,10 +6,9 @@
 // s = <q_i, k_j>, c = scale log2 e, m a per-row reference.
 //
 // A unit is two tiles of 128 query rows (A and B; one TMEM lane per row) that read
-// the same keys: the same rows of two query heads of one key/value head, where
-// the heads of a group are even in number (both tiles then see the same blocks, and neither
-// ever works alone), else 256 rows of one head.  Keys stream in blocks of 128 that
-// both tiles use, so each K/V byte read from L2 serves 256 rows.  Per SM one CTA, its warps:
+// the same keys: 256 rows of one query head, or 128 rows of two heads of one
+// key/value head (prompt_shape).  Keys stream in blocks of 128 that both tiles
+// use, so each K/V byte read from L2 serves 256 rows.  Per SM one CTA, its warps:
 //   warps 0-3 / 4-7  softmax of tile A / B, thread r owning row r: the block's
 //            scores from TMEM into registers, their maximum, the weights in
 //            base 2, written over the scores as 16-bit pairs;
@@ -111,7 +110,15 @@ struct PromptUnit {
   }
 };
 
-__host__ __device__ inline UnitShape prompt_shape(int group) { return group % 2 == 0 ? UnitShape{2, PT} : UnitShape{1, 2 * PT}; }
+// Two heads of a group at the same rows where the group is even, d = 128 and the
+// prompts are not very long; else 256 rows of a head.  Two heads see the same blocks, so
+// neither tile ever works alone, which the last rows of many sequences would; two
+// successive tiles end one after the other, so that one's output leaves under the other's last
+// block.  32 / 8 heads, d = 128, causal, heads paired against rows: 16 x 1024 tokens 156 / 162 us,
+// 8 x 2048 243 / 249, eight of 1 to 4096 297 / 309, 8192 404 / 405, 16384 1500 / 1468; d = 64: 8192 293 / 279.
+__host__ __device__ inline UnitShape prompt_shape(int group, int d, int max_seqlen) {
+  return group % 2 == 0 && d == 128 && max_seqlen <= 8192 ? UnitShape{2, PT} : UnitShape{1, 2 * PT};
+}
 
 // Walks the non-empty units in order (query tile descending, sequence, head);
 // a warp's lanes look at 32 sequences at a time.  The walk only moves forward.
@@ -276,8 +283,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const UnitShape us = prompt_shape(a.Hq / a.Hkv);
+  dependent_launch();
+  const UnitShape us = prompt_shape(a.Hq / a.Hkv, D, a.max_seqlen);
   bool bad = false;
   // A bounded wait; every lane of the warp leaves with the same `bad`.
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -674,7 +681,7 @@ cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if ((e = make_map_rows(&mq, a.q, a.cap, a.Hq, D, a.q_stride, bf16)) != cudaSuccess) return e;
   if ((e = make_map_rows(&mk, a.k, a.cap, a.Hkv, D, a.k_stride, bf16)) != cudaSuccess) return e;
   if ((e = make_map_rows(&mv, a.v, a.cap, a.Hkv, D, a.v_stride, bf16)) != cudaSuccess) return e;
-  const UnitShape us = prompt_shape(a.Hq / a.Hkv);
+  const UnitShape us = prompt_shape(a.Hq / a.Hkv, D, a.max_seqlen);
   const long long units = static_cast<long long>(a.B) * (a.Hq / us.heads) * ((a.max_seqlen - 1) / us.rows + 1);
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   cudaLaunchConfig_t cfg = {};

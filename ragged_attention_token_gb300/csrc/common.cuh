@@ -174,6 +174,15 @@ cudaError_t launch_attend_small(const AttendArgs& a, rra_dtype in, rra_dtype out
 cudaError_t launch_attend_tc_fused_host(const AttendArgs& a, rra_dtype in, rra_dtype out, int num_sms,
                                         cudaStream_t stream);
 
+// For kernels launched as programmatic dependents: lets the next kernel of the
+// stream start its set-up as soon as every CTA of this one is running, then waits for the
+// kernels before it, which precedes every access to global memory.  Every CTA
+// calls it, so that no kernel completes before those it depends on.
+__device__ __forceinline__ void dependent_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Linear layer with its epilogue: c = act(a W^T + bias) + residual for the T = cu[B] rows.
 struct LinearEpiArgs {
   const int32_t* cu;

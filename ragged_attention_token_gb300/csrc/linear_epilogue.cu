@@ -280,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
   cluster_sync_all();                                    // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependent_launch();
   const int T = __ldg(a.cu + a.B);
   bool bad = false;
   if (T < 0 || T > a.cap) {
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   extern __shared__ __align__(16) uint8_t smem_few[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int n0 = static_cast<int>(blockIdx.x) * 16;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependent_launch();
   const int T = __ldg(a.cu + a.B);
   if (T < 0 || T > a.cap) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);

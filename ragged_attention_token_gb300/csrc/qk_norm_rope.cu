@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
   constexpr int LPH = D / 16, HPW = 32 / LPH;    // lanes of a head row, heads of a warp
   constexpr int U = RopeCfg<D>::UNROLL;
   const int lane = threadIdx.x & 31, p = lane % LPH, sub = lane / LPH;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependent_launch();
   const int rows_used = __ldg(a.cu + a.B);
   if (rows_used < 0 || rows_used > a.cap) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);

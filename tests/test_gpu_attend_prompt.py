@@ -54,6 +54,7 @@ def test_attend_prompt_heads_and_ragged_batches(Hq, Hkv, d, causal):
     _run([130, 0, 1, 257, 0, 64, 33, 0], Hq, Hkv, d, torch.bfloat16, causal, seed=Hq + d)
     _run([0, 0, 5], Hq, Hkv, d, torch.float16, causal, seed=1)
     _run([0, 1], Hq, Hkv, d, torch.float16, causal, seed=2, pad=0, max_seqlen=5000)
+    _run([130, 0, 1, 257, 33], Hq, Hkv, d, torch.bfloat16, causal, seed=3, max_seqlen=100000)
 
 
 @pytest.mark.parametrize("d", [64, 128])
