@@ -2,7 +2,7 @@
 // the T = cu_seqlens[B] packed rows (T read on the device), a [cap, K] and
 // W [N, K] both K-major.
 //
-// Two kernels.
+// Three kernels, by the rows that a can hold.
 //
 // linear_pair_kernel: tcgen05 on pairs of SMs (cta_group::2).  A pair owns a
 // tile of 256 rows x LN columns (LN = 256, 128 or 64): each CTA holds 128 of the rows
@@ -18,6 +18,13 @@
 // rounding, through 4 KB of shared memory per warp to whole 128-byte row
 // pieces.  LN is chosen on the device, where T is known: the width whose
 // rounds over the pairs take the least time.
+//
+// linear_mid_kernel: up to 128 rows (a token of each sequence of a large batch).  The
+// work is still the read of W, so W is the product's M operand (128 of its rows by all
+// rows of a): with a as the M operand its 128 rows are read from shared memory for
+// every 64 columns of W, 320 cycles for each 8 KB of W a pair streams (64 x 4096 x
+// 4096: 16.6 us, here 11.7).  A cluster of up to 8 CTAs shares K of a tile, TMA rings of 192 KB keeping W on
+// its way, and joins the sums through distributed shared memory.
 //
 // linear_few_kernel: a handful of rows (one token of each sequence).  The work
 // is one read of W, so W goes in 16-byte chunks into the mma.sync operands of the
@@ -514,6 +521,215 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L_TMEM_COLS) : "memory");
 }
 
+// ------------------------------------------------------------- medium rows
+
+constexpr int M_ROWS = 128;                              // most rows of a; W rows of a tile (TMEM lanes)
+constexpr int M_SPLIT = 8;                               // most CTAs of a cluster
+constexpr int M_THREADS = 192;                           // warp 0 loads, warp 1 products, warps 2-5 epilogue
+constexpr int M_MAX_STAGES = 9;
+constexpr uint32_t M_RING_BYTES = 192 * 1024;            // 6 to 9 stages; then the partial sums
+constexpr uint32_t M_W_BYTES = 128 * 128;
+constexpr uint32_t M_OFF_BAR = M_RING_BYTES;
+constexpr uint32_t MB_FULL = 0, MB_EMPTY = 8 * M_MAX_STAGES, MB_DONE = 16 * M_MAX_STAGES;
+constexpr uint32_t MW_TMEM = MB_DONE + 8, MW_ABORT = MW_TMEM + 4;
+constexpr uint32_t M_SMEM = M_OFF_BAR + 256;
+constexpr int M_PARTS = 4;                               // accumulators (128 columns each) that share K, see L_PART
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr));
+  return v;
+}
+
+// Four neighbouring outputs: + residual, one rounding.
+__device__ __forceinline__ void finish4(float* c, const float* residual, float4 v) {
+  if (residual != nullptr) {
+    const float4 r = *reinterpret_cast<const float4*>(residual);
+    v = make_float4(v.x + r.x, v.y + r.y, v.z + r.z, v.w + r.w);
+  }
+  *reinterpret_cast<float4*>(c) = v;
+}
+template <typename T>
+__device__ __forceinline__ void finish4(T* c, const T* residual, float4 v) {
+  float x[8] = {v.x, v.y, v.z, v.w, 0.f, 0.f, 0.f, 0.f};
+  if (residual != nullptr) {
+    const uint2 r = *reinterpret_cast<const uint2*>(residual);
+    Chunk<T>::add(x, make_uint4(r.x, r.y, 0u, 0u));
+  }
+  const uint4 w = Chunk<T>::pack(x);
+  *reinterpret_cast<uint2*>(c) = make_uint2(w.x, w.y);
+}
+
+// One cluster: 128 columns of c; its CTAs share K.  D[n, t] = sum_k W[n, k] a[t, k].
+template <typename Tin, typename Tout>
+__global__ void __launch_bounds__(M_THREADS, 1)
+    linear_mid_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                      const LinearEpiArgs a, int act, int splits) {
+  extern __shared__ __align__(1024) uint8_t smem_mid[];
+  const uint32_t base = smem_u32(smem_mid), bars = base + M_OFF_BAR;
+  auto bar = [&](uint32_t kind, uint32_t i) { return bars + kind + 8 * i; };
+  const uint32_t abort_flag = bars + MW_ABORT;
+  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_mid + M_OFF_BAR + MW_TMEM);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(blockIdx.x) % splits, n0 = static_cast<int>(blockIdx.x) / splits * 128;
+  if (warp == 1) {
+    tmem_alloc(bars + MW_TMEM, 128 * M_PARTS);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < M_MAX_STAGES; ++s) {
+      mbar_init(bar(MB_FULL, s), 1);
+      mbar_init(bar(MB_EMPTY, s), 1);
+    }
+    mbar_init(bar(MB_DONE, 0), 1);
+    st_shared_u32(abort_flag, 0u);
+    fence_barrier_init();
+    prefetch_tensormap(&map_a);
+    prefetch_tensormap(&map_w);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+  dependent_launch();
+  const int T = __ldg(a.cu + a.B);
+  const bool valid = T >= 0 && T <= a.cap;
+  if (!valid && blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
+  const int rows = valid ? T : 0, boxes = (rows + 31) / 32, cols = (rows + 15) & ~15;
+  const uint32_t stage_bytes = M_W_BYTES + static_cast<uint32_t>(boxes) * 4096u;
+  const uint32_t stages = min(static_cast<uint32_t>(M_MAX_STAGES), M_RING_BYTES / stage_bytes);
+  const int kchunks = (a.K + LK - 1) / LK;
+  const int k_from = static_cast<int>(static_cast<long long>(kchunks) * rank / splits);
+  const int k_to = rows > 0 ? static_cast<int>(static_cast<long long>(kchunks) * (rank + 1) / splits) : k_from;
+  const int parts = min(M_PARTS, max(1, (k_to - k_from + L_PART - 1) / L_PART));
+  const int per_part = (k_to - k_from + parts - 1) / parts;
+  bool bad = false;
+  if (warp == 0) {
+    // -------------------------------------------------------------- loads
+    if (elect_one()) {
+      uint32_t s = 0, lap = 0;
+      for (int kc = k_from; kc < k_to; ++kc) {
+        if (lap > 0 && !mbar_wait_or_abort(bar(MB_EMPTY, s), (lap - 1) & 1, abort_flag)) {
+          bad = true;
+          break;
+        }
+        const uint32_t dst = base + s * stage_bytes;
+        mbar_expect_tx(bar(MB_FULL, s), stage_bytes);
+        tma_load_2d(dst, &map_w, kc * LK, n0, bar(MB_FULL, s));          // rows past N, columns past K: zeros
+        for (int b = 0; b < boxes; ++b) tma_load_2d(dst + M_W_BYTES + b * 4096, &map_a, kc * LK, 32 * b, bar(MB_FULL, s));
+        if (++s == stages) {
+          s = 0;
+          ++lap;
+        }
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- products
+    if (elect_one()) {
+      const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 128, cols);
+      const uint64_t dw0 = sdesc(base, 16, 1024), dx0 = sdesc(base + M_W_BYTES, 16, 1024);
+      uint32_t s = 0, lap = 0;
+      for (int kc = k_from; kc < k_to; ++kc) {
+        if (!mbar_wait_or_abort(bar(MB_FULL, s), lap & 1, abort_flag)) {
+          bad = true;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t off = s * (stage_bytes >> 4);
+        const int part = (kc - k_from) / per_part;
+        const bool first = (kc - k_from) % per_part == 0;
+#pragma unroll
+        for (int kk = 0; kk < LK / 16; ++kk)
+          umma_f16(tmem + part * 128, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+        umma_commit(bar(MB_EMPTY, s));
+        if (++s == stages) {
+          s = 0;
+          ++lap;
+        }
+      }
+      if (!bad) umma_commit(bar(MB_DONE, 0));
+    }
+    bad = __any_sync(0xffffffffu, bad);
+  }
+  // Every warp: the products are done (and with them every copy has been read).
+  if (!bad && !mbar_wait_or_abort(bar(MB_DONE, 0), 0, abort_flag)) bad = true;
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && lane == 0) {
+    st_shared_u32(abort_flag, 1u);
+    record_error(a.err, RRA_DEVERR_WAIT_TIMEOUT);
+  }
+  __syncthreads();
+  const bool aborted = ld_shared_volatile_u32(abort_flag) != 0u;
+  if (aborted && tid == 0) {
+    const long long t0 = clock64();                      // copies and products still in flight land
+    while (clock64() - t0 < 2000000LL) {
+    }
+  }
+  __syncthreads();
+  // Partial sums [row of a][128] over the ring.
+  if (warp >= 2 && !aborted && k_from < k_to) {
+    tc_fence_after();
+    const int quad = warp & 3, n = quad * 32 + lane;
+    for (int j = 0; j < cols; j += 16) {
+      float v[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + j, v);
+      for (int p = 1; p < parts && p * per_part < k_to - k_from; ++p) {
+        float x[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + p * 128 + j, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st_shared_u32(base + static_cast<uint32_t>((j + i) * 128 + n) * 4u, __float_as_uint(v[i]));
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();
+  // Four neighbouring outputs a thread, the cluster's rows shared out, sums in rank order.
+  for (int e = rank * M_THREADS + tid; !aborted && e < rows * 32; e += splits * M_THREADS) {
+    const int t = e >> 5, c = 4 * (e & 31), n = n0 + c;
+    if (n >= a.N) continue;                              // N is a multiple of 8: whole quads
+    const uint32_t at = base + static_cast<uint32_t>(t * 128 + c) * 4u;
+    float4 y[M_SPLIT];
+#pragma unroll
+    for (int p = 0; p < M_SPLIT; ++p)
+      if (p < splits) y[p] = ld_cluster4(map_rank(at, static_cast<uint32_t>(p)));
+    float v[4] = {y[0].x, y[0].y, y[0].z, y[0].w};
+#pragma unroll
+    for (int p = 1; p < M_SPLIT; ++p) {
+      if (p < splits) {
+        v[0] += y[p].x;
+        v[1] += y[p].y;
+        v[2] += y[p].z;
+        v[3] += y[p].w;
+      }
+    }
+    if (a.bias != nullptr) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + n));
+      v[0] += b.x;
+      v[1] += b.y;
+      v[2] += b.z;
+      v[3] += b.w;
+    }
+    activate(v, act);
+    const size_t o = static_cast<size_t>(t) * a.N + n;
+    finish4(static_cast<Tout*>(a.c) + o, a.residual != nullptr ? static_cast<const Tout*>(a.residual) + o : nullptr,
+            make_float4(v[0], v[1], v[2], v[3]));
+  }
+  cluster_sync_all();                                    // no CTA leaves while another may still read its sums
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 128 * M_PARTS);
+}
+
 // ------------------------------------------------------------------ few rows
 
 constexpr int FEW_WARPS = 8, FEW_PART = 4;
@@ -733,6 +949,29 @@ cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, ma, mw[0], mw[1], mw[2], a, act);
 }
 
+template <typename Tin, typename Tout>
+cudaError_t launch_mid(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
+  if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
+  auto kernel = linear_mid_kernel<Tin, Tout>;
+  cudaError_t e = allow_smem<Tin, Tout, -1>(kernel, M_SMEM);
+  if (e != cudaSuccess) return e;
+  const bool bf16 = IsBf16<Tin>::value == 1;
+  CUtensorMap ma, mw;
+  if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, 32)) != cudaSuccess) return e;
+  if ((e = make_map_2d(&mw, a.w, a.N, a.K, bf16, 128)) != cudaSuccess) return e;
+  // K is split until the CTAs fill the SMs once, each keeping two chunks of 64 at least.
+  const int tiles = (a.N + 127) / 128, kchunks = (a.K + LK - 1) / LK;
+  int splits = 1;
+  while (splits < M_SPLIT && 2 * splits * tiles <= num_sms && kchunks >= 4 * splits) splits *= 2;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = dependent_config(attr, tiles * splits, M_THREADS, M_SMEM, stream);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mw, a, act, splits);
+}
+
 template <typename Tin, typename Tout, int NT>
 cudaError_t launch_few(const LinearEpiArgs& a, int act, cudaStream_t stream) {
   auto kernel = linear_few_kernel<Tin, Tout, NT>;
@@ -747,7 +986,7 @@ template <typename Tin, typename Tout>
 cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
   if (a.cap <= 16) return launch_few<Tin, Tout, 2>(a, act, stream);
-  if (a.cap <= 32) return launch_few<Tin, Tout, 4>(a, act, stream);
+  if (a.cap <= M_ROWS) return launch_mid<Tin, Tout>(a, act, num_sms, stream);
   return launch_pair<Tin, Tout>(a, act, num_sms, stream);
 }
 
