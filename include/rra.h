@@ -23,7 +23,8 @@
  *     tensors are [cap, H, d] with cap = B*N rows, of which the first T (the
  *     number of kept tokens, known only on the device) are written.
  *   - d must be 64 (else RRA_ERR_UNSUPPORTED); 1 <= N <= 1024; H >= 1;
- *     1 <= B <= 65535; B*N*H*d < 2^31.
+ *     1 <= B <= 65535; B*N*H*d < 2^31.  (The operators of a language model's block
+ *     further down state their own, wider limits.)
  *   - The keep mask is uint8 [B, N]; any nonzero byte keeps the token.
  *   - Input dtype is RRA_F16 or RRA_BF16; attention outputs may also be
  *     RRA_F32.  Softmax and both products accumulate in fp32.
@@ -552,7 +553,8 @@ RRA_API rra_status rra_attend_prompt(const void* q, long long q_stride, const vo
  * uses its first kv_len[b] rows (the new tokens' rows among them, the last
  * ones).  q [B*nq, Hq, d]; row b*nq + i attends to the keys
  * j < kv_len[b] - (nq - 1 - i); a row that sees no key gets zeros.
- * o [B*nq, Hq, d] contiguous, of the same dtype.  1 <= nq <= 64.  Rows from
+ * o [B*nq, Hq, d] contiguous, of the same dtype.  1 <= nq <= 64;
+ * B * Hkv * ceil(nq * (Hq / Hkv) / 16) < 2^27; 1e-30 <= scale <= 1e30.  Rows from
  * kv_len[b] on may hold anything; offsets into the cache are 64-bit.  A
  * kv_len[b] below 0 records RRA_DEVERR_SEQ_NEGATIVE, one above cap
  * RRA_DEVERR_SEQ_TOO_LONG; that sequence's rows are not written.  Products,
@@ -561,8 +563,8 @@ RRA_API rra_status rra_attend_cache(const void* q, long long q_stride, const voi
                                     const int32_t* kv_len, int B, int nq, int cap, int Hq, int Hkv, int d,
                                     float scale, rra_dtype dtype, void* o, void* stream);
 
-/* Bound, in clock cycles, on any one on-chip wait of the tcgen05 attention
- * kernels (0, the initial value: about one second).  A wait that runs out
+/* Bound, in clock cycles, on any one on-chip wait of the image attention's tcgen05
+ * kernels (0, the initial value: about one second, which every other kernel keeps).  A wait that runs out
  * makes the CTA record RRA_DEVERR_WAIT_TIMEOUT, give its own copies and
  * products a short grace period, release its tensor memory and return, its
  * output incomplete; the device stays usable.  A test hook for that failure

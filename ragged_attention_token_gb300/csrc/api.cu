@@ -827,6 +827,8 @@ rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cac
                             rra_dtype dtype, void* o, void* stream) {
   RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
   if (nq < 1 || nq > 64) return fail(RRA_ERR_UNSUPPORTED, "nq=%d outside [1, 64]", nq);
+  if (static_cast<long long>(B) * Hkv * ((nq * (Hq / Hkv) + 15) / 16) >= (1LL << 27))
+    return fail(RRA_ERR_UNSUPPORTED, "B * Hkv * ceil(nq * Hq / Hkv / 16) >= 2^27");
   if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
   RRA_CHECK_PTR(q);
   RRA_CHECK_PTR(k_cache);

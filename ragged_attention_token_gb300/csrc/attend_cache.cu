@@ -392,7 +392,6 @@ cudaError_t launch_d(const CacheArgs& a, int num_sms, cudaStream_t stream) {
     cluster *= 2;
     min_chunks = 32;
   }
-  if (units * cluster >= (1LL << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -129,6 +129,7 @@ struct UnitWalk {
   long long before;    // non-empty units before the group (qt, b0)
   int lane;
 
+  // Rows of sequence b, 0 for one that is not there or not valid (`record`: its code is recorded).
   __device__ int rows_of(const PromptArgs& a, int b, int& s0, int& n, bool record) const {
     if (b >= a.B) return 0;
     s0 = __ldg(a.cu + b);
@@ -142,12 +143,25 @@ struct UnitWalk {
     return n;
   }
 
+  // To the first tile of the longest sequence (max_seqlen may be far above it).
+  __device__ void start(const PromptArgs& a, bool record) {
+    int most = 0;
+    for (int b = lane; b < a.B; b += 32) {
+      int s0, n;
+      most = max(most, rows_of(a, b, s0, n, record));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    qt = (most + us.rows - 1) / us.rows - 1;
+    b0 = 0;
+    before = 0;
+  }
+
   // The unit with index `target` (not below any earlier target), or q0 < 0.
-  __device__ PromptUnit find(const PromptArgs& a, long long target, bool record) {
+  __device__ PromptUnit find(const PromptArgs& a, long long target) {
     PromptUnit u;
     while (qt >= 0) {
       int s0 = 0, n = 0;
-      const int rows = rows_of(a, b0 + lane, s0, n, record && qt == 0);
+      const int rows = rows_of(a, b0 + lane, s0, n, false);
       const unsigned live = __ballot_sync(0xffffffffu, rows > qt * us.rows);
       const int per = a.Hq / us.heads;
       const long long here = static_cast<long long>(__popc(live)) * per;
@@ -306,13 +320,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P_REGS_OTHER));
     if (warp == P_LOAD_WARP) {
       // ------------------------------------------------------------ loads
-      UnitWalk walk{us, (a.max_seqlen - 1) / us.rows, 0, 0, lane};
+      UnitWalk walk{us, 0, 0, 0, lane};
+      walk.start(a, blockIdx.x == 0);
       const long long G = gridDim.x, c = blockIdx.x;
       uint32_t it = 0, nq[2] = {0, 0};
-      const bool recorder = blockIdx.x == 0;
       for (int i = 0; !bad; ++i) {
         // Round i of G units, walked forwards and backwards in turn.
-        const PromptUnit u = walk.find(a, i * G + ((i & 1) ? G - 1 - c : c), recorder);
+        const PromptUnit u = walk.find(a, i * G + ((i & 1) ? G - 1 - c : c));
         if (i >= 2 && !wait(bar(PB_U_EMPTY, i & 1), ((i >> 1) - 1) & 1)) break;
         if (lane == 0) {
           const uint32_t d = bars + P_DESC + 32u * static_cast<uint32_t>(i & 1);

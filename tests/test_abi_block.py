@@ -79,7 +79,7 @@ CACHE = dict(q=0x1000000, qs=2048, k=0x2000000, v=0x3000000, lens=0x300, B=2, nq
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(d=256), UNS), (dict(nq=0), UNS), (dict(nq=65), UNS), (dict(B=0), INV), (dict(cap=0), INV), (dict(Hq=5), INV),
+    (dict(d=256), UNS), (dict(nq=0), UNS), (dict(nq=65), UNS), (dict(B=65535, Hkv=4096, Hq=4096, qs=4096 * 128), UNS), (dict(B=0), INV), (dict(cap=0), INV), (dict(Hq=5), INV),
     (dict(scale=NAN), INV), (dict(scale=-0.5), INV), (dict(dt=rra.RRA_F32), INV), (dict(q=None), INV),
     (dict(k=None), INV), (dict(v=None), INV), (dict(lens=None), INV), (dict(o=None), INV), (dict(lens=0x301), MIS),
     (dict(k=0x2000004), MIS), (dict(qs=2052), MIS), (dict(qs=2040), INV), (dict(o=0x2000000), INV),
@@ -101,5 +101,9 @@ def test_binding_refuses_before_the_library():
         rra.qk_norm_rope(z(4, 2, 64), z(4, 2, 64), None, cu, 1, z(4, 2, 64), z(4, 2, 64), torch.zeros(32))
     with pytest.raises(ValueError):                                         # 3 rows for 2 sequences
         rra.attend_cache(z(3, 2, 64), z(2, 8, 2, 64), z(2, 8, 2, 64), cu, z(3, 2, 64), scale=0.125)
+    with pytest.raises(ValueError):                                         # float weights
+        rra.linear_epilogue(z(4, 64), z(8, 64, dt=torch.float32), cu, 1, z(4, 8))
+    with pytest.raises(ValueError):                                         # fewer entries than B + 1
+        rra.linear_epilogue(z(4, 64), z(8, 64), cu, 2, z(4, 8))
     with pytest.raises(ValueError):                                         # c of another shape
         rra.linear_epilogue(z(4, 64), z(8, 64), cu, 1, z(4, 16))

@@ -147,6 +147,30 @@ def test_attend_prompt_rows_past_32_bits():
     assert bool((o[:cap - n] == 0).all())
 
 
+def test_attend_prompt_many_short_sequences_and_a_loose_bound():
+    """Thousands of sequences of 0 to 5 rows; a max_seqlen far above the longest costs nothing."""
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 6, 5000)
+    T, d, dtype = int(lens.sum()), 64, torch.float16
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn((T, 1, d), generator=g).to(dtype) for _ in range(3))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    outs = []
+    for S in (5, 1 << 30):
+        o = nan_fill(torch.empty((T, 1, d), dtype=dtype, device="cuda"))
+        rra.get_device_error(clear=True)
+        rra.attend_prompt(q.cuda(), k.cuda(), v.cuda(), cu, len(lens), S, o, scale=0.125)
+        torch.cuda.synchronize()
+        assert rra.get_device_error() == 0
+        outs.append(o.cpu())
+    assert torch.equal(outs[0], outs[1])
+    a = 0
+    for n in lens:
+        if n:
+            check_rows(outs[0][a:a + n], q[a:a + n], k[a:a + n], v[a:a + n], 0.125, np.arange(n), dtype)
+        a += n
+
+
 def test_attend_prompt_repeats_bit_for_bit_and_in_graphs():
     lens, Hq, Hkv, d = [700, 1, 130], 8, 2, 128
     T = sum(lens)

@@ -82,3 +82,92 @@ def test_prompt_then_one_token(Hq, Hkv, d, dtype):
     for got, rows in ((y_prompt, prompt_rows), (y_next, last_rows), (y_full, np.arange(len(x64)))):
         err = np.abs(got.cpu().double().numpy() - y[rows])
         assert np.all(err <= 24 * u * (1 + np.abs(y[rows]))), float(err.max())
+
+
+def _step(seed, cap, T, dtype=torch.bfloat16):
+    """A call of each operator on its own buffers, as a function, and the outputs it writes."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s, dt=dtype: torch.randn(s, generator=g, device="cuda").to(dt)
+    Hq, Hkv, d, C, R = 4, 2, 128, 320, 700
+    x, w, b = r(cap, C), r((Hq + 2 * Hkv) * d, C), r((Hq + 2 * Hkv) * d, dt=torch.float32)
+    res = r(cap, (Hq + 2 * Hkv) * d)
+    qkv = torch.zeros((cap, Hq + 2 * Hkv, d), dtype=dtype, device="cuda")
+    qo, ko = torch.zeros((cap, Hq, d), dtype=dtype, device="cuda"), torch.zeros((cap, Hkv, d), dtype=dtype, device="cuda")
+    o, oc = torch.zeros_like(qo), torch.zeros((2, Hq, d), dtype=dtype, device="cuda")
+    kc, vc = r(2, R, Hkv, d), r(2, R, Hkv, d)
+    cu = torch.tensor([0, T // 3, T], dtype=torch.int32, device="cuda")
+    pos = torch.arange(cap, dtype=torch.int32, device="cuda")
+    f = 10000.0 ** (-torch.arange(d // 2, device="cuda") / (d // 2))
+    lens = torch.tensor([R, 33], dtype=torch.int32, device="cuda")
+
+    def call(stream=None):
+        rra.linear_epilogue(x, w, cu, 2, qkv.view(cap, -1), bias=b, act=rra.ACT_SILU, residual=res, stream=stream)
+        rra.qk_norm_rope(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], pos, cu, 2, qo, ko, f, q_weight=f.new_ones(d), stream=stream)
+        rra.attend_prompt(qo, ko, qkv[:, Hq + Hkv:], cu, 2, T, o, scale=0.09, stream=stream)
+        rra.attend_cache(qo[:2], kc, vc, lens, oc, scale=0.09, stream=stream)
+
+    return call, [qkv, qo, ko, o, oc]
+
+
+@pytest.mark.parametrize("cap,T", [(3, 3), (16, 9), (100, 77), (400, 391)])
+def test_streams_graphs_and_calls_at_once(cap, T):
+    """Eager, on another stream (given, and current), captured and replayed, and two at once: the same bits every time."""
+    first, outs1 = _step(1, cap, T)
+    second, outs2 = _step(2, cap, T)
+    first(), second()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in outs1 + outs2]
+    assert all(bool(torch.isfinite(x.float()).all()) for x in want)
+
+    def check():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs1 + outs2))
+        for x in outs1 + outs2:
+            x.zero_()
+        torch.cuda.synchronize()
+
+    for x in outs1 + outs2:
+        x.zero_()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        first(s1)
+        with torch.cuda.stream(s2):
+            second()
+    check()
+    graphs = []
+    for call in (first, second):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            call()
+        graphs.append(gr)
+    for _ in range(5):
+        for gr, s in zip(graphs, (s1, s2)):
+            with torch.cuda.stream(s):
+                gr.replay()
+    check()
+    assert rra.get_device_error() == 0
+
+
+def test_errors_go_to_the_bound_word():
+    """A thread's bound error word takes the block operators' codes too, and the device's own word stays clear."""
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rra.get_device_error(clear=True)
+    rra.bind_error_word(word)
+    try:
+        a, w = torch.zeros((4, 64), device="cuda").bfloat16(), torch.zeros((16, 64), device="cuda").bfloat16()
+        c = torch.zeros((4, 16), device="cuda")
+        rra.linear_epilogue(a, w, torch.tensor([0, 5], dtype=torch.int32, device="cuda"), 1, c)
+        assert rra.read_error_word(word) == rra.DEVERR_INDEX_RANGE
+        x = torch.zeros((2, 1, 64), device="cuda").half()
+        rra.attend_prompt(x, x.clone(), x.clone(), torch.tensor([0, 2], dtype=torch.int32, device="cuda"), 1, 1,
+                          x.clone(), scale=0.1)
+        assert rra.read_error_word(word) == rra.DEVERR_SEQ_TOO_LONG
+        kv = torch.zeros((2, 3, 1, 64), device="cuda").half()
+        rra.attend_cache(x, kv, kv.clone(), torch.tensor([4, 1], dtype=torch.int32, device="cuda"), x.clone(), scale=0.1)
+        assert rra.read_error_word(word) == rra.DEVERR_SEQ_TOO_LONG
+        rra.qk_norm_rope(x, x.clone(), None, torch.tensor([0, 3], dtype=torch.int32, device="cuda"), 1, x.clone(), x.clone())
+        assert rra.read_error_word(word) == rra.DEVERR_INDEX_RANGE
+    finally:
+        rra.bind_error_word(None)
+    assert rra.get_device_error() == 0
