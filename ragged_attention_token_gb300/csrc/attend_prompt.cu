@@ -196,8 +196,16 @@ __device__ __forceinline__ float prompt_scores(uint32_t tS, int lim, float (&s)[
 #pragma unroll
   for (int g = 0; g < 4; ++g) tmem_wait_ld32(s + 32 * g);
   if constexpr (MASK) {
+    // By groups of 32 columns: those that every lane sees are left as they are
+    // (on the diagonal a warp's rows end in one group).
+    const int least = __reduce_min_sync(0xffffffffu, lim);
 #pragma unroll
-    for (int i = 0; i < PT; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+    for (int g = 0; g < 4; ++g) {
+      if (least < 32 * g + 32) {
+#pragma unroll
+        for (int i = 32 * g; i < 32 * g + 32; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+      }
+    }
   }
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -491,20 +499,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               }
             }
             if (j == nb - 1) {
-              // The next unit's first S goes ahead of this unit's last P V: tile A's when
-              // its products are all issued (P over S) or its scores read (own P).
+              // Tile A's products are all issued (P over S) or it has ended (own P): its
+              // first S of the next unit goes ahead of tile B's last P V.
               if (!wait1(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
               next = read_unit(i + 1);
-              if (next.q0 >= 0) {
-                const uint32_t k0 = kv0 + 2 * nb;
-                if (C::OWN_P || nbb > 0) {
-                  if (!next_s(0, 0, k0, next.blocks(0, us, a.causal) == 1)) break;
-                  started |= 1;
-                }
-                if (C::OWN_P && next.has_b(us)) {
-                  if (!next_s(1, 0, k0, next.blocks(1, us, a.causal) == 1)) break;
-                  started |= 2;
-                }
+              if (next.q0 >= 0 && (C::OWN_P ? nba < nbb : nbb > 0)) {
+                if (!next_s(0, 0, kv0 + 2 * nb, next.blocks(0, us, a.causal) == 1)) break;
+                started |= 1;
               }
             }
             if constexpr (C::OWN_P) {
