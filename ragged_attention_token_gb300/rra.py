@@ -377,11 +377,13 @@ def linear_epilogue(a, w, cu_seqlens, B: int, c, bias=None, act: int = ACT_NONE,
     dev, dt, out = _device(a), a.dtype, c.dtype
     cap, K = a.shape
     N = w.shape[0]
-    _check(lib().rra_linear_epilogue(_typed(a, dt, "a", None, dev), _typed(w, dt, "w", (N, K), dev),
-                                     _typed(bias, torch.float32, "bias", (N,), dev),
-                                     _typed(residual, out, "residual", (cap, N), dev), _cu(cu_seqlens, B, dev), B, cap,
-                                     K, N, _DTYPE[dt], int(act), _typed(c, out, "c", (cap, N), dev), _DTYPE[out],
-                                     _on(stream, dev)))
+    st = (_LIB or lib()).rra_linear_epilogue(_typed(a, dt, "a", None, dev), _typed(w, dt, "w", (N, K), dev),
+                                             _typed(bias, torch.float32, "bias", (N,), dev),
+                                             _typed(residual, out, "residual", (cap, N), dev), _cu(cu_seqlens, B, dev),
+                                             B, cap, K, N, _DTYPE[dt], int(act), _typed(c, out, "c", (cap, N), dev),
+                                             _DTYPE[out], _on(stream, dev))
+    if st:
+        _check(st)
 
 
 def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=None, q_weight=None, k_weight=None,
@@ -409,13 +411,17 @@ def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=Non
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
     f32 = torch.float32
-    _check(lib().rra_qk_norm_rope(qp, qs, kp, ks, vp, vs, _typed(positions, torch.int32, "positions", (cap,), dev),
-                                  _cu(cu_seqlens, B, dev), B, cap, Hq, Hkv, d, _DTYPE[dt],
-                                  _typed(q_weight, f32, "q_weight", (d,), dev),
-                                  _typed(k_weight, f32, "k_weight", (d,), dev), float(eps),
-                                  _typed(inv_freq, f32, "inv_freq", None, dev), rot, 1 if interleaved else 0,
-                                  float(rope_scale), qo, qos, ko, kos, vo, vos,
-                                  _typed(kv_rows, torch.int32, "kv_rows", (cap,), dev), out_rows, _on(stream, dev)))
+    st = (_LIB or lib()).rra_qk_norm_rope(qp, qs, kp, ks, vp, vs,
+                                          _typed(positions, torch.int32, "positions", (cap,), dev),
+                                          _cu(cu_seqlens, B, dev), B, cap, Hq, Hkv, d, _DTYPE[dt],
+                                          _typed(q_weight, f32, "q_weight", (d,), dev),
+                                          _typed(k_weight, f32, "k_weight", (d,), dev), float(eps),
+                                          _typed(inv_freq, f32, "inv_freq", None, dev), rot, 1 if interleaved else 0,
+                                          float(rope_scale), qo, qos, ko, kos, vo, vos,
+                                          _typed(kv_rows, torch.int32, "kv_rows", (cap,), dev), out_rows,
+                                          _on(stream, dev))
+    if st:
+        _check(st)
 
 
 def attend_prompt(q, k, v, cu_seqlens, B: int, max_seqlen: int, o, scale: float, causal: bool = True, stream=None):
@@ -426,9 +432,11 @@ def attend_prompt(q, k, v, cu_seqlens, B: int, max_seqlen: int, o, scale: float,
     qp, qs = _rows(q, dt, "q", shape, dev)
     kp, ks = _rows(k, dt, "k", (cap, Hkv, d), dev)
     vp, vs = _rows(v, dt, "v", (cap, Hkv, d), dev)
-    _check(lib().rra_attend_prompt(qp, qs, kp, ks, vp, vs, _cu(cu_seqlens, B, dev), B, cap, int(max_seqlen), Hq,
-                                   Hkv, d, float(scale), 1 if causal else 0, _DTYPE[dt], _typed(o, dt, "o", shape, dev),
-                                   _on(stream, dev)))
+    st = (_LIB or lib()).rra_attend_prompt(qp, qs, kp, ks, vp, vs, _cu(cu_seqlens, B, dev), B, cap, int(max_seqlen), Hq,
+                                           Hkv, d, float(scale), 1 if causal else 0, _DTYPE[dt],
+                                           _typed(o, dt, "o", shape, dev), _on(stream, dev))
+    if st:
+        _check(st)
 
 
 def attend_cache(q, k_cache, v_cache, kv_len, o, scale: float, stream=None):
@@ -440,10 +448,13 @@ def attend_cache(q, k_cache, v_cache, kv_len, o, scale: float, stream=None):
     if B == 0 or rows % B:
         raise ValueError(f"q has {rows} rows, no multiple of the cache's {B} sequences")
     qp, qs = _rows(q, dt, "q", (rows, Hq, d), dev)
-    _check(lib().rra_attend_cache(qp, qs, _typed(k_cache, dt, "k_cache", None, dev),
-                                  _typed(v_cache, dt, "v_cache", shape, dev),
-                                  _typed(kv_len, torch.int32, "kv_len", (B,), dev), B, rows // B, cap, Hq, Hkv, d,
-                                  float(scale), _DTYPE[dt], _typed(o, dt, "o", (rows, Hq, d), dev), _on(stream, dev)))
+    st = (_LIB or lib()).rra_attend_cache(qp, qs, _typed(k_cache, dt, "k_cache", None, dev),
+                                          _typed(v_cache, dt, "v_cache", shape, dev),
+                                          _typed(kv_len, torch.int32, "kv_len", (B,), dev), B, rows // B, cap, Hq, Hkv,
+                                          d, float(scale), _DTYPE[dt], _typed(o, dt, "o", (rows, Hq, d), dev),
+                                          _on(stream, dev))
+    if st:
+        _check(st)
 
 
 class Plan:
