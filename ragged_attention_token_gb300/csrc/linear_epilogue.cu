@@ -17,7 +17,7 @@
 // CTAs drain the last one: bias, activation and residual in fp32, one
 // rounding, through 4 KB of shared memory per warp to whole 128-byte row
 // pieces.  LN is chosen on the device, where T is known: the width whose
-// rounds over the pairs take the least time.
+// rounds over the pairs take the least time, the last round cut finer where it leaves pairs idle.
 //
 // linear_mid_kernel: up to 128 rows (a token of each sequence of a large batch).  The
 // work is still the read of W, so W is the product's M operand (128 of its rows by all
@@ -38,6 +38,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "tc_ptx.cuh"
 
 namespace rra {
@@ -105,12 +106,11 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// Arrival on a barrier of the pair's leader.  It publishes no memory (what it
-// orders are this warp's TMEM reads, by the tcgen05 fence before it), so it
-// releases at CTA scope: at cluster scope it waited for the warp's global
-// stores, 1800 cycles a tile.
+// Arrival on a barrier of the pair's leader.  It publishes no memory: what it
+// orders are this warp's TMEM reads, which have completed (tcgen05.wait::ld and the fence
+// before it), so it is relaxed: a release waited for the warp's global stores, 1800 cycles a tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
@@ -123,21 +123,33 @@ __device__ __forceinline__ float fast_rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float exp2f_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // 1 / (1 + e^-x): within a few 2^-23 of its value; 0 where e^-x overflows.
 __device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.f + __expf(-x)); }
-// x/2 (1 + erf(x / sqrt 2)) by Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26: erfc(z) = (a1 t + ... + a5 t^5) e^{-z^2}, t = 1 / (1 + p z), z >= 0,
-// within 1.5e-7.  For x < 0 the result is x erfc(|z|) / 2, with no cancellation.
-// (With erff the epilogue of a K = 384 layer took 2.5 times as long as its products.)
-__device__ __forceinline__ float act_gelu(float x) {
-  const float z = fabsf(x) * 0.70710678118654752f;
-  const float t = fast_rcp(fmaf(0.3275911f, z, 1.f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f) * t;
-  const float h = 0.5f * q * __expf(-z * z);   // erfc(|z|) / 2
-  return x * (x < 0.f ? h : 1.f - h);
+// x/2 (1 + erf(x / sqrt 2)) of two values, by Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26: erfc(z) = (a1 t + ... + a5 t^5) e^{-z^2}, t = 1 / (1 + p z),
+// z >= 0, within 1.5e-7.  With h = erfc(|x| / sqrt 2) / 2 the result is
+// x (1/2 + copysign(1/2 - h, x)).  (With erff the epilogue of a K = 384 layer took
+// 2.5 times as long as its products.)
+__device__ __forceinline__ void act_gelu2(float& x, float& y) {
+  auto both = [](float c) { return pair_f2(c, c); };
+  const uint64_t v = pair_f2(x, y), z = pair_f2(fabsf(x), fabsf(y));
+  const float2 d = halves_f2(fma_pair(z, both(0.3275911f * 0.70710678118654752f), both(1.f)));
+  const uint64_t t = pair_f2(fast_rcp(d.x), fast_rcp(d.y));
+  uint64_t q = fma_pair(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+  q = fma_pair(q, t, both(0.5f * 1.421413741f));
+  q = fma_pair(q, t, both(-0.5f * 0.284496736f));
+  q = fma_pair(q, t, both(0.5f * 0.254829592f));
+  q = mul_pair(q, t);
+  const float2 e = halves_f2(mul_pair(mul_pair(v, v), both(-0.5f * 1.4426950408889634f)));   // e^{-x^2 / 2} in base 2
+  const float2 r = halves_f2(fma_pair(q, pair_f2(-exp2f_approx(e.x), -exp2f_approx(e.y)), both(0.5f)));
+  const float2 o = halves_f2(mul_pair(v, pair_f2(0.5f + copysignf(r.x, x), 0.5f + copysignf(r.y, y))));
+  x = o.x;
+  y = o.y;
 }
 // (1 + tanh u) / 2 = 1 / (1 + e^{-2u}).
 __device__ __forceinline__ float act_gelu_tanh(float x) {
@@ -152,7 +164,7 @@ __device__ __forceinline__ void activate(float (&v)[E], int act) {
     for (int i = 0; i < E; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
   } else if (act == RRA_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = act_gelu(v[i]);
+    for (int i = 0; i < E; i += 2) act_gelu2(v[i], v[E > 1 ? i + 1 : i]);
   } else if (act == RRA_ACT_GELU_TANH) {
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = act_gelu_tanh(v[i]);
@@ -218,17 +230,34 @@ template <> struct Chunk<__half> {
   }
 };
 
-// Columns of a tile: the width whose rounds over `pairs` pairs cost least, a
-// tile of LN columns counted as LN + 64 (its A half is loaded whatever its width).
-__device__ __forceinline__ int tile_columns(int T, int N, int pairs, int most) {
-  const long long mt = (T + 2 * LM - 1) / (2 * LM);
-  int best = most;
-  long long cost = -1;
+// How the T x N outputs are cut into tiles: `wide` tiles of ln columns in whole
+// rounds over the pairs, then those of the last round cut f ways (1, 2 or 4) where that
+// round has pairs to spare.
+struct Tiling {
+  int ln, f, mt, nt;
+  long long wide, all;
+};
+
+// The cut whose rounds take least: a tile of n columns costs 64 + n/4, the shared
+// memory its products read (per 16-wide step 4 KB of a and n/64 KB of W).
+__device__ __forceinline__ Tiling make_tiling(int T, int N, int pairs, int most) {
+  Tiling best{};
+  long long least = -1;
+  const int mt = (T + 2 * LM - 1) / (2 * LM);
   for (int ln = most; ln >= 64; ln /= 2) {
-    const long long tiles = mt * ((N + ln - 1) / ln), c = (tiles + pairs - 1) / pairs * (ln + 64);
-    if (cost < 0 || c < cost) {
-      cost = c;
-      best = ln;
+    const int nt = (N + ln - 1) / ln;
+    const long long tiles = static_cast<long long>(mt) * nt, rounds = tiles / pairs, rem = tiles - rounds * pairs;
+    int f = 1;
+    while (rounds > 0 && ln / f > 64 && 2 * f * rem <= pairs) f *= 2;
+    const long long cost = rounds * (64 + ln / 4) + (rem > 0 ? 64 + ln / f / 4 : 0);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best.ln = ln;
+      best.f = f;
+      best.mt = mt;
+      best.nt = nt;
+      best.wide = f > 1 ? rounds * pairs : tiles;
+      best.all = best.wide + (tiles - best.wide) * f;
     }
   }
   return best;
@@ -245,6 +274,22 @@ __device__ __forceinline__ void tile_at(long long t, int mt, int nt, int& m, int
   const int r = static_cast<int>(t - static_cast<long long>(band) * L_BAND * nt);
   m = band * L_BAND + r % rows;
   n = r / rows;
+}
+
+// Piece t of the work: its row tile, first column and width (a width of 0: past N).
+__device__ __forceinline__ void piece_at(const Tiling& g, long long t, int N, int& m, int& n0, int& width) {
+  int n;
+  if (t < g.wide) {
+    tile_at(t, g.mt, g.nt, m, n);
+    n0 = n * g.ln;
+    width = g.ln;
+  } else {
+    const long long q = t - g.wide;
+    tile_at(g.wide + q / g.f, g.mt, g.nt, m, n);
+    width = g.ln / g.f;
+    n0 = n * g.ln + static_cast<int>(q % g.f) * width;
+    if (n0 >= N) width = 0;
+  }
 }
 
 template <typename Tin, typename Tout>
@@ -296,28 +341,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     const int pairs = static_cast<int>(gridDim.x) / 2, pair = static_cast<int>(blockIdx.x) / 2;
     const int kchunks = (a.K + LK - 1) / LK;
     const int parts = PARTS ? (kchunks + L_PART - 1) / L_PART : 1;
-    const int ln = tile_columns(T, a.N, pairs, parts > 1 ? LN_PARTS : LN_MAX);
-    const int nt = (a.N + ln - 1) / ln;
-    const int mt = (T + 2 * LM - 1) / (2 * LM);
-    const long long tiles = static_cast<long long>(mt) * nt;
-    const uint32_t stage_bytes = L_A_BYTES + static_cast<uint32_t>(ln / 2) * 128u;   // A rows, then W rows
+    const Tiling g = make_tiling(T, a.N, pairs, parts > 1 ? LN_PARTS : LN_MAX);
+    const uint32_t stage_bytes = L_A_BYTES + static_cast<uint32_t>(g.ln / 2) * 128u;   // A rows, then W rows
     const uint32_t stages = L_RING_BYTES / stage_bytes;
     if (warp == 0) {
       // ------------------------------------------------------------ loads
-      const CUtensorMap* mw = ln == 256 ? &map_w128 : (ln == 128 ? &map_w64 : &map_w32);
       uint32_t s = 0, lap = 0;                           // ring position: stage and times round
       if (elect_one()) {
-        for (long long t = pair; t < tiles && !bad; t += pairs) {
-          int m0, n0;
-          tile_at(t, mt, nt, m0, n0);
+        for (long long t = pair; t < g.all && !bad; t += pairs) {
+          int m0, n0, width;
+          piece_at(g, t, a.N, m0, n0, width);
+          if (width == 0) continue;
           m0 = m0 * 2 * LM + static_cast<int>(rank) * LM;
-          n0 = n0 * ln + static_cast<int>(rank) * (ln / 2);
+          n0 += static_cast<int>(rank) * (width / 2);
+          const CUtensorMap* mw = width == 256 ? &map_w128 : (width == 128 ? &map_w64 : &map_w32);
+          const uint32_t bytes = 2 * (L_A_BYTES + static_cast<uint32_t>(width / 2) * 128u);
           for (int kc = 0; kc < kchunks; ++kc) {
             if (lap > 0 && !mbar_wait_or_abort(bar(LB_EMPTY, s), (lap - 1) & 1, abort_flag)) {
               bad = true;
               break;
             }
-            if (rank == 0) mbar_expect_tx(bar(LB_FULL, s), 2 * stage_bytes);
+            if (rank == 0) mbar_expect_tx(bar(LB_FULL, s), bytes);
             const uint32_t full = map_rank(bar(LB_FULL, s), 0), dst = base + s * stage_bytes;
             tma_load_2d_pair(dst, &map_a, kc * LK, m0, full);       // rows past cap, columns past K: zeros
             tma_load_2d_pair(dst + L_A_BYTES, mw, kc * LK, n0, full);
@@ -332,10 +376,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     } else if (warp == 1) {
       // ------------------------------------------------------------ products
       if (rank == 0 && elect_one()) {
-        const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, ln);
         const uint64_t da0 = sdesc(base, 16, 1024), dw0 = sdesc(base + L_A_BYTES, 16, 1024);
         uint32_t s = 0, lap = 0, i = 0;
-        for (long long t = pair; t < tiles && !bad; t += pairs) {
+        for (long long t = pair; t < g.all && !bad; t += pairs) {
+          int m0, n0, width;
+          piece_at(g, t, a.N, m0, n0, width);
+          if (width == 0) continue;
+          const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, width);
           for (int part = 0; part < parts && !bad; ++part, ++i) {
             const uint32_t b = i & 1;
             if (i >= 2 && !mbar_wait_or_abort(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag)) {
@@ -381,13 +428,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         bias0 = __ldg(a.bias + min(col0 + lane, a.N - 1));
         if (CPP > 32) bias1 = __ldg(a.bias + min(col0 + 32 + lane, a.N - 1));
       };
-      for (long long t = pair; t < tiles; t += pairs, ++i) {
-        int m0, n0;
-        tile_at(t, mt, nt, m0, n0);
+      for (long long t = pair; t < g.all; t += pairs) {
+        int m0, n0, width;
+        piece_at(g, t, a.N, m0, n0, width);
+        if (width == 0) continue;
         m0 = m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
-        n0 *= ln;
         load_bias(n0 + half * CPP);
-        const int cols = m0 < T ? min(ln, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
+        const int cols = m0 < T ? min(width, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
         // The tile's partial products, into registers: the sum of those before the last, fp32 outputs only.
         constexpr int SUMS = PARTS ? LN_PARTS / CPP / 2 : 1;
         float sum[SUMS][CPP];
@@ -496,6 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           __syncwarp();                                  // read back before the next piece is written
         }
         if (half * CPP >= cols && lane == 0) mbar_arrive_cluster(acc_empty[b]);   // no piece for this warp
+        ++i;
       }
     }
     if (bad && lane == 0) {

@@ -20,6 +20,7 @@
 // fp32 below 2^24) again as two floats, minus the nearest integer.  The
 // remainder in [-1/2, 1/2] turns is good to about 2^-24 of a turn.
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace rra {
 namespace {
@@ -40,41 +41,20 @@ __device__ __forceinline__ void rotation(float pos, float f, float& c, float& s)
   sincospif(2.f * r, &s, &c);
 }
 
-// Pairs of fp32, one register pair (sm_100 and later compute both at once).
-__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint64_t to_f2(uint32_t w, __nv_bfloat16) {
-  return pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return pair_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 __device__ __forceinline__ uint64_t to_f2(uint32_t w, __half) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack_f2(f.x, f.y);
+  return pair_f2(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t from_f2(uint64_t v, __nv_bfloat16) {
-  const float2 f = unpack_f2(v);
+  const float2 f = halves_f2(v);
   const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 __device__ __forceinline__ uint32_t from_f2(uint64_t v, __half) {
-  const float2 f = unpack_f2(v);
+  const float2 f = halves_f2(v);
   const __half2 t = __floats2half2_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&t);
 }
@@ -104,8 +84,8 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
   const int c0 = INTERLEAVED || !turned ? 16 * p : 8 * p, c1 = INTERLEAVED || !turned ? c0 + 8 : c0 + half;
   auto partner_of = [](const uint64_t (&v)[8], int j) {
     if constexpr (!INTERLEAVED) return v[j ^ 4];
-    const float2 f = unpack_f2(v[j]);
-    return pack_f2(f.y, f.x);
+    const float2 f = halves_f2(v[j]);
+    return pair_f2(f.y, f.x);
   };
   const int full_q = (a.Hq + HPW - 1) / HPW, full_k = (a.Hkv + HPW - 1) / HPW;
   const int ends[3] = {full_q, full_q + full_k, full_q + 2 * full_k};
@@ -188,23 +168,23 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
       if (!turned) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          P[j] = pack_f2(w[2 * j], w[2 * j + 1]);
+          P[j] = pair_f2(w[2 * j], w[2 * j + 1]);
           Q[j] = 0ull;
         }
       } else if constexpr (INTERLEAVED) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          P[j] = pack_f2(w[2 * j] * cs[j], w[2 * j + 1] * cs[j]);
-          Q[j] = pack_f2(-w[2 * j + 1] * sn[j], w[2 * j] * sn[j]);
+          P[j] = pair_f2(w[2 * j] * cs[j], w[2 * j + 1] * cs[j]);
+          Q[j] = pair_f2(-w[2 * j + 1] * sn[j], w[2 * j] * sn[j]);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = 2 * j;
-          P[j] = pack_f2(w[e] * cs[e], w[e + 1] * cs[e + 1]);
-          Q[j] = pack_f2(-w[8 + e] * sn[e], -w[9 + e] * sn[e + 1]);
-          P[4 + j] = pack_f2(w[8 + e] * cs[e], w[9 + e] * cs[e + 1]);
-          Q[4 + j] = pack_f2(w[e] * sn[e], w[e + 1] * sn[e + 1]);
+          P[j] = pair_f2(w[e] * cs[e], w[e + 1] * cs[e + 1]);
+          Q[j] = pair_f2(-w[8 + e] * sn[e], -w[9 + e] * sn[e + 1]);
+          P[4 + j] = pair_f2(w[8 + e] * cs[e], w[9 + e] * cs[e + 1]);
+          Q[4 + j] = pair_f2(w[e] * sn[e], w[e + 1] * sn[e + 1]);
         }
       }
     };
@@ -217,28 +197,28 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = to_f2(w[j], T());
       if (normed) {
-        uint64_t s0 = mul_f2(v[0], v[0]), s1 = mul_f2(v[1], v[1]);
+        uint64_t s0 = mul_pair(v[0], v[0]), s1 = mul_pair(v[1], v[1]);
 #pragma unroll
         for (int j = 2; j < 8; j += 2) {
-          s0 = fma_f2(v[j], v[j], s0);
-          s1 = fma_f2(v[j + 1], v[j + 1], s1);
+          s0 = fma_pair(v[j], v[j], s0);
+          s1 = fma_pair(v[j + 1], v[j + 1], s1);
         }
-        const float2 a0 = unpack_f2(s0), a1 = unpack_f2(s1);
+        const float2 a0 = halves_f2(s0), a1 = halves_f2(s1);
         float ss = (a0.x + a0.y) + (a1.x + a1.y);
 #pragma unroll
         for (int m = LPH / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         inv = rsqrtf(fmaf(ss, 1.f / D, a.eps));
       }
-      const uint64_t inv2 = pack_f2(inv, inv);
+      const uint64_t inv2 = pair_f2(inv, inv);
       if (all_turned) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = from_f2(mul_f2(fma_f2(partner_of(v, j), Q[j], mul_f2(v[j], P[j])), inv2), T());
+        for (int j = 0; j < 8; ++j) y[j] = from_f2(mul_pair(fma_pair(partner_of(v, j), Q[j], mul_pair(v[j], P[j])), inv2), T());
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          uint64_t z = mul_f2(v[j], P[j]);
-          if (turned) z = fma_f2(partner_of(v, j), Q[j], z);   // (not 0 * partner: it may be infinite)
-          y[j] = from_f2(mul_f2(z, inv2), T());
+          uint64_t z = mul_pair(v[j], P[j]);
+          if (turned) z = fma_pair(partner_of(v, j), Q[j], z);   // (not 0 * partner: it may be infinite)
+          y[j] = from_f2(mul_pair(z, inv2), T());
         }
       }
       x[0] = make_uint4(y[0], y[1], y[2], y[3]);

@@ -91,7 +91,10 @@ def test_linear_epilogue_types(cap, T, act, dtype, out):
 
 
 @pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (2569, 2600, 768, 2304),
-                                       (300, 300, 72, 8200), (700, 1200, 1544, 4104)])
+                                       (300, 300, 72, 8200), (700, 1200, 1544, 4104),
+                                       # a last round of few tiles, cut in four, in two, and past the last column
+                                       (11000, 11000, 72, 512), (11000, 11008, 72, 264), (11000, 11000, 584, 264),
+                                       (7000, 7000, 136, 1000)])
 def test_linear_epilogue_exact_integers(T, cap, K, N):
     """Small whole numbers: every product and sum is exact, so the output is too."""
     g = torch.Generator(device="cuda").manual_seed(T + K)
