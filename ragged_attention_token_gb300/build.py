@@ -4,7 +4,7 @@
 
 Each .cu file in csrc/ compiles to an object in parallel; the objects link
 into ragged_attention_token_gb300/librra.so against the shared CUDA runtime.
-A rebuild happens only when a source or header is newer than the library.
+csrc/fastcall.cpp becomes the Python extension _rra_fast.so beside it.  A rebuild happens only when a source or header is newer than the library.
 """
 from __future__ import annotations
 
@@ -47,6 +47,37 @@ def _deps() -> list[str]:
     return deps
 
 
+# The block operators' argument marshalling in C++ (a Python extension against
+# torch's headers).  Without it rra.py marshals those calls itself.
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
+FAST_PATH = os.path.join(PKG_DIR, "_rra_fast.so")
+
+
+def _fast_up_to_date() -> bool:
+    deps = [FAST_SRC, os.path.join(INCLUDE, "rra.h"), os.path.abspath(__file__)]
+    return os.path.exists(FAST_PATH) and all(os.path.getmtime(p) <= os.path.getmtime(FAST_PATH) for p in deps)
+
+
+def build_fast(verbose: bool = False, force: bool = False) -> str:
+    """Compile the marshalling extension with the host compiler; returns its path."""
+    if not force and _fast_up_to_date():
+        return FAST_PATH
+    import sysconfig
+
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(troot, "include"),
+           os.path.join(troot, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = FAST_PATH + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[x for d in inc for x in ("-isystem", d)],
+          FAST_SRC, "-o", tmp, "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
+         verbose)
+    os.replace(tmp, FAST_PATH)
+    return FAST_PATH
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB_PATH):
         return False
@@ -65,6 +96,10 @@ def _run(cmd: list[str], verbose: bool) -> str:
 
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:
     """Compile every CUDA source for sm_103a and link librra.so; returns its path."""
+    try:
+        build_fast(verbose=verbose, force=force)
+    except (RuntimeError, OSError, ImportError) as e:
+        print(f"the marshalling extension was not built (calls are marshalled in Python): {e}", file=sys.stderr)
     if not force and up_to_date():
         return LIB_PATH
     nvcc = _nvcc()

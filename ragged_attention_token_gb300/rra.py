@@ -81,6 +81,8 @@ _SIGNATURES = {
 }
 
 _LIB = None
+# The block operators' marshalling in C++ (_rra_fast.so), or None: then this module marshals those calls.
+_FAST = None
 
 
 class RRAError(RuntimeError):
@@ -97,7 +99,7 @@ def header_symbols(path: str = HEADER_PATH) -> list[str]:
 
 def lib() -> ctypes.CDLL:
     """Load librra.so once (raises if it has not been built)."""
-    global _LIB
+    global _LIB, _FAST
     if _LIB is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
@@ -107,6 +109,14 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        try:
+            from . import _rra_fast
+            _rra_fast.bind(*(ctypes.cast(getattr(L, f), _vp).value
+                             for f in ("rra_linear_epilogue", "rra_qk_norm_rope", "rra_attend_prompt",
+                                       "rra_attend_cache")))
+            _FAST = _rra_fast
+        except ImportError:
+            pass
         _LIB = L
     return _LIB
 
@@ -337,8 +347,8 @@ def _refuse(t, dtype, name: str, shape) -> None:
 def _typed(t, dtype, name: str, shape, dev: int):
     """Pointer of a contiguous tensor with this dtype and shape (None: any) on device `dev`, or None.
 
-    The block operators' smallest calls take a few microseconds on the GPU, so
-    a tensor costs one line of attribute reads here."""
+    The block operators' smallest calls take a few microseconds on the GPU, so a tensor
+    costs one line of attribute reads here (and less in _rra_fast)."""
     if t is None:
         return None
     if t.dtype is not dtype or (shape is not None and t.shape != shape) or t.get_device() != dev or not t.is_contiguous():
@@ -372,8 +382,18 @@ def _on(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
+def _done(status: int) -> bool:
+    """Whether _FAST made the call (-1: it left it to this module); raises on an error status."""
+    if status > 0:
+        _check(status)
+    return status == 0
+
+
 def linear_epilogue(a, w, cu_seqlens, B: int, c, bias=None, act: int = ACT_NONE, residual=None, stream=None):
     """rra_linear_epilogue: c[t] = act(a[t] @ w.T + bias) + residual[t] for the T = cu_seqlens[B] packed rows."""
+    if _FAST is not None and _done(_FAST.linear(a, w, cu_seqlens, B, c, bias, act, residual,
+                                                None if stream is None else _stream(stream))):
+        return
     dev, dt, out = _device(a), a.dtype, c.dtype
     cap, K = a.shape
     N = w.shape[0]
@@ -391,6 +411,10 @@ def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=Non
                  kv_rows=None, stream=None):
     """rra_qk_norm_rope: per-head RMS norm (with a weight) and rotation (with inv_freq) of q [cap, Hq, d] and
     k [cap, Hkv, d]; k_out / v_out take row t, or row kv_rows[t] of their own rows."""
+    if _FAST is not None and _done(_FAST.rope(q, k, positions, cu_seqlens, B, q_out, k_out, inv_freq, q_weight, k_weight,
+                                              eps, 1 if interleaved else 0, rope_scale, v, v_out, kv_rows,
+                                              None if stream is None else _stream(stream))):
+        return
     dev, dt = _device(q), q.dtype
     cap, Hq, d = q.shape
     Hkv = k.shape[1]
@@ -426,6 +450,9 @@ def qk_norm_rope(q, k, positions, cu_seqlens, B: int, q_out, k_out, inv_freq=Non
 
 def attend_prompt(q, k, v, cu_seqlens, B: int, max_seqlen: int, o, scale: float, causal: bool = True, stream=None):
     """rra_attend_prompt: attention over B packed sequences, q [cap, Hq, d], k and v [cap, Hkv, d], o [cap, Hq, d]."""
+    if _FAST is not None and _done(_FAST.prompt(q, k, v, cu_seqlens, B, max_seqlen, o, scale, 1 if causal else 0,
+                                                None if stream is None else _stream(stream))):
+        return
     dev, dt, shape = _device(q), q.dtype, q.shape
     cap, Hq, d = shape
     Hkv = k.shape[1]
@@ -442,6 +469,9 @@ def attend_prompt(q, k, v, cu_seqlens, B: int, max_seqlen: int, o, scale: float,
 def attend_cache(q, k_cache, v_cache, kv_len, o, scale: float, stream=None):
     """rra_attend_cache: attention of the nq newest tokens of each sequence, q [B*nq, Hq, d], over
     k_cache and v_cache [B, cap, Hkv, d], of which kv_len [B] rows are in use."""
+    if _FAST is not None and _done(_FAST.cache(q, k_cache, v_cache, kv_len, o, scale,
+                                               None if stream is None else _stream(stream))):
+        return
     dev, dt, shape = _device(q), q.dtype, k_cache.shape
     B, cap, Hkv, d = shape
     rows, Hq, _ = q.shape

@@ -4,6 +4,10 @@ a cache, then one more token of every sequence against that cache.  The oracle c
 same weights; the one-token step must agree with the prompt pass over the longer prompts."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -171,3 +175,85 @@ def test_errors_go_to_the_bound_word():
     finally:
         rra.bind_error_word(None)
     assert rra.get_device_error() == 0
+
+
+def test_both_marshalling_paths_make_the_same_call(monkeypatch):
+    """The C++ marshalling and the binding's own: the same bits, and the same refusals."""
+    assert rra.lib() and rra._FAST is not None, "the marshalling extension was not built"
+    call, outs = _step(5, 40, 37)
+    call()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in outs]
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: rra.linear_epilogue(z(4, 64), z(8, 72), cu, 1, z(4, 8)),                               # K differs
+        lambda: rra.linear_epilogue(z(4, 64), z(8, 64), cu, 1, z(4, 8), bias=z(8)),                    # bias type
+        lambda: rra.linear_epilogue(z(64, 4).t(), z(8, 64), cu, 1, z(4, 8)),                           # not contiguous
+        lambda: rra.linear_epilogue(z(4, 64), z(8, 64), cu, 2, z(4, 8)),                               # cu too short
+        lambda: rra.linear_epilogue(z(4, 64), z(8, 64), cu.long(), 1, z(4, 8)),                        # cu type
+        lambda: rra.attend_prompt(z(4, 2, 64), z(4, 2, 64), z(4, 1, 64), cu, 1, 4, z(4, 2, 64), scale=0.1),
+        lambda: rra.attend_prompt(z(4, 64, 2).transpose(1, 2), z(4, 2, 64), z(4, 2, 64), cu, 1, 4, z(4, 2, 64), scale=0.1),
+        lambda: rra.attend_cache(z(3, 2, 64), z(2, 8, 2, 64), z(2, 8, 2, 64), cu, z(3, 2, 64), scale=0.1),
+        lambda: rra.qk_norm_rope(z(4, 2, 64), z(4, 2, 64), None, cu, 1, z(4, 2, 64), z(4, 2, 64).cpu()),
+        lambda: rra.qk_norm_rope(z(4, 2, 64), z(4, 2, 64), None, cu, 1, z(4, 2, 64), z(4, 2, 64), v=z(4, 2, 64)),
+        lambda: rra.linear_epilogue(z(4, 60), z(8, 60), cu, 1, z(4, 8)),                               # the library's own
+        lambda: rra.attend_prompt(z(4, 2, 64), z(4, 2, 64), z(4, 2, 64), cu, 1, 4, z(4, 2, 64), scale=-0.1),
+    ]
+    kinds = []
+    for f in bad:
+        with pytest.raises((ValueError, rra.RRAError)) as e:
+            f()
+        kinds.append((type(e.value), getattr(e.value, "status", None)))
+    monkeypatch.setattr(rra, "_FAST", None)
+    for x in outs:
+        x.zero_()
+    call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
+    for f, kind in zip(bad, kinds):
+        with pytest.raises((ValueError, rra.RRAError)) as e:
+            f()
+        assert (type(e.value), getattr(e.value, "status", None)) == kind
+
+
+def test_first_calls_may_be_captured():
+    """In a fresh process, the first call of every operator inside a stream capture (kernels and the rest of a
+    device's set-up load there), replayed against the eager result."""
+    code = """
+import torch
+from ragged_attention_token_gb300 import rra
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+x, w, q, kc = r(300, 64), r(128, 64), r(300, 4, 128), r(2, 700, 2, 128)
+cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+ln = torch.tensor([700, 5], dtype=torch.int32, device="cuda")
+c = [torch.zeros(n, 128, device="cuda").bfloat16() for n in (8, 100, 300)]
+qo, ko, o, oc = (torch.zeros_like(y) for y in (q, q[:, :2], q, q[:2]))
+cus = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (8, 100, 300)]
+ones = torch.ones(128, device="cuda")
+k2 = q[:, 2:].contiguous()
+x8, x100 = x[:8].contiguous(), x[:100].contiguous()
+q2 = q[:2].contiguous()
+def step():
+    for a, n, y in zip((x8, x100, x), cus, c):
+        rra.linear_epilogue(a, w, n, 1, y)
+    rra.qk_norm_rope(q, k2, None, cu, 1, qo, ko, q_weight=ones)
+    rra.attend_prompt(q, k2, k2, cu, 1, 300, o, scale=0.1)
+    rra.attend_cache(q2, kc, kc, ln, oc, scale=0.1)
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    step()
+gr.replay()
+torch.cuda.synchronize()
+got = [y.clone() for y in (*c, qo, ko, o, oc)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (*c, qo, ko, o, oc))) and bool(got[-1].float().abs().sum() > 0)
+assert rra.get_device_error() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stdout + out.stderr
