@@ -19,11 +19,11 @@
 // pieces.  LN is chosen on the device, where T is known: the width whose
 // rounds over the pairs take the least time, the last round cut finer where it leaves pairs idle.
 //
-// linear_mid_kernel: up to 128 rows (a token of each sequence of a large batch).  The
-// work is still the read of W, so W is the product's M operand (128 of its rows by all
+// linear_mid_kernel: 17 to 256 rows (a token of each sequence of a large batch), by the
+// rule at launch_typed.  The work is still the read of W, so W is the product's M operand (128 of its rows by all
 // rows of a): with a as the M operand its 128 rows are read from shared memory for
 // every 64 columns of W, 320 cycles for each 8 KB of W a pair streams (64 x 4096 x
-// 4096: 16.6 us, here 11.7).  A cluster of up to 8 CTAs shares K of a tile, TMA rings of 192 KB keeping W on
+// 4096: 16.6 us, here 11.2).  A cluster of up to 8 CTAs shares K of a tile, TMA rings of 192 KB keeping W on
 // its way, and joins the sums through distributed shared memory.
 //
 // linear_few_kernel: a handful of rows (one token of each sequence).  The work
@@ -235,12 +235,12 @@ template <> struct Chunk<__half> {
 // round has pairs to spare.
 struct Tiling {
   int ln, f, mt, nt;
-  long long wide, all;
+  long long wide, all, cost;
 };
 
 // The cut whose rounds take least: a tile of n columns costs 64 + n/4, the shared
 // memory its products read (per 16-wide step 4 KB of a and n/64 KB of W).
-__device__ __forceinline__ Tiling make_tiling(int T, int N, int pairs, int most) {
+__host__ __device__ __forceinline__ Tiling make_tiling(int T, int N, int pairs, int most) {
   Tiling best{};
   long long least = -1;
   const int mt = (T + 2 * LM - 1) / (2 * LM);
@@ -252,6 +252,7 @@ __device__ __forceinline__ Tiling make_tiling(int T, int N, int pairs, int most)
     const long long cost = rounds * (64 + ln / 4) + (rem > 0 ? 64 + ln / f / 4 : 0);
     if (least < 0 || cost < least) {
       least = cost;
+      best.cost = cost;
       best.ln = ln;
       best.f = f;
       best.mt = mt;
@@ -571,17 +572,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
 
 // ------------------------------------------------------------- medium rows
 
-constexpr int M_ROWS = 128;                              // most rows of a; W rows of a tile (TMEM lanes)
+constexpr int M_ROWS = 256;                              // most rows of a
 constexpr int M_SPLIT = 8;                               // most CTAs of a cluster
-constexpr int M_THREADS = 192;                           // warp 0 loads, warp 1 products, warps 2-5 epilogue
+constexpr int M_THREADS = 320;                           // warp 0 loads, warp 1 products, warps 2-9 epilogue
 constexpr int M_MAX_STAGES = 9;
-constexpr uint32_t M_RING_BYTES = 192 * 1024;            // 6 to 9 stages; then the partial sums
+constexpr uint32_t M_RING_BYTES = 192 * 1024;            // 4 to 9 stages; then the partial sums
 constexpr uint32_t M_W_BYTES = 128 * 128;
 constexpr uint32_t M_OFF_BAR = M_RING_BYTES;
 constexpr uint32_t MB_FULL = 0, MB_EMPTY = 8 * M_MAX_STAGES, MB_DONE = 16 * M_MAX_STAGES;
 constexpr uint32_t MW_TMEM = MB_DONE + 8, MW_ABORT = MW_TMEM + 4;
 constexpr uint32_t M_SMEM = M_OFF_BAR + 256;
-constexpr int M_PARTS = 4;                               // accumulators (128 columns each) that share K, see L_PART
+constexpr int M_TMEM_COLS = 512;                         // accumulators of 128 (or 256) columns that share K, see L_PART
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x) % splits, n0 = static_cast<int>(blockIdx.x) / splits * 128;
   if (warp == 1) {
-    tmem_alloc(bars + MW_TMEM, 128 * M_PARTS);
+    tmem_alloc(bars + MW_TMEM, M_TMEM_COLS);
     tmem_relinquish();
   }
   if (tid == 0) {
@@ -656,7 +657,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   const int kchunks = (a.K + LK - 1) / LK;
   const int k_from = static_cast<int>(static_cast<long long>(kchunks) * rank / splits);
   const int k_to = rows > 0 ? static_cast<int>(static_cast<long long>(kchunks) * (rank + 1) / splits) : k_from;
-  const int parts = min(M_PARTS, max(1, (k_to - k_from + L_PART - 1) / L_PART));
+  const int part_cols = cols > 128 ? 256 : 128;
+  const int parts = min(M_TMEM_COLS / part_cols, max(1, (k_to - k_from + L_PART - 1) / L_PART));
   const int per_part = (k_to - k_from + parts - 1) / parts;
   bool bad = false;
   if (warp == 0) {
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         const bool first = (kc - k_from) % per_part == 0;
 #pragma unroll
         for (int kk = 0; kk < LK / 16; ++kk)
-          umma_f16(tmem + part * 128, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+          umma_f16(tmem + part * part_cols, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
         umma_commit(bar(MB_EMPTY, s));
         if (++s == stages) {
           s = 0;
@@ -726,12 +728,12 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   if (warp >= 2 && !aborted && k_from < k_to) {
     tc_fence_after();
     const int quad = warp & 3, n = quad * 32 + lane;
-    for (int j = 0; j < cols; j += 16) {
+    for (int j = ((warp - 2) >> 2) * 16; j < cols; j += 32) {
       float v[16];
       tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + j, v);
       for (int p = 1; p < parts && p * per_part < k_to - k_from; ++p) {
         float x[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + p * 128 + j, x);
+        tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + p * part_cols + j, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] += x[i];
       }
@@ -742,40 +744,49 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   }
   __syncthreads();
   cluster_sync_all();
-  // Four neighbouring outputs a thread, the cluster's rows shared out, sums in rank order.
-  for (int e = rank * M_THREADS + tid; !aborted && e < rows * 32; e += splits * M_THREADS) {
-    const int t = e >> 5, c = 4 * (e & 31), n = n0 + c;
-    if (n >= a.N) continue;                              // N is a multiple of 8: whole quads
-    const uint32_t at = base + static_cast<uint32_t>(t * 128 + c) * 4u;
-    float4 y[M_SPLIT];
+  // Four neighbouring outputs a thread, two such at a time, the cluster's rows
+  // shared out, sums in rank order.
+  const int step = splits * M_THREADS;
+  for (int e0 = rank * M_THREADS + tid; !aborted && e0 < rows * 32; e0 += 2 * step) {
+    float4 y[2][M_SPLIT];
 #pragma unroll
-    for (int p = 0; p < M_SPLIT; ++p)
-      if (p < splits) y[p] = ld_cluster4(map_rank(at, static_cast<uint32_t>(p)));
-    float v[4] = {y[0].x, y[0].y, y[0].z, y[0].w};
+    for (int u = 0; u < 2; ++u) {
+      const int e = min(e0 + u * step, rows * 32 - 1);
+      const uint32_t at = base + static_cast<uint32_t>((e >> 5) * 128 + 4 * (e & 31)) * 4u;
 #pragma unroll
-    for (int p = 1; p < M_SPLIT; ++p) {
-      if (p < splits) {
-        v[0] += y[p].x;
-        v[1] += y[p].y;
-        v[2] += y[p].z;
-        v[3] += y[p].w;
+      for (int p = 0; p < M_SPLIT; ++p)
+        if (p < splits) y[u][p] = ld_cluster4(map_rank(at, static_cast<uint32_t>(p)));
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = e0 + u * step, t = e >> 5, n = n0 + 4 * (e & 31);
+      if (e >= rows * 32 || n >= a.N) continue;          // N is a multiple of 8: whole quads
+      float v[4] = {y[u][0].x, y[u][0].y, y[u][0].z, y[u][0].w};
+#pragma unroll
+      for (int p = 1; p < M_SPLIT; ++p) {
+        if (p < splits) {
+          v[0] += y[u][p].x;
+          v[1] += y[u][p].y;
+          v[2] += y[u][p].z;
+          v[3] += y[u][p].w;
+        }
       }
+      if (a.bias != nullptr) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + n));
+        v[0] += b.x;
+        v[1] += b.y;
+        v[2] += b.z;
+        v[3] += b.w;
+      }
+      activate(v, act);
+      const size_t o = static_cast<size_t>(t) * a.N + n;
+      finish4(static_cast<Tout*>(a.c) + o, a.residual != nullptr ? static_cast<const Tout*>(a.residual) + o : nullptr,
+              make_float4(v[0], v[1], v[2], v[3]));
     }
-    if (a.bias != nullptr) {
-      const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + n));
-      v[0] += b.x;
-      v[1] += b.y;
-      v[2] += b.z;
-      v[3] += b.w;
-    }
-    activate(v, act);
-    const size_t o = static_cast<size_t>(t) * a.N + n;
-    finish4(static_cast<Tout*>(a.c) + o, a.residual != nullptr ? static_cast<const Tout*>(a.residual) + o : nullptr,
-            make_float4(v[0], v[1], v[2], v[3]));
   }
   cluster_sync_all();                                    // no CTA leaves while another may still read its sums
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 128 * M_PARTS);
+  if (warp == 1) tmem_dealloc(tmem, M_TMEM_COLS);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -997,8 +1008,16 @@ cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, ma, mw[0], mw[1], mw[2], a, act);
 }
 
+// CTAs that share K of a tile: K is split until they fill the SMs once, each keeping two chunks of 64 at least.
+int mid_splits(const LinearEpiArgs& a, int num_sms) {
+  const int tiles = (a.N + 127) / 128, kchunks = (a.K + LK - 1) / LK;
+  int splits = 1;
+  while (splits < M_SPLIT && 2 * splits * tiles <= num_sms && kchunks >= 4 * splits) splits *= 2;
+  return splits;
+}
+
 template <typename Tin, typename Tout>
-cudaError_t launch_mid(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
+cudaError_t launch_mid(const LinearEpiArgs& a, int act, int splits, cudaStream_t stream) {
   if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
   auto kernel = linear_mid_kernel<Tin, Tout>;
   cudaError_t e = allow_smem<Tin, Tout, -1>(kernel, M_SMEM);
@@ -1007,12 +1026,8 @@ cudaError_t launch_mid(const LinearEpiArgs& a, int act, int num_sms, cudaStream_
   CUtensorMap ma, mw;
   if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, 32)) != cudaSuccess) return e;
   if ((e = make_map_2d(&mw, a.w, a.N, a.K, bf16, 128)) != cudaSuccess) return e;
-  // K is split until the CTAs fill the SMs once, each keeping two chunks of 64 at least.
-  const int tiles = (a.N + 127) / 128, kchunks = (a.K + LK - 1) / LK;
-  int splits = 1;
-  while (splits < M_SPLIT && 2 * splits * tiles <= num_sms && kchunks >= 4 * splits) splits *= 2;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = dependent_config(attr, tiles * splits, M_THREADS, M_SMEM, stream);
+  cudaLaunchConfig_t cfg = dependent_config(attr, (a.N + 127) / 128 * splits, M_THREADS, M_SMEM, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -1034,7 +1049,17 @@ template <typename Tin, typename Tout>
 cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
   if (a.cap <= 16) return launch_few<Tin, Tout, 2>(a, act, stream);
-  if (a.cap <= M_ROWS) return launch_mid<Tin, Tout>(a, act, num_sms, stream);
+  if (a.cap <= M_ROWS) {
+    // The way whose products read less shared memory in turn, in cycles: 64 + rows/2 a step of 16 in K with W
+    // as the M operand, make_tiling's cost with a; joining the sums takes about 36 a row there.  4096 x 4096: 64
+    // rows 11.2 against 16.6 us, 200 rows 15.6 / 16.1, 256 rows 17.4 / 16.3; 768 x 2304: 64 rows 5.8 / 6.1, 128
+    // rows 7.0 / 6.2; 16384 x 4096: 256 rows 36.7 / 48.3.
+    const int splits = mid_splits(a, num_sms), kchunks = (a.K + LK - 1) / LK, tiles = (a.N + 127) / 128;
+    const long long here = 4LL * ((kchunks + splits - 1) / splits) * (64 + a.cap / 2) *
+                               ((static_cast<long long>(tiles) * splits + num_sms - 1) / num_sms) + 36 * a.cap;
+    const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * kchunks;
+    if (here < there) return launch_mid<Tin, Tout>(a, act, splits, stream);
+  }
   return launch_pair<Tin, Tout>(a, act, num_sms, stream);
 }
 

@@ -71,7 +71,7 @@ def test_linear_epilogue_sizes(T, K, N):
     _run(T, 320, K, N, torch.bfloat16, torch.float32, "gelu", True, True, seed=T * 31 + K + N)
 
 
-@pytest.mark.parametrize("cap", [1, 3, 8, 16, 24, 32, 48, 64])
+@pytest.mark.parametrize("cap", [1, 3, 8, 16, 24, 32, 48, 64, 129, 200, 256, 257])
 @pytest.mark.parametrize("K,N", [(8, 8), (72, 24), (768, 384), (4096, 512), (1032, 1000)])
 def test_linear_epilogue_few_rows(cap, K, N):
     """The serving form: a handful of rows, all in use and not."""
@@ -91,7 +91,8 @@ def test_linear_epilogue_types(cap, T, act, dtype, out):
 
 
 @pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (2569, 2600, 768, 2304),
-                                       (300, 300, 72, 8200), (700, 1200, 1544, 4104),
+                                       (300, 300, 72, 8200), (700, 1200, 1544, 4104), (200, 256, 8200, 1032),
+                                       (161, 200, 4104, 4104), (200, 200, 1032, 16392),
                                        # a last round of few tiles, cut in four, in two, and past the last column
                                        (11000, 11000, 72, 512), (11000, 11008, 72, 264), (11000, 11000, 584, 264),
                                        (7000, 7000, 136, 1000)])
