@@ -823,20 +823,17 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int n0 = static_cast<int>(blockIdx.x) * 16;
   dependent_launch();
+  // Needed at the end only: rows of a from T to cap are multiplied too (each gives its
+  // own outputs, which are not stored), so that no copy waits for T.
   const int T = __ldg(a.cu + a.B);
-  if (T < 0 || T > a.cap) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
-    return;
-  }
-  if (T == 0) return;
   const Tin* W = static_cast<const Tin*>(a.w);
   const Tin* X = static_cast<const Tin*>(a.a);
-  // Rows past N repeat the last one, rows past T are zeros: their results are not stored.
+  // Rows past N repeat the last one, rows past cap are zeros: their results are not stored.
   const Tin* w0 = W + static_cast<size_t>(min(n0 + g, a.N - 1)) * a.K;
   const Tin* w1 = W + static_cast<size_t>(min(n0 + g + 8, a.N - 1)) * a.K;
   const Tin* x[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = X + static_cast<size_t>(min(8 * t + g, T - 1)) * a.K;
+  for (int t = 0; t < NT; ++t) x[t] = X + static_cast<size_t>(min(8 * t + g, a.cap - 1)) * a.K;
   // Sums of the products, in parts of FEW_PART steps (see L_PART) added up in sum.
   float d[NT][4], sum[NT][4];
 #pragma unroll
@@ -867,7 +864,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
     cp_async16(chunk(u, 1), w1 + k);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      if (8 * t + g < T) cp_async16(chunk(u, 2 + t), x[t] + k);
+      if (8 * t + g < a.cap) cp_async16(chunk(u, 2 + t), x[t] + k);
   };
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -882,7 +879,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
     const uint4 va = in ? ld_shared_v4(chunk(u, 0)) : z, vb = in ? ld_shared_v4(chunk(u, 1)) : z;
     uint4 vx[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) vx[t] = in && 8 * t + g < T ? ld_shared_v4(chunk(u, 2 + t)) : z;
+    for (int t = 0; t < NT; ++t) vx[t] = in && 8 * t + g < a.cap ? ld_shared_v4(chunk(u, 2 + t)) : z;
     if (i + U < mine) fetch(i + U, u);
     cp_async_commit();
     if (++u == U) u = 0;
@@ -911,6 +908,10 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
     part[warp][g + 8][8 * t + 2 * q + 1] = sum[t][3];
   }
   __syncthreads();
+  if (T < 0 || T > a.cap) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
+    return;
+  }
   for (int e = threadIdx.x; e < 16 * NT * 8; e += 32 * FEW_WARPS) {
     const int j = e & 15, t = e >> 4, n = n0 + j;
     if (t >= T || n >= a.N) continue;
