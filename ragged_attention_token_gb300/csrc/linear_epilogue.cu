@@ -19,8 +19,8 @@
 // pieces.  LN is chosen on the device, where T is known: the width whose
 // rounds over the pairs take the least time, the last round cut finer where it leaves pairs idle.
 //
-// linear_mid_kernel: 17 to 256 rows (a token of each sequence of a large batch), by the
-// rule at launch_typed.  The work is still the read of W, so W is the product's M operand (128 of its rows by all
+// linear_mid_kernel: tens to hundreds of rows (a token of each sequence of a large
+// batch), or few outputs over a long K, by the rule at launch_typed.  The work is still the read of W, so W is the product's M operand (128 of its rows by all
 // rows of a): with a as the M operand its 128 rows are read from shared memory for
 // every 64 columns of W, 320 cycles for each 8 KB of W a pair streams (64 x 4096 x
 // 4096: 16.6 us, here 11.2).  A cluster of up to 8 CTAs shares K of a tile, TMA rings of 192 KB keeping W on
@@ -572,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
 
 // ------------------------------------------------------------- medium rows
 
-constexpr int M_ROWS = 256;                              // most rows of a
+constexpr int M_ROWS = 256;                              // most rows of a in a tile
 constexpr int M_SPLIT = 8;                               // most CTAs of a cluster
 constexpr int M_THREADS = 320;                           // warp 0 loads, warp 1 products, warps 2-9 epilogue
 constexpr int M_MAX_STAGES = 9;
@@ -616,18 +616,19 @@ __device__ __forceinline__ void finish4(T* c, const T* residual, float4 v) {
   *reinterpret_cast<uint2*>(c) = make_uint2(w.x, w.y);
 }
 
-// One cluster: 128 columns of c; its CTAs share K.  D[n, t] = sum_k W[n, k] a[t, k].
+// One cluster: `row_step` rows by 128 columns of c; its CTAs share K.  D[n, t] = sum_k W[n, k] a[t, k].
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(M_THREADS, 1)
     linear_mid_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                      const LinearEpiArgs a, int act, int splits) {
+                      const LinearEpiArgs a, int act, int splits, int row_step) {
   extern __shared__ __align__(1024) uint8_t smem_mid[];
   const uint32_t base = smem_u32(smem_mid), bars = base + M_OFF_BAR;
   auto bar = [&](uint32_t kind, uint32_t i) { return bars + kind + 8 * i; };
   const uint32_t abort_flag = bars + MW_ABORT;
   const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_mid + M_OFF_BAR + MW_TMEM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(blockIdx.x) % splits, n0 = static_cast<int>(blockIdx.x) / splits * 128;
+  const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
+  const int ntiles = (a.N + 127) / 128, n0 = tile % ntiles * 128, t0 = tile / ntiles * row_step;
   if (warp == 1) {
     tmem_alloc(bars + MW_TMEM, M_TMEM_COLS);
     tmem_relinquish();
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   const int T = __ldg(a.cu + a.B);
   const bool valid = T >= 0 && T <= a.cap;
   if (!valid && blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
-  const int rows = valid ? T : 0, boxes = (rows + 31) / 32, cols = (rows + 15) & ~15;
+  const int rows = valid ? max(0, min(T - t0, row_step)) : 0, boxes = (rows + 31) / 32, cols = (rows + 15) & ~15;
   const uint32_t stage_bytes = M_W_BYTES + static_cast<uint32_t>(boxes) * 4096u;
   const uint32_t stages = min(static_cast<uint32_t>(M_MAX_STAGES), M_RING_BYTES / stage_bytes);
   const int kchunks = (a.K + LK - 1) / LK;
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         const uint32_t dst = base + s * stage_bytes;
         mbar_expect_tx(bar(MB_FULL, s), stage_bytes);
         tma_load_2d(dst, &map_w, kc * LK, n0, bar(MB_FULL, s));          // rows past N, columns past K: zeros
-        for (int b = 0; b < boxes; ++b) tma_load_2d(dst + M_W_BYTES + b * 4096, &map_a, kc * LK, 32 * b, bar(MB_FULL, s));
+        for (int b = 0; b < boxes; ++b) tma_load_2d(dst + M_W_BYTES + b * 4096, &map_a, kc * LK, t0 + 32 * b, bar(MB_FULL, s));
         if (++s == stages) {
           s = 0;
           ++lap;
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         v[3] += b.w;
       }
       activate(v, act);
-      const size_t o = static_cast<size_t>(t) * a.N + n;
+      const size_t o = static_cast<size_t>(t0 + t) * a.N + n;
       finish4(static_cast<Tout*>(a.c) + o, a.residual != nullptr ? static_cast<const Tout*>(a.residual) + o : nullptr,
               make_float4(v[0], v[1], v[2], v[3]));
     }
@@ -1009,16 +1010,30 @@ cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, ma, mw[0], mw[1], mw[2], a, act);
 }
 
-// CTAs that share K of a tile: K is split until they fill the SMs once, each keeping two chunks of 64 at least.
-int mid_splits(const LinearEpiArgs& a, int num_sms) {
-  const int tiles = (a.N + 127) / 128, kchunks = (a.K + LK - 1) / LK;
-  int splits = 1;
-  while (splits < M_SPLIT && 2 * splits * tiles <= num_sms && kchunks >= 4 * splits) splits *= 2;
-  return splits;
+// How linear_mid_kernel cuts its work: tiles of row_step rows by 128 columns, K of each split while the clusters run
+// at once (of 152 SMs clusters of 4 find room on 144, of 8 on 120) and each CTA keeps two chunks of 64; and about what it takes, in cycles: per step of 16 in K 64 +
+// rows/2 for the shared memory that the products read, and some 36 a row for joining the sums.
+struct MidCut {
+  int splits, row_step;
+  long long ctas, cycles;
+};
+MidCut cut_mid(const LinearEpiArgs& a, int num_sms) {
+  MidCut m;
+  const long long row_tiles = (a.cap - 1LL) / M_ROWS + 1, tiles = row_tiles * ((a.N + 127) / 128);
+  const int kchunks = (a.K + LK - 1) / LK;
+  m.row_step = static_cast<int>((a.cap + row_tiles - 1) / row_tiles + 15) & ~15;
+  m.splits = 1;
+  const int at_once[] = {num_sms, num_sms * 18 / 19, num_sms * 15 / 19};  // clusters of 2, 4, 8
+  for (const int room : at_once)
+    if (m.splits < M_SPLIT && 2 * m.splits * tiles <= room && kchunks >= 4 * m.splits) m.splits *= 2;
+  m.ctas = tiles * m.splits;
+  m.cycles = (4LL * ((kchunks + m.splits - 1) / m.splits) * (64 + m.row_step / 2) + 36 * m.row_step) *
+             ((m.ctas + num_sms - 1) / num_sms);
+  return m;
 }
 
 template <typename Tin, typename Tout>
-cudaError_t launch_mid(const LinearEpiArgs& a, int act, int splits, cudaStream_t stream) {
+cudaError_t launch_mid(const LinearEpiArgs& a, int act, const MidCut& cut, cudaStream_t stream) {
   if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
   auto kernel = linear_mid_kernel<Tin, Tout>;
   cudaError_t e = allow_smem<Tin, Tout, -1>(kernel, M_SMEM);
@@ -1028,12 +1043,12 @@ cudaError_t launch_mid(const LinearEpiArgs& a, int act, int splits, cudaStream_t
   if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, 32)) != cudaSuccess) return e;
   if ((e = make_map_2d(&mw, a.w, a.N, a.K, bf16, 128)) != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = dependent_config(attr, (a.N + 127) / 128 * splits, M_THREADS, M_SMEM, stream);
+  cudaLaunchConfig_t cfg = dependent_config(attr, static_cast<int>(cut.ctas), M_THREADS, M_SMEM, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cut.splits);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, ma, mw, a, act, splits);
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mw, a, act, cut.splits, cut.row_step);
 }
 
 template <typename Tin, typename Tout, int NT>
@@ -1050,17 +1065,13 @@ template <typename Tin, typename Tout>
 cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
   if (a.cap <= 16) return launch_few<Tin, Tout, 2>(a, act, stream);
-  if (a.cap <= M_ROWS) {
-    // The way whose products read less shared memory in turn, in cycles: 64 + rows/2 a step of 16 in K with W
-    // as the M operand, make_tiling's cost with a; joining the sums takes about 36 a row there.  4096 x 4096: 64
-    // rows 11.2 against 16.6 us, 200 rows 15.6 / 16.1, 256 rows 17.4 / 16.3; 768 x 2304: 64 rows 5.8 / 6.1, 128
-    // rows 7.0 / 6.2; 16384 x 4096: 256 rows 36.7 / 48.3.
-    const int splits = mid_splits(a, num_sms), kchunks = (a.K + LK - 1) / LK, tiles = (a.N + 127) / 128;
-    const long long here = 4LL * ((kchunks + splits - 1) / splits) * (64 + a.cap / 2) *
-                               ((static_cast<long long>(tiles) * splits + num_sms - 1) / num_sms) + 36 * a.cap;
-    const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * kchunks;
-    if (here < there) return launch_mid<Tin, Tout>(a, act, splits, stream);
-  }
+  // The way that takes less, by the shared memory that the products read in turn (make_tiling's cost for pairs).
+  // 4096 x 4096: 64 rows 11.2 us with W as the M operand against 16.6, 200 rows 15.6 / 16.1, 256 rows 17.4 / 16.3; 768 x
+  // 2304: 64 rows 5.8 / 6.1, 128 rows 7.0 / 6.2; 16384 x 4096: 256 rows 36.7 / 48.3; 7440 x 72: 392 rows 12.4 / 23.8.
+  // (Only where all of its clusters run at once: further rounds repeat a cluster's set-up.)
+  const MidCut cut = cut_mid(a, num_sms);
+  const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * ((a.K + LK - 1) / LK);
+  if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) return launch_mid<Tin, Tout>(a, act, cut, stream);
   return launch_pair<Tin, Tout>(a, act, num_sms, stream);
 }
 

@@ -92,7 +92,8 @@ def test_linear_epilogue_types(cap, T, act, dtype, out):
 
 @pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (2569, 2600, 768, 2304),
                                        (300, 300, 72, 8200), (700, 1200, 1544, 4104), (200, 256, 8200, 1032),
-                                       (161, 200, 4104, 4104), (200, 200, 1032, 16392),
+                                       (161, 200, 4104, 4104), (392, 392, 7440, 72), (300, 1000, 4784, 136), (2, 281, 4784, 136),
+                                       (513, 513, 2056, 520), (200, 200, 1032, 16392),
                                        # a last round of few tiles, cut in four, in two, and past the last column
                                        (11000, 11000, 72, 512), (11000, 11008, 72, 264), (11000, 11000, 584, 264),
                                        (7000, 7000, 136, 1000)])
