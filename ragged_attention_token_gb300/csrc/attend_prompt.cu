@@ -8,7 +8,10 @@
 // A unit is two tiles of 128 query rows (A and B; one TMEM lane per row) that read
 // the same keys: 256 rows of one query head, or 128 rows of two heads of one
 // key/value head (prompt_shape).  Keys stream in blocks of 128 that both tiles
-// use, so each K/V byte read from L2 serves 256 rows.  Per SM one CTA, its warps:
+// use, so each K/V byte read from L2 serves 256 rows.  Where the units of a call
+// would leave SMs idle, both tiles are the same 128 rows of a head instead and take
+// every other block of keys each; their sums are joined through shared memory.
+// Per SM one CTA, its warps:
 //   warps 0-3 / 4-7  softmax of tile A / B, thread r owning row r: the block's
 //            scores from TMEM into registers, their maximum, the weights in
 //            base 2, written over the scores as 16-bit pairs;
@@ -38,6 +41,8 @@
 // round to round.  Every wait is bounded; a CTA that gives up records
 // RRA_DEVERR_WAIT_TIMEOUT, lets copies and products in flight land, frees its
 // TMEM and returns.
+#include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -67,7 +72,8 @@ struct PromptCfg {
   static constexpr uint32_t OFF_KV = 2 * TILE;
   static constexpr uint32_t OFF_OUT = OFF_KV + SLOTS * TILE;      // output staging, 4 KB a softmax warp
   static constexpr uint32_t OFF_BAR = OFF_OUT + P_SOFTMAX_WARPS * 4096;
-  static constexpr uint32_t SMEM = OFF_BAR + 512;
+  static constexpr uint32_t OFF_JOIN = OFF_BAR + 512;             // [2][128] reference and sum of a row (split units)
+  static constexpr uint32_t SMEM = OFF_JOIN + 2 * PT * 8;
   // TMEM columns: S of A and B, O of A and B; P over S, or, where there is
   // room (d = 64), beside it: then the next S need not wait for this P V, and
   // goes as soon as the scores are in registers (32 heads, 8192 rows, not causal: 594 -> 547 us).
@@ -90,34 +96,58 @@ constexpr uint32_t PW_TMEM = 248, PW_ABORT = 252;
 constexpr uint32_t P_DESC = 256;        // [2] x 32 bytes: s0, n, q0, h (q0 < 0: no more units)
 constexpr uint32_t PB_S_READ = 320;     // [2] the scores are in registers (one arrival per softmax warp of the tile)
 constexpr uint32_t PB_TAIL = 336;       // [2] a V block's tail to zero; zeroed
+constexpr uint32_t PB_JOIN = 352;       // [2] tile w's share for the other tile is in shared memory (one arrival per warp)
 
-// How units are made up: `heads` query heads and `rows` rows (2 and 128, or 1 and 256).
+// How units are made up: `heads` query heads and `rows` rows (2 and 128, or 1 and 256), or
+// `split`: 1 and 128, tile w taking the key blocks w, w + 2, ...
 struct UnitShape {
-  int heads, rows;
+  int heads, rows, split;
 };
 
 struct PromptUnit {
   int s0, n, q0, h;
   // First row and head of tile w.
-  __device__ int row0(int w, const UnitShape& us) const { return us.heads == 2 ? q0 : q0 + w * PT; }
+  __device__ int row0(int w, const UnitShape& us) const { return us.rows == PT ? q0 : q0 + w * PT; }
   __device__ int head(int w, const UnitShape& us) const { return us.heads == 2 ? h + w : h; }
-  __device__ bool has_b(const UnitShape& us) const { return us.heads == 2 || n - q0 > PT; }
-  // Key blocks of tile w.
-  __device__ int blocks(int w, const UnitShape& us, int causal) const {
-    if (w == 1 && !has_b(us)) return 0;
+  // Key blocks that the rows of tile w see; split: those of both tiles.
+  __device__ int seen(int w, const UnitShape& us, int causal) const {
+    if (w == 1 && us.rows > PT && n - q0 <= PT) return 0;
     const int all = (n + PT - 1) / PT;
     return causal ? min(all, row0(w, us) / PT + 1) : all;
   }
+  // Key blocks of tile w, and of the unit.
+  __device__ int blocks(int w, const UnitShape& us, int causal) const {
+    return us.split ? (seen(0, us, causal) + 1 - w) / 2 : seen(w, us, causal);
+  }
+  __device__ int blocks(const UnitShape& us, int causal) const { return max(seen(0, us, causal), seen(1, us, causal)); }
 };
 
-// Two heads of a group at the same rows where the group is even, d = 128 and the
-// prompts are not very long; else 256 rows of a head.  Two heads see the same blocks, so
+// About how long a call takes with units of this shape, in key blocks of a unit (1.8 us at d = 128, 1.2 at
+// d = 64; a change of unit takes 2): its longest unit alone, or all of them spread over the SMs, for sequences as long as
+// the mean (causal: units of every length; not causal: rounds of equal ones).
+inline double prompt_time(const PromptArgs& a, const UnitShape& us, int num_sms) {
+  const int longest = std::min(a.max_seqlen, a.cap), mean_len = std::min(longest, std::max(1, a.cap / a.B));
+  auto blocks = [&](int n) { return (n - 1) / PT + 1; };
+  const long long tiles = std::min(a.B * ((a.max_seqlen - 1LL) / us.rows + 1), a.cap / us.rows + static_cast<long long>(a.B));
+  const double rounds = static_cast<double>(tiles * (a.Hq / us.heads)) / num_sms, per = us.split ? 0.5 : 1.0;
+  const double mean = 2 + per * (a.causal ? (blocks(mean_len) + us.rows / PT) / 2.0 : blocks(mean_len));
+  const double alone = 2 + (us.split ? (blocks(longest) + 1) / 2 : blocks(longest));
+  return std::max(alone, mean * (a.causal ? rounds + 1 / 3.0 : std::ceil(rounds)));
+}
+
+// Whole: two heads of a group at the same rows where the group is even, d = 128 and
+// the prompts are not very long; else 256 rows of a head.  Two heads see the same blocks, so
 // neither tile ever works alone, which the last rows of many sequences would; two
 // successive tiles end one after the other, so that one's output leaves under the other's last
 // block.  32 / 8 heads, d = 128, causal, heads paired against rows: 16 x 1024 tokens 156 / 162 us,
 // 8 x 2048 243 / 249, eight of 1 to 4096 297 / 309, 8192 404 / 405, 16384 1500 / 1468; d = 64: 8192 293 / 279.
-__host__ __device__ inline UnitShape prompt_shape(int group, int d, int max_seqlen) {
-  return group % 2 == 0 && d == 128 && max_seqlen <= 8192 ? UnitShape{2, PT} : UnitShape{1, 2 * PT};
+// Split: where that takes less by prompt_time.  d = 128, causal, whole against split: 32 / 8 heads, 200 tokens 9.1 /
+// 7.0 us, 1024 20.2 / 16.5, 4096 115 / 118, 16 x 1024 156 / 202; 8 / 1 heads, 4096 63 / 35, 8192 121 / 110; d = 64, 12
+// heads, not causal: 577 11.1 / 8.4, 4096 86 / 67, 8192 241 / 240, 16 x 512 23.9 / 33.1.
+inline UnitShape prompt_shape(const PromptArgs& a, int d, int num_sms) {
+  const UnitShape whole = a.Hq / a.Hkv % 2 == 0 && d == 128 && a.max_seqlen <= 8192 ? UnitShape{2, PT, 0} : UnitShape{1, 2 * PT, 0};
+  const UnitShape split{1, PT, 1};
+  return prompt_time(a, split, num_sms) < prompt_time(a, whole, num_sms) ? split : whole;
 }
 
 // Walks the non-empty units in order (query tile descending, sequence, head);
@@ -258,11 +288,12 @@ __device__ __forceinline__ float prompt_weights(uint32_t tP, const float (&s)[PT
   return a0 + a1;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(P_THREADS, 1)
     attend_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+                         const __grid_constant__ CUtensorMap map_v, const PromptArgs a, const int heads, const int rows) {
   using C = PromptCfg<D>;
+  const UnitShape us{SPLIT ? 1 : heads, SPLIT ? PT : rows, SPLIT};
   constexpr bool BF = IsBf16<T>::value == 1;
   extern __shared__ __align__(1024) uint8_t smem_prompt[];   // the swizzled tiles start 1024-byte aligned
   const uint32_t base = smem_u32(smem_prompt);
@@ -285,7 +316,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(PB_Q_FULL, i), 1);
-      mbar_init(bar(PB_Q_EMPTY, i), 1);
+      mbar_init(bar(PB_Q_EMPTY, i), SPLIT ? P_SOFTMAX_WARPS / 2 : 1);
+      mbar_init(bar(PB_JOIN, i), P_SOFTMAX_WARPS / 2);
       mbar_init(bar(PB_S_FULL, i), 1);
       mbar_init(bar(PB_P_READY, i), P_SOFTMAX_WARPS / 2);
       mbar_init(bar(PB_PV_DONE, i), 1);
@@ -306,7 +338,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
   dependent_launch();
-  const UnitShape us = prompt_shape(a.Hq / a.Hkv, D, a.max_seqlen);
   bool bad = false;
   // A bounded wait; every lane of the warp leaves with the same `bad`.
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -347,7 +378,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         __syncwarp();
         if (u.q0 < 0) break;
         const int hk = u.h / (a.Hq / a.Hkv);
-        const int nb = max(u.blocks(0, us, a.causal), u.blocks(1, us, a.causal));
+        const int nb = u.blocks(us, a.causal);
         auto load_q = [&](int w) {
           if (nq[w] > 0 && !wait(bar(PB_Q_EMPTY, w), (nq[w] - 1) & 1)) return;
           ++nq[w];
@@ -371,7 +402,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         };
         load_q(0);
         if (!bad) load_kv(&map_k, 0);
-        if (!bad && u.has_b(us)) load_q(1);
+        if (!bad && u.blocks(1, us, a.causal) > 0) load_q(1);
         if (!bad) load_kv(&map_v, 0);
         for (int j = 1; j < nb && !bad; ++j) {
           load_kv(&map_k, j);
@@ -388,7 +419,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
         const PromptUnit u = read_unit(i);
         if (u.q0 < 0) break;
-        const int nb = max(u.blocks(0, us, a.causal), u.blocks(1, us, a.causal));
+        const int nb = u.blocks(us, a.causal);
         const int keys = min(PT, u.n - (nb - 1) * PT), pad = -keys & 15;
         kv0 += 2 * static_cast<uint32_t>(nb);
         if (pad > 0) {
@@ -468,12 +499,44 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           umma_commit(bar(PB_PV_DONE, w));
           return true;
         };
+        // A V block of `keys` keys: those behind them, up to 16, are zeroed before its P V.
+        auto tail = [&](int keys) {
+          if ((keys & 15) == 0) return true;
+          mbar_arrive(bar(PB_TAIL, 0));
+          return wait1(bar(PB_TAIL, 1), ntail++ & 1);
+        };
         PromptUnit u{0, 0, -1, 0};
         int started = 0;                        // tiles (bits) whose first S was issued during the previous unit
         if (wait1(bar(PB_U_FULL, 0), 0)) u = read_unit(0);
         for (int i = 0; !bad && u.q0 >= 0; ++i) {
-          const int nba = u.blocks(0, us, a.causal), nbb = u.blocks(1, us, a.causal), nb = max(nba, nbb);
+          const int nba = u.blocks(0, us, a.causal), nbb = u.blocks(1, us, a.causal), nb = u.blocks(us, a.causal);
           PromptUnit next{0, 0, -2, 0};         // not read yet
+          if constexpr (SPLIT) {
+            // Block j for tile j & 1; S of its next block ahead of (own P) or behind its P V.  The Q tiles are
+            // handed back by the join, so nothing of the next unit is issued ahead.
+            auto s_of = [&](int j) {
+              if (!next_s(j & 1, j >> 1, kv0 + 2 * j, false)) return false;
+              release(kv0 + 2 * j);
+              return true;
+            };
+            if (!s_of(0) || (nb > 1 && !s_of(1))) break;
+            for (int j = 0; j < nb && !bad; ++j) {
+              const uint32_t vi = kv0 + 2 * j + 1;
+              if (!kv_wait(vi)) break;
+              const int keys = min(PT, u.n - j * PT);
+              if (!tail(keys)) break;
+              if (C::OWN_P && j + 2 < nb && !s_of(j + 2)) break;
+              if (!next_pv(j & 1, j >> 1, (keys + 15) / 16, vi)) break;
+              release(vi);
+              if (!C::OWN_P && j + 2 < nb && !s_of(j + 2)) break;
+            }
+            if (bad || !wait1(bar(PB_U_FULL, (i + 1) & 1), ((i + 1) >> 1) & 1)) break;
+            next = read_unit(i + 1);
+            kv0 += 2 * static_cast<uint32_t>(nb);
+            mbar_arrive(bar(PB_U_EMPTY, i & 1));
+            u = next;
+            continue;
+          }
           if (!(started & 1) && !next_s(0, 0, kv0, nba == 1)) break;
           if (nbb > 0 && !(started & 2) && !next_s(1, 0, kv0, nbb == 1)) break;
           started = 0;
@@ -482,11 +545,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             const uint32_t vi = kv0 + 2 * j + 1, ki = vi + 1;
             if (!kv_wait(vi)) break;
             const int keys = min(PT, u.n - j * PT), ksteps = (keys + 15) / 16;
-            if (keys & 15) {
-              mbar_arrive(bar(PB_TAIL, 0));
-              if (!wait1(bar(PB_TAIL, 1), ntail & 1)) break;
-              ++ntail;
-            }
+            if (!tail(keys)) break;
             // With the next block's S ahead of this block's P V (own P), or right behind it.
             if constexpr (C::OWN_P) {
               if (j + 1 < nba && !next_s(0, j + 1, ki, j + 2 == nba)) break;
@@ -540,22 +599,24 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     const uint32_t tS = tmem + lane_off + C::T_S + w * PT, tO = tmem + lane_off + C::T_O + w * D;
     const uint32_t tP = tmem + lane_off + C::T_P + w * C::P_STEP;
     uint32_t count = 0;                     // blocks of this tile so far
+    uint32_t joins = 0;                     // units joined so far
     for (int i = 0;; ++i) {
       if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
       const PromptUnit u = read_unit(i);
       if (u.q0 < 0) break;
-      const int nbw = u.blocks(w, us, a.causal);
+      const int nbw = u.blocks(w, us, a.causal), last = u.seen(w, us, a.causal) - 1;
       float m_ref = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nbw; ++j) {
         if (!wait(bar(PB_S_FULL, w), count & 1)) break;
         tc_fence_after();
         float s[PT], mx;
-        if (j + 1 < nbw) {
+        const int jk = SPLIT ? 2 * j + w : j;           // the block of keys
+        if (jk < last) {
           mx = prompt_scores<false>(tS, PT, s);
         } else {
           // The last block: the sequence's end, and the diagonal when causal.
-          int lim = u.n - j * PT;
-          if (a.causal) lim = min(lim, u.row0(w, us) + row - j * PT + 1);
+          int lim = u.n - jk * PT;
+          if (a.causal) lim = min(lim, u.row0(w, us) + row - jk * PT + 1);
           mx = prompt_scores<true>(tS, lim, s);
         }
         if constexpr (C::OWN_P) {
@@ -582,9 +643,74 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(PB_P_READY, w));
       }
       if (bad) break;
-      if (nbw > 0) {
+      if (SPLIT && last > 0) {
+        // Both tiles hold the row: each hands the other the half of O's columns that it writes out (fp32, over the Q
+        // tile that its own products have read), and reference and sum.
         if (!wait(bar(PB_PV_DONE, w), (count - 1) & 1)) break;
         tc_fence_after();
+        constexpr int H = D / 2, CH = H / 8;               // columns of a tile; 16-byte chunks of a row's outputs
+        auto at = [&](int tile, int c) { return s_q(tile) + row * (H * 4) + ((c ^ (row & 7)) << 4); };
+        const uint32_t ml = bars + 512u + static_cast<uint32_t>(row) * 8u;
+#pragma unroll
+        for (int g = 0; g < H / 32; ++g) {
+          float o[32];
+          tmem_ld32(tO + (w ^ 1) * H + 32 * g, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(at(w, 8 * g + k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                         __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+        }
+        st_shared_u32(ml + w * (PT * 8), __float_as_uint(m_ref));
+        st_shared_u32(ml + w * (PT * 8) + 4, __float_as_uint(l_run));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PB_JOIN, w));
+        if (!wait(bar(PB_JOIN, w ^ 1), joins & 1)) break;
+        ++joins;
+        const float m_o = __uint_as_float(ld_shared_u32(ml + (w ^ 1) * (PT * 8)));
+        const float l_o = __uint_as_float(ld_shared_u32(ml + (w ^ 1) * (PT * 8) + 4));
+        const float m = fmaxf(m_ref, m_o), mu = m == -INFINITY ? 0.f : m;
+        const float f = fast_exp2(m_ref - mu), f_o = fast_exp2(m_o - mu), l = l_run * f + l_o * f_o;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l), x = f * inv, x_o = f_o * inv;
+        const uint32_t stg = base + C::OFF_OUT + static_cast<uint32_t>(warp) * 4096u;
+        auto out_at = [&](int r, int c) { return stg + r * (H * 2) + ((c ^ ((CH == 8 ? r : r >> 1) & (CH - 1))) << 4); };
+#pragma unroll
+        for (int g = 0; g < H / 32; ++g) {
+          float o[32];
+          tmem_ld32(tO + w * H + 32 * g, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = ld_shared_v4(at(w ^ 1, 8 * g + k));
+            o[4 * k] = o[4 * k] * x + __uint_as_float(v.x) * x_o;
+            o[4 * k + 1] = o[4 * k + 1] * x + __uint_as_float(v.y) * x_o;
+            o[4 * k + 2] = o[4 * k + 2] * x + __uint_as_float(v.z) * x_o;
+            o[4 * k + 3] = o[4 * k + 3] * x + __uint_as_float(v.w) * x_o;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pack2<Tout2<T>>(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
+            st_shared_v4(out_at(lane, 4 * g + k), p[0], p[1], p[2], p[3]);
+          }
+        }
+        fence_proxy_async();                               // the next Q tile comes by TMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PB_Q_EMPTY, w ^ 1));
+        const int r0 = u.q0 + (warp & 3) * 32;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const int rr = (32 / CH) * k + lane / CH, cc = lane % CH;
+          const uint4 v = ld_shared_v4(out_at(rr, cc));
+          if (r0 + rr < u.n)
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.o) +
+                                      (static_cast<long long>(u.s0 + r0 + rr) * a.Hq + u.h) * D + w * H + 8 * cc) = v;
+        }
+        __syncwarp();
+        tc_fence_before();
+      } else if (nbw > 0) {
+        if (!wait(bar(PB_PV_DONE, w), (count - 1) & 1)) break;
+        tc_fence_after();
+        if (SPLIT && lane == 0) mbar_arrive(bar(PB_Q_EMPTY, 0));   // a unit of one block: tile A's alone
         const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
         // 64 columns at a time through the warp's 4 KB of staging (rows of
         // 128 bytes, 16-byte chunks swizzled): whole row pieces leave, four to an
@@ -672,10 +798,10 @@ cudaError_t make_map_rows(CUtensorMap* map, const void* ptr, int rows, int H, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int D>
-cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+template <typename T, int D, bool SPLIT>
+cudaError_t launch_shape(const PromptArgs& a, const UnitShape& us, int num_sms, cudaStream_t stream) {
   using C = PromptCfg<D>;
-  auto kernel = attend_prompt_kernel<T, D>;
+  auto kernel = attend_prompt_kernel<T, D, SPLIT>;
   constexpr int kMaxDevices = 64;
   static bool attr_set[kMaxDevices] = {};
   static std::mutex m;
@@ -696,7 +822,6 @@ cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if ((e = make_map_rows(&mq, a.q, a.cap, a.Hq, D, a.q_stride, bf16)) != cudaSuccess) return e;
   if ((e = make_map_rows(&mk, a.k, a.cap, a.Hkv, D, a.k_stride, bf16)) != cudaSuccess) return e;
   if ((e = make_map_rows(&mv, a.v, a.cap, a.Hkv, D, a.v_stride, bf16)) != cudaSuccess) return e;
-  const UnitShape us = prompt_shape(a.Hq / a.Hkv, D, a.max_seqlen);
   const long long units = static_cast<long long>(a.B) * (a.Hq / us.heads) * ((a.max_seqlen - 1) / us.rows + 1);
   const int grid = static_cast<int>(units < num_sms ? units : num_sms);
   cudaLaunchConfig_t cfg = {};
@@ -709,7 +834,13 @@ cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, us.heads, us.rows);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+  const UnitShape us = prompt_shape(a, D, num_sms);
+  return us.split ? launch_shape<T, D, true>(a, us, num_sms, stream) : launch_shape<T, D, false>(a, us, num_sms, stream);
 }
 
 }  // namespace

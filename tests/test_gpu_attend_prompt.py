@@ -190,3 +190,67 @@ def test_attend_prompt_repeats_bit_for_bit_and_in_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_prompt_many_units(d, causal):
+    """More units than SMs, whole: ragged tiles end to end, one call long enough that every CTA takes several."""
+    rng = np.random.default_rng(d)
+    lens = [int(x) for x in rng.integers(0, 300, 24)] + [127, 128, 129, 255, 256, 257, 1, 2]
+    _run(lens, 12, 12, d, torch.bfloat16, causal, seed=d)
+    _run(lens, 8, 4, d, torch.float16, causal, seed=d + 1)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,causal,lens", [
+    (128, 8, 1, True, [4096]), (128, 16, 4, True, [2047]), (64, 12, 4, False, [3900]), (64, 12, 12, True, [3841, 1]),
+    (128, 12, 12, False, [100, 3009, 128, 0, 129])])
+def test_attend_prompt_keys_split_over_several_rounds(d, Hq, Hkv, causal, lens):
+    """Few long prompts: both tiles of a unit are the same rows, and CTAs take several units, some of one block."""
+    rows = np.array([0, 1, 126, 127, 128, 129, 255, 256, 1000, 2046, 2047, 3008, 3840, 3899, 4095])
+    _run(lens, Hq, Hkv, d, torch.bfloat16, causal, seed=Hq, rows=rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_prompt_blocks_of_infinite_scores(d, dtype):
+    """Every other block of 128 keys at -inf (scores -inf, weights 0), either way round; and scores far apart from block to block."""
+    n = 700
+    g = torch.Generator().manual_seed(9)
+    q, v = torch.rand((n, 2, d), generator=g).to(dtype) + 0.5, torch.randn((n, 2, d), generator=g).to(dtype)
+    k = torch.randn((n, 2, d), generator=g).to(dtype)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    block = torch.arange(n) // 128
+    for odd in (0, 1):
+        kk = k.clone()
+        kk[block % 2 == odd, :, 3] = float("-inf")
+        o = nan_fill(torch.empty((n, 2, d), dtype=dtype, device="cuda"))
+        rra.attend_prompt(q.cuda(), kk.cuda(), v.cuda(), cu, 1, n, o, scale=0.1, causal=False)
+        seen = block % 2 != odd
+        m = int(seen.sum())
+        check_rows(o.cpu()[:m], q[:m], k[seen], v[seen], 0.1, np.full(m, m - 1), dtype)
+        # Causal: rows of block 0 that see -inf alone sum to nothing and come out as zeros.
+        rra.attend_prompt(q.cuda(), kk.cuda(), v.cuda(), cu, 1, n, o, scale=0.1)
+        torch.cuda.synchronize()
+        got = o.cpu().float()
+        assert bool(torch.isfinite(got).all())
+        if odd == 0:
+            assert bool((got[:128] == 0).all()) and bool((got[128:] != 0).any())
+        kk = k.clone()
+        kk[block % 2 == odd] *= 40.0
+        rra.attend_prompt(q.cuda(), kk.cuda(), v.cuda(), cu, 1, n, o, scale=0.1)
+        check_rows(o.cpu(), q, kk, v, 0.1, np.arange(n), dtype)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_prompt_overlapping_sequences(d):
+    """Offsets that go back make more units than the capacity suggests: each valid sequence is answered, the rest reported."""
+    n, S = 300, 40
+    q, k, v = (torch.randn((n, 4, d), device="cuda").bfloat16() for _ in range(3))
+    cu = torch.tensor([0, n] * S, dtype=torch.int32, device="cuda")
+    o = nan_fill(torch.empty_like(q))
+    rra.get_device_error(clear=True)
+    rra.attend_prompt(q, k, v, cu, 2 * S - 1, n, o, scale=0.1)
+    torch.cuda.synchronize()
+    assert rra.get_device_error(clear=True) == rra.DEVERR_SEQ_NEGATIVE
+    check_rows(o.cpu(), q.cpu(), k.cpu(), v.cpu(), 0.1, np.arange(n), torch.bfloat16)
