@@ -107,11 +107,11 @@ struct UnitShape {
 struct PromptUnit {
   int s0, n, q0, h;
   // First row and head of tile w.
-  __device__ int row0(int w, const UnitShape& us) const { return us.rows == PT ? q0 : q0 + w * PT; }
+  __device__ int row0(int w, const UnitShape& us) const { return us.heads == 2 || us.split ? q0 : q0 + w * PT; }
   __device__ int head(int w, const UnitShape& us) const { return us.heads == 2 ? h + w : h; }
   // Key blocks that the rows of tile w see; split: those of both tiles.
   __device__ int seen(int w, const UnitShape& us, int causal) const {
-    if (w == 1 && us.rows > PT && n - q0 <= PT) return 0;
+    if (w == 1 && us.heads == 1 && !us.split && n - q0 <= PT) return 0;
     const int all = (n + PT - 1) / PT;
     return causal ? min(all, row0(w, us) / PT + 1) : all;
   }
@@ -141,12 +141,15 @@ inline double prompt_time(const PromptArgs& a, const UnitShape& us, int num_sms)
 // successive tiles end one after the other, so that one's output leaves under the other's last
 // block.  32 / 8 heads, d = 128, causal, heads paired against rows: 16 x 1024 tokens 156 / 162 us,
 // 8 x 2048 243 / 249, eight of 1 to 4096 297 / 309, 8192 404 / 405, 16384 1500 / 1468; d = 64: 8192 293 / 279.
+__host__ __device__ inline UnitShape whole_shape(int group, int d, int max_seqlen) {
+  return group % 2 == 0 && d == 128 && max_seqlen <= 8192 ? UnitShape{2, PT, 0} : UnitShape{1, 2 * PT, 0};
+}
+
 // Split: where that takes less by prompt_time.  d = 128, causal, whole against split: 32 / 8 heads, 200 tokens 9.1 /
 // 7.0 us, 1024 20.2 / 16.5, 4096 115 / 118, 16 x 1024 156 / 202; 8 / 1 heads, 4096 63 / 35, 8192 121 / 110; d = 64, 12
 // heads, not causal: 577 11.1 / 8.4, 4096 86 / 67, 8192 241 / 240, 16 x 512 23.9 / 33.1.
 inline UnitShape prompt_shape(const PromptArgs& a, int d, int num_sms) {
-  const UnitShape whole = a.Hq / a.Hkv % 2 == 0 && d == 128 && a.max_seqlen <= 8192 ? UnitShape{2, PT, 0} : UnitShape{1, 2 * PT, 0};
-  const UnitShape split{1, PT, 1};
+  const UnitShape whole = whole_shape(a.Hq / a.Hkv, d, a.max_seqlen), split{1, PT, 1};
   return prompt_time(a, split, num_sms) < prompt_time(a, whole, num_sms) ? split : whole;
 }
 
@@ -291,9 +294,9 @@ __device__ __forceinline__ float prompt_weights(uint32_t tP, const float (&s)[PT
 template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(P_THREADS, 1)
     attend_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, const PromptArgs a, const int heads, const int rows) {
+                         const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
   using C = PromptCfg<D>;
-  const UnitShape us{SPLIT ? 1 : heads, SPLIT ? PT : rows, SPLIT};
+  const UnitShape us = SPLIT ? UnitShape{1, PT, 1} : whole_shape(a.Hq / a.Hkv, D, a.max_seqlen);
   constexpr bool BF = IsBf16<T>::value == 1;
   extern __shared__ __align__(1024) uint8_t smem_prompt[];   // the swizzled tiles start 1024-byte aligned
   const uint32_t base = smem_u32(smem_prompt);
@@ -499,17 +502,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           umma_commit(bar(PB_PV_DONE, w));
           return true;
         };
-        // A V block of `keys` keys: those behind them, up to 16, are zeroed before its P V.
-        auto tail = [&](int keys) {
-          if ((keys & 15) == 0) return true;
-          mbar_arrive(bar(PB_TAIL, 0));
-          return wait1(bar(PB_TAIL, 1), ntail++ & 1);
-        };
         PromptUnit u{0, 0, -1, 0};
         int started = 0;                        // tiles (bits) whose first S was issued during the previous unit
         if (wait1(bar(PB_U_FULL, 0), 0)) u = read_unit(0);
         for (int i = 0; !bad && u.q0 >= 0; ++i) {
-          const int nba = u.blocks(0, us, a.causal), nbb = u.blocks(1, us, a.causal), nb = u.blocks(us, a.causal);
+          const int nba = u.blocks(0, us, a.causal), nbb = u.blocks(1, us, a.causal), nb = SPLIT ? u.seen(0, us, a.causal) : max(nba, nbb);
           PromptUnit next{0, 0, -2, 0};         // not read yet
           if constexpr (SPLIT) {
             // Block j for tile j & 1; S of its next block ahead of (own P) or behind its P V.  The Q tiles are
@@ -524,7 +521,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
               const uint32_t vi = kv0 + 2 * j + 1;
               if (!kv_wait(vi)) break;
               const int keys = min(PT, u.n - j * PT);
-              if (!tail(keys)) break;
+              if (keys & 15) {
+                mbar_arrive(bar(PB_TAIL, 0));
+                if (!wait1(bar(PB_TAIL, 1), ntail & 1)) break;
+                ++ntail;
+              }
               if (C::OWN_P && j + 2 < nb && !s_of(j + 2)) break;
               if (!next_pv(j & 1, j >> 1, (keys + 15) / 16, vi)) break;
               release(vi);
@@ -545,7 +546,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             const uint32_t vi = kv0 + 2 * j + 1, ki = vi + 1;
             if (!kv_wait(vi)) break;
             const int keys = min(PT, u.n - j * PT), ksteps = (keys + 15) / 16;
-            if (!tail(keys)) break;
+            if (keys & 15) {
+              mbar_arrive(bar(PB_TAIL, 0));
+              if (!wait1(bar(PB_TAIL, 1), ntail & 1)) break;
+              ++ntail;
+            }
             // With the next block's S ahead of this block's P V (own P), or right behind it.
             if constexpr (C::OWN_P) {
               if (j + 1 < nba && !next_s(0, j + 1, ki, j + 2 == nba)) break;
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
       const PromptUnit u = read_unit(i);
       if (u.q0 < 0) break;
-      const int nbw = u.blocks(w, us, a.causal), last = u.seen(w, us, a.causal) - 1;
+      const int nbw = u.blocks(w, us, a.causal), last = (SPLIT ? u.seen(w, us, a.causal) : nbw) - 1;
       float m_ref = -INFINITY, l_run = 0.f;
       for (int j = 0; j < nbw; ++j) {
         if (!wait(bar(PB_S_FULL, w), count & 1)) break;
@@ -834,7 +839,7 @@ cudaError_t launch_shape(const PromptArgs& a, const UnitShape& us, int num_sms, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, us.heads, us.rows);
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
 }
 
 template <typename T, int D>
