@@ -56,10 +56,11 @@ constexpr int PT = 128;                      // rows of a tile, keys of a block
 constexpr int P_SOFTMAX_WARPS = 8;
 constexpr int P_LOAD_WARP = 8, P_MMA_WARP = 9, P_TAIL_WARP = 10;
 constexpr int P_THREADS = 384;               // three warpgroups; warp 11 only lends its registers
-// Registers: 384 threads start with 168 each; the softmax warpgroups take 216
-// (a row's 128 scores stay in registers), the third gives down to 72:
-// 8 x 216 + 4 x 72 = 12 x 168.
-constexpr int P_REGS_SOFTMAX = 216, P_REGS_OTHER = 72;
+// Registers: 384 threads start with 168 each; the softmax warpgroups take 200
+// (a row's 128 scores stay in registers), the third gives down to 104:
+// 8 x 200 + 4 x 104 = 12 x 168.  At 216 and 72 the thread that issues the products
+// spilled, between the products: 16 x 1024 tokens, 32 / 8 heads, d = 128, 153 against 127 us; one of 16384 1467 / 1401.
+constexpr int P_REGS_SOFTMAX = 200, P_REGS_OTHER = 104;
 static_assert(8 * P_REGS_SOFTMAX + 4 * P_REGS_OTHER <= 12 * 168, "register split exceeds the launch's registers");
 constexpr uint32_t P_TMEM_COLS = 512;
 constexpr uint32_t P_SUB = PT * 128;         // one 64-element column group of a tile: 128 rows x 128 B
@@ -122,16 +123,18 @@ struct PromptUnit {
   __device__ int blocks(const UnitShape& us, int causal) const { return max(seen(0, us, causal), seen(1, us, causal)); }
 };
 
-// About how long a call takes with units of this shape, in key blocks of a unit (1.8 us at d = 128, 1.2 at
-// d = 64; a change of unit takes 2): its longest unit alone, or all of them spread over the SMs, for sequences as long as
-// the mean (causal: units of every length; not causal: rounds of equal ones).
-inline double prompt_time(const PromptArgs& a, const UnitShape& us, int num_sms) {
+// About how long a call takes with units of this shape, in key blocks of a unit (1.7 us at d = 128, 1.2 at
+// d = 64): its longest unit alone, with 2 for its start and end, or all of them spread over the SMs, for sequences as
+// long as the mean (causal: units of every length; not causal: rounds of equal ones), with 2 for a change of unit, 1
+// where the next unit's first products go out under this one's last.  (0.52: at d = 128 a split unit's ring holds one
+// block ahead for each tile; 32 heads of 16384, not causal: 3210 us split, 2820 whole.)
+inline double prompt_time(const PromptArgs& a, const UnitShape& us, int d, int num_sms) {
   const int longest = std::min(a.max_seqlen, a.cap), mean_len = std::min(longest, std::max(1, a.cap / a.B));
   auto blocks = [&](int n) { return (n - 1) / PT + 1; };
   const long long tiles = std::min(a.B * ((a.max_seqlen - 1LL) / us.rows + 1), a.cap / us.rows + static_cast<long long>(a.B));
-  const double rounds = static_cast<double>(tiles * (a.Hq / us.heads)) / num_sms, per = us.split ? 0.5 : 1.0;
-  const double mean = 2 + per * (a.causal ? (blocks(mean_len) + us.rows / PT) / 2.0 : blocks(mean_len));
-  const double alone = 2 + (us.split ? (blocks(longest) + 1) / 2 : blocks(longest));
+  const double rounds = static_cast<double>(tiles * (a.Hq / us.heads)) / num_sms, per = us.split ? (d == 128 ? 0.52 : 0.5) : 1.0;
+  const double mean = (us.split ? 2 : 1) + per * (a.causal ? (blocks(mean_len) + us.rows / PT) / 2.0 : blocks(mean_len));
+  const double alone = 2 + (us.split ? (blocks(longest) + 1) / 2 * 2 * per : blocks(longest));
   return std::max(alone, mean * (a.causal ? rounds + 1 / 3.0 : std::ceil(rounds)));
 }
 
@@ -139,18 +142,18 @@ inline double prompt_time(const PromptArgs& a, const UnitShape& us, int num_sms)
 // the prompts are not very long; else 256 rows of a head.  Two heads see the same blocks, so
 // neither tile ever works alone, which the last rows of many sequences would; two
 // successive tiles end one after the other, so that one's output leaves under the other's last
-// block.  32 / 8 heads, d = 128, causal, heads paired against rows: 16 x 1024 tokens 156 / 162 us,
-// 8 x 2048 243 / 249, eight of 1 to 4096 297 / 309, 8192 404 / 405, 16384 1500 / 1468; d = 64: 8192 293 / 279.
+// block.  32 / 8 heads, d = 128, causal, heads paired against rows: 16 x 1024 tokens 127 / 140 us,
+// 8 x 2048 207 / 222, eight of 1 to 4096 212 / 228, 8192 369 / 370, 16384 1406 / 1399; d = 64: 8192 281 / 263.
 __host__ __device__ inline UnitShape whole_shape(int group, int d, int max_seqlen) {
   return group % 2 == 0 && d == 128 && max_seqlen <= 8192 ? UnitShape{2, PT, 0} : UnitShape{1, 2 * PT, 0};
 }
 
 // Split: where that takes less by prompt_time.  d = 128, causal, whole against split: 32 / 8 heads, 200 tokens 9.1 /
-// 7.0 us, 1024 20.2 / 16.5, 4096 115 / 118, 16 x 1024 156 / 202; 8 / 1 heads, 4096 63 / 35, 8192 121 / 110; d = 64, 12
-// heads, not causal: 577 11.1 / 8.4, 4096 86 / 67, 8192 241 / 240, 16 x 512 23.9 / 33.1.
+// 7.7 us, 1024 18.8 / 17.4, 4096 104 / 117, 16 x 512 47 / 80; 8 / 1 heads, 4096 58 / 34, 8192 111 / 109; d = 64, 12
+// heads, not causal: 1024 15.0 / 11.3, 4096 85 / 68, 8192 237 / 243, 16 x 512 23.2 / 33.5.
 inline UnitShape prompt_shape(const PromptArgs& a, int d, int num_sms) {
   const UnitShape whole = whole_shape(a.Hq / a.Hkv, d, a.max_seqlen), split{1, PT, 1};
-  return prompt_time(a, split, num_sms) < prompt_time(a, whole, num_sms) ? split : whole;
+  return prompt_time(a, split, d, num_sms) < prompt_time(a, whole, d, num_sms) ? split : whole;
 }
 
 // Walks the non-empty units in order (query tile descending, sequence, head);
