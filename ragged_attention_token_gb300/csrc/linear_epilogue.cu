@@ -20,7 +20,8 @@
 // rounds over the pairs take the least time, the last round cut finer where it leaves pairs idle.
 //
 // linear_mid_kernel: tens to hundreds of rows (a token of each sequence of a large
-// batch), or few outputs over a long K, by the rule at launch_typed.  The work is still the read of W, so W is the product's M operand (128 of its rows by all
+// batch), or few outputs over a long K, by the rule at launch_typed.  The work is
+// still the read of W, so W is the product's M operand (128 of its rows by up to 256
 // rows of a): with a as the M operand its 128 rows are read from shared memory for
 // every 64 columns of W, 320 cycles for each 8 KB of W a pair streams (64 x 4096 x
 // 4096: 16.6 us, here 11.2).  A cluster of up to 8 CTAs shares K of a tile, TMA rings of 192 KB keeping W on
@@ -440,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         const int cols = m0 < T ? min(width, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
         // The tile's partial products, into registers: the sum of those before the last, fp32 outputs only.
         constexpr int SUMS = PARTS ? LN_PARTS / CPP / 2 : 1;
-        float sum[SUMS][CPP]={};
+        float sum[SUMS][CPP] = {};
         for (int part = 0; part + 1 < parts && !bad; ++part, ++i) {
           if (!mbar_wait_or_abort(bar(LB_ACC_FULL, i & 1), (i >> 1) & 1, abort_flag)) bad = true;
           bad = __any_sync(0xffffffffu, bad);
