@@ -542,7 +542,8 @@ RRA_API rra_status rra_qk_norm_rope(const void* q, long long q_stride, const voi
  * product.  A length above
  * max_seqlen records RRA_DEVERR_SEQ_TOO_LONG, a decreasing cu_seqlens
  * RRA_DEVERR_SEQ_NEGATIVE, rows outside [0, cap] RRA_DEVERR_INDEX_RANGE; such
- * a sequence is not written. */
+ * a sequence is not written.  A call repeated gives the same bits; the order of a
+ * row's sums may differ between calls of other B, cap, max_seqlen or heads. */
 RRA_API rra_status rra_attend_prompt(const void* q, long long q_stride, const void* k, long long k_stride,
                                      const void* v, long long v_stride, const int32_t* cu_seqlens, int B, int cap,
                                      int max_seqlen, int Hq, int Hkv, int d, float scale, int causal,
