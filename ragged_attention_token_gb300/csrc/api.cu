@@ -965,7 +965,7 @@ rra_status rra_attend_gather(const void* q, const void* k, const void* v, const 
   RRA_TRY(check_shape(B, N, H, d));
   if (!valid_in(in_dtype)) return fail(RRA_ERR_INVALID_ARG, "input dtype invalid");
   if (!valid_out(out_dtype)) return fail(RRA_ERR_INVALID_ARG, "output dtype invalid");
-  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
+  if (!finite(scale)) return fail(RRA_ERR_INVALID_ARG, "scale is not finite");
   RRA_CHECK_PTR(q);
   RRA_CHECK_PTR(k);
   RRA_CHECK_PTR(v);
