@@ -593,8 +593,13 @@ constexpr uint32_t M_W_BYTES = 128 * 128;
 constexpr uint32_t M_OFF_BAR = M_RING_BYTES;
 constexpr uint32_t MB_FULL = 0, MB_EMPTY = 8 * M_MAX_STAGES, MB_DONE = 16 * M_MAX_STAGES;
 constexpr uint32_t MW_TMEM = MB_DONE + 8, MW_ABORT = MW_TMEM + 4;
+constexpr uint32_t MB_ACC_FULL = MW_ABORT + 4, MB_ACC_EMPTY = MB_ACC_FULL + 32;   // [4] each, fp32 outputs
+static_assert(MB_ACC_FULL % 8 == 0 && MB_ACC_EMPTY + 32 <= 256, "barriers behind the ring");
 constexpr uint32_t M_SMEM = M_OFF_BAR + 256;
-constexpr int M_TMEM_COLS = 512;                         // accumulators of 128 (or 256) columns that share K, see L_PART
+// Accumulators of 128 (or 256) columns that share K.  fp32 outputs (see L_PART): parts of 8 chunks take them in turn, and
+// the epilogue warps add each finished part to their sums in registers while the next ones run (256 rows of 16384 -> 4096
+// 37.5 us; 16-bit outputs 37.2).  16-bit outputs: one part of K each, added at the end.
+constexpr int M_TMEM_COLS = 512;
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -633,6 +638,7 @@ template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(M_THREADS, 1)
     linear_mid_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                       const LinearEpiArgs a, int act, int splits, int row_step) {
+  constexpr bool PARTS = sizeof(Tout) == 4;
   extern __shared__ __align__(1024) uint8_t smem_mid[];
   const uint32_t base = smem_u32(smem_mid), bars = base + M_OFF_BAR;
   auto bar = [&](uint32_t kind, uint32_t i) { return bars + kind + 8 * i; };
@@ -651,6 +657,12 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       mbar_init(bar(MB_EMPTY, s), 1);
     }
     mbar_init(bar(MB_DONE, 0), 1);
+    if constexpr (PARTS) {
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(bar(MB_ACC_FULL, i), 1);
+        mbar_init(bar(MB_ACC_EMPTY, i), M_THREADS / 32 - 2);
+      }
+    }
     st_shared_u32(abort_flag, 0u);
     fence_barrier_init();
     prefetch_tensormap(&map_a);
@@ -671,7 +683,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   const int k_from = static_cast<int>(static_cast<long long>(kchunks) * rank / splits);
   const int k_to = rows > 0 ? static_cast<int>(static_cast<long long>(kchunks) * (rank + 1) / splits) : k_from;
   const int part_cols = cols > 128 ? 256 : 128;
-  const int parts = min(M_TMEM_COLS / part_cols, max(1, (k_to - k_from + L_PART - 1) / L_PART));
+  const int slots = M_TMEM_COLS / part_cols, wanted = max(1, (k_to - k_from + L_PART - 1) / L_PART);
+  const int parts = PARTS ? wanted : min(slots, wanted);
   const int per_part = (k_to - k_from + parts - 1) / parts;
   bool bad = false;
   if (warp == 0) {
@@ -700,19 +713,30 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 128, cols);
       const uint64_t dw0 = sdesc(base, 16, 1024), dx0 = sdesc(base + M_W_BYTES, 16, 1024);
       uint32_t s = 0, lap = 0;
+      int slot = 0, turn = 0, at = 0;                    // accumulator, times round them, chunks of its part so far
       for (int kc = k_from; kc < k_to; ++kc) {
         if (!mbar_wait_or_abort(bar(MB_FULL, s), lap & 1, abort_flag)) {
           bad = true;
           break;
         }
+        if (PARTS && at == 0 && turn > 0 && !mbar_wait_or_abort(bar(MB_ACC_EMPTY, slot), (turn - 1) & 1, abort_flag)) {
+          bad = true;
+          break;
+        }
         tc_fence_after();
         const uint64_t off = s * (stage_bytes >> 4);
-        const int part = (kc - k_from) / per_part;
-        const bool first = (kc - k_from) % per_part == 0;
 #pragma unroll
         for (int kk = 0; kk < LK / 16; ++kk)
-          umma_f16(tmem + part * part_cols, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+          umma_f16(tmem + slot * part_cols, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, (at > 0 || kk > 0) ? 1u : 0u);
         umma_commit(bar(MB_EMPTY, s));
+        if (++at == per_part || kc + 1 == k_to) {
+          if (PARTS) umma_commit(bar(MB_ACC_FULL, slot));
+          at = 0;
+          if (++slot == slots) {
+            slot = 0;
+            ++turn;
+          }
+        }
         if (++s == stages) {
           s = 0;
           ++lap;
@@ -721,6 +745,35 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       if (!bad) umma_commit(bar(MB_DONE, 0));
     }
     bad = __any_sync(0xffffffffu, bad);
+  }
+  // fp32: this warp's share of each part, as it finishes, into sums: rows of W by lane, 16 rows of a at 32 y.
+  float sum[PARTS ? M_ROWS / 32 : 1][16] = {};
+  const int half16 = ((warp - 2) >> 2) * 16;
+  if (PARTS && warp >= 2) {
+    const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half16;
+    int slot = 0, turn = 0;
+    for (int k = k_from; k < k_to; k += per_part) {
+      if (!mbar_wait_or_abort(bar(MB_ACC_FULL, slot), turn & 1, abort_flag)) bad = true;
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad) break;
+      tc_fence_after();
+#pragma unroll
+      for (int y = 0; y < M_ROWS / 32; ++y) {
+        if (half16 + 32 * y < cols) {
+          float x[16];
+          tmem_ld16(at + slot * part_cols + 32 * y, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[PARTS ? y : 0][i] += x[i];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(MB_ACC_EMPTY, slot));
+      if (++slot == slots) {
+        slot = 0;
+        ++turn;
+      }
+    }
   }
   // Every warp: the products are done (and with them every copy has been read).
   if (!bad && !mbar_wait_or_abort(bar(MB_DONE, 0), 0, abort_flag)) bad = true;
@@ -741,7 +794,17 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   if (warp >= 2 && !aborted && k_from < k_to) {
     tc_fence_after();
     const int quad = warp & 3, n = quad * 32 + lane;
-    for (int j = ((warp - 2) >> 2) * 16; j < cols; j += 32) {
+    if constexpr (PARTS) {
+#pragma unroll
+      for (int y = 0; y < M_ROWS / 32; ++y) {
+        if (half16 + 32 * y < cols) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            st_shared_u32(base + static_cast<uint32_t>((half16 + 32 * y + i) * 128 + n) * 4u, __float_as_uint(sum[y][i]));
+        }
+      }
+    }
+    for (int j = half16; !PARTS && j < cols; j += 32) {
       float v[16];
       tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + j, v);
       for (int p = 1; p < parts && p * per_part < k_to - k_from; ++p) {
