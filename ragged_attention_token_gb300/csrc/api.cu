@@ -9,7 +9,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "common.cuh"
+#include "block.cuh"
 
 namespace rra {
 namespace {

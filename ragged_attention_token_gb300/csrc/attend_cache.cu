@@ -23,7 +23,7 @@
 // Rows of the cache from kv_len on are not read: the copies fill their places with zeros.
 #include <mutex>
 
-#include "common.cuh"
+#include "block.cuh"
 #include "tc_ptx.cuh"
 #include "softmax_tc.cuh"
 

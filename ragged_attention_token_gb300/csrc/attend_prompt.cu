@@ -45,7 +45,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "common.cuh"
+#include "block.cuh"
 #include "tc_ptx.cuh"
 #include "softmax_tc.cuh"
 

@@ -38,7 +38,7 @@
 // TMEM and returns.
 #include <mutex>
 
-#include "common.cuh"
+#include "block.cuh"
 #include "f32x2.cuh"
 #include "tc_ptx.cuh"
 

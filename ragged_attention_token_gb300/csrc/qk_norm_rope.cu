@@ -19,7 +19,7 @@
 // sum of two floats (Dekker's product, by fma), times the position (exact in
 // fp32 below 2^24) again as two floats, minus the nearest integer.  The
 // remainder in [-1/2, 1/2] turns is good to about 2^-24 of a turn.
-#include "common.cuh"
+#include "block.cuh"
 #include "f32x2.cuh"
 
 namespace rra {
