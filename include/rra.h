@@ -564,8 +564,9 @@ RRA_API rra_status rra_attend_cache(const void* q, long long q_stride, const voi
                                     const int32_t* kv_len, int B, int nq, int cap, int Hq, int Hkv, int d,
                                     float scale, rra_dtype dtype, void* o, void* stream);
 
-/* Bound, in clock cycles, on any one on-chip wait of the image attention's tcgen05
- * kernels (0, the initial value: about one second, which every other kernel keeps).  A wait that runs out
+/* Bound, in clock cycles, on any one on-chip wait of the tcgen05 kernels of the image
+ * attention, rra_linear_epilogue and rra_attend_prompt (0, the initial value: about one second,
+ * which rra_linear_packed's kernel always keeps).  A wait that runs out
  * makes the CTA record RRA_DEVERR_WAIT_TIMEOUT, give its own copies and
  * products a short grace period, release its tensor memory and return, its
  * output incomplete; the device stays usable.  A test hook for that failure

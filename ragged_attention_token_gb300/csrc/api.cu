@@ -23,7 +23,7 @@ thread_local char g_last_message[256] = "";
 // rra_bind_error_word: the error word of this host thread's launches (null:
 // the device's own word).
 thread_local int32_t* g_bound_error_word = nullptr;
-// rra_set_wait_limit: the attention kernels' bound on one on-chip wait, in
+// rra_set_wait_limit: the tcgen05 kernels' bound on one on-chip wait, in
 // clock cycles (0: the kernels' default).
 std::atomic<long long> g_wait_limit{0};
 std::atomic<uint64_t> g_launches{0};
@@ -682,6 +682,7 @@ rra_status rra_linear_epilogue(const void* a, const void* w, const float* bias, 
   g.residual = residual;
   g.c = c;
   g.err = error_word(*st);
+  g.wait_limit = g_wait_limit.load();
   cudaError_t e = launch_linear_epilogue(g, in_dtype, out_dtype, act, st->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "linear_epilogue launch");
   g_launches += 1;
@@ -816,6 +817,7 @@ rra_status rra_attend_prompt(const void* q, long long q_stride, const void* k, l
   g.causal = causal != 0;
   g.o = o;
   g.err = error_word(*st);
+  g.wait_limit = g_wait_limit.load();
   cudaError_t e = launch_attend_prompt(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "attend_prompt launch");
   g_launches += 1;

@@ -294,7 +294,8 @@ __device__ __forceinline__ float prompt_weights(uint32_t tP, const float (&s)[PT
   return a0 + a1;
 }
 
-template <typename T, int D, bool SPLIT>
+// LIMIT: the instantiation of launches made with a wait limit set (rra_set_wait_limit).
+template <typename T, int D, bool SPLIT, bool LIMIT>
 __global__ void __launch_bounds__(P_THREADS, 1)
     attend_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   bool bad = false;
   // A bounded wait; every lane of the warp leaves with the same `bad`.
   auto wait = [&](uint32_t b, uint32_t parity) {
-    if (!mbar_wait_or_abort(b, parity, abort_flag)) bad = true;
+    if (!mbar_wait_limited<LIMIT>(b, parity, abort_flag, a.wait_limit)) bad = true;
     bad = __any_sync(0xffffffffu, bad);
     return !bad;
   };
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       // 95 to 150 cycles a product (against 64 of the tensor core).
       if (elect_one()) {
         auto wait1 = [&](uint32_t b, uint32_t parity) {
-          if (!mbar_wait_or_abort(b, parity, abort_flag)) bad = true;
+          if (!mbar_wait_limited<LIMIT>(b, parity, abort_flag, a.wait_limit)) bad = true;
           return !bad;
         };
         const uint32_t idesc_s = idesc_f16(BF ? 1u : 0u, 0, PT, PT);
@@ -806,10 +807,10 @@ cudaError_t make_map_rows(CUtensorMap* map, const void* ptr, int rows, int H, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int D, bool SPLIT>
+template <typename T, int D, bool SPLIT, bool LIMIT>
 cudaError_t launch_shape(const PromptArgs& a, const UnitShape& us, int num_sms, cudaStream_t stream) {
   using C = PromptCfg<D>;
-  auto kernel = attend_prompt_kernel<T, D, SPLIT>;
+  auto kernel = attend_prompt_kernel<T, D, SPLIT, LIMIT>;
   constexpr int kMaxDevices = 64;
   static bool attr_set[kMaxDevices] = {};
   static std::mutex m;
@@ -845,10 +846,16 @@ cudaError_t launch_shape(const PromptArgs& a, const UnitShape& us, int num_sms, 
   return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
 }
 
+template <typename T, int D, bool LIMIT>
+cudaError_t launch_lim(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+  const UnitShape us = prompt_shape(a, D, num_sms);
+  return us.split ? launch_shape<T, D, true, LIMIT>(a, us, num_sms, stream)
+                  : launch_shape<T, D, false, LIMIT>(a, us, num_sms, stream);
+}
+
 template <typename T, int D>
 cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  const UnitShape us = prompt_shape(a, D, num_sms);
-  return us.split ? launch_shape<T, D, true>(a, us, num_sms, stream) : launch_shape<T, D, false>(a, us, num_sms, stream);
+  return a.wait_limit > 0 ? launch_lim<T, D, true>(a, num_sms, stream) : launch_lim<T, D, false>(a, num_sms, stream);
 }
 
 }  // namespace

@@ -2,7 +2,7 @@
 // recorded DRAM bytes to a hash of that kernel's source and headers, which this one does not belong to.
 #pragma once
 
-#include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace rra {
 
@@ -15,6 +15,18 @@ __device__ __forceinline__ void dependent_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A bounded wait: by the default bound, or, in the kernels for launches made with a limit set (rra_set_wait_limit), by
+// that one, polling, so that a bound below the hardware's suspension of a wait holds too.
+template <bool LIMIT>
+__device__ __forceinline__ bool mbar_wait_limited(uint32_t bar, uint32_t parity, uint32_t abort_flag, long long limit) {
+  if constexpr (!LIMIT) return mbar_wait_or_abort(bar, parity, abort_flag);
+  const long long t0 = clock64();
+  while (!mbar_test_wait(bar, parity)) {
+    if (ld_shared_volatile_u32(abort_flag) != 0u || clock64() - t0 > limit) return false;
+  }
+  return true;
+}
+
 // Linear layer with its epilogue: c = act(a W^T + bias) + residual for the T = cu[B] rows.
 struct LinearEpiArgs {
   const int32_t* cu;
@@ -25,6 +37,7 @@ struct LinearEpiArgs {
   const void* residual;    // [cap, N] of the output type, or null; may be c
   void* c;
   int32_t* err;
+  long long wait_limit;    // clock cycles one on-chip wait may take before giving up (0: the default)
 };
 cudaError_t launch_linear_epilogue(const LinearEpiArgs& a, rra_dtype in, rra_dtype out, rra_activation act,
                                    int num_sms, cudaStream_t stream);
@@ -57,6 +70,7 @@ struct PromptArgs {
   int causal;
   void* o;
   int32_t* err;
+  long long wait_limit;                    // as above
 };
 cudaError_t launch_attend_prompt(const PromptArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream);
 

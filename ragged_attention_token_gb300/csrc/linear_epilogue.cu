@@ -296,7 +296,8 @@ __device__ __forceinline__ void piece_at(const Tiling& g, long long t, int N, in
 
 // PARTS: fp32 outputs of K above one part.  A kernel of its own: the registers of the sums cost the
 // one-part epilogue half its speed (SiLU on 7078 rows of 512 -> 3600: 78.9 against 39.5 us).
-template <typename Tin, typename Tout, bool PARTS>
+// LIMIT: the instantiation of launches made with a wait limit set (rra_set_wait_limit).
+template <typename Tin, typename Tout, bool PARTS, bool LIMIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w128,
                        const __grid_constant__ CUtensorMap map_w64, const __grid_constant__ CUtensorMap map_w32,
@@ -361,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           const CUtensorMap* mw = width == 256 ? &map_w128 : (width == 128 ? &map_w64 : &map_w32);
           const uint32_t bytes = 2 * (L_A_BYTES + static_cast<uint32_t>(width / 2) * 128u);
           for (int kc = 0; kc < kchunks; ++kc) {
-            if (lap > 0 && !mbar_wait_or_abort(bar(LB_EMPTY, s), (lap - 1) & 1, abort_flag)) {
+            if (lap > 0 && !mbar_wait_limited<LIMIT>(bar(LB_EMPTY, s), (lap - 1) & 1, abort_flag, a.wait_limit)) {
               bad = true;
               break;
             }
@@ -389,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, width);
           for (int part = 0; part < parts && !bad; ++part, ++i) {
             const uint32_t b = i & 1;
-            if (i >= 2 && !mbar_wait_or_abort(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag)) {
+            if (i >= 2 && !mbar_wait_limited<LIMIT>(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag, a.wait_limit)) {
               bad = true;
               break;
             }
@@ -397,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
             const uint32_t acc = tmem + b * LN_MAX;
             const int k_from = part * L_PART, k_to = PARTS ? min(kchunks, k_from + L_PART) : kchunks;
             for (int kc = k_from; kc < k_to; ++kc) {
-              if (!mbar_wait_or_abort(bar(LB_FULL, s), lap & 1, abort_flag)) {
+              if (!mbar_wait_limited<LIMIT>(bar(LB_FULL, s), lap & 1, abort_flag, a.wait_limit)) {
                 bad = true;
                 break;
               }
@@ -443,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         constexpr int SUMS = PARTS ? LN_PARTS / CPP / 2 : 1;
         float sum[SUMS][CPP] = {};
         for (int part = 0; part + 1 < parts && !bad; ++part, ++i) {
-          if (!mbar_wait_or_abort(bar(LB_ACC_FULL, i & 1), (i >> 1) & 1, abort_flag)) bad = true;
+          if (!mbar_wait_limited<LIMIT>(bar(LB_ACC_FULL, i & 1), (i >> 1) & 1, abort_flag, a.wait_limit)) bad = true;
           bad = __any_sync(0xffffffffu, bad);
           if (bad) break;
           tc_fence_after();
@@ -464,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         }
         if (bad) break;
         const uint32_t b = i & 1;
-        if (!mbar_wait_or_abort(bar(LB_ACC_FULL, b), (i >> 1) & 1, abort_flag)) bad = true;
+        if (!mbar_wait_limited<LIMIT>(bar(LB_ACC_FULL, b), (i >> 1) & 1, abort_flag, a.wait_limit)) bad = true;
         bad = __any_sync(0xffffffffu, bad);
         if (bad) break;
         tc_fence_after();
@@ -634,7 +635,7 @@ __device__ __forceinline__ void finish4(T* c, const T* residual, float4 v) {
 }
 
 // One cluster: `row_step` rows by 128 columns of c; its CTAs share K.  D[n, t] = sum_k W[n, k] a[t, k].
-template <typename Tin, typename Tout>
+template <typename Tin, typename Tout, bool LIMIT>
 __global__ void __launch_bounds__(M_THREADS, 1)
     linear_mid_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                       const LinearEpiArgs a, int act, int splits, int row_step) {
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     if (elect_one()) {
       uint32_t s = 0, lap = 0;
       for (int kc = k_from; kc < k_to; ++kc) {
-        if (lap > 0 && !mbar_wait_or_abort(bar(MB_EMPTY, s), (lap - 1) & 1, abort_flag)) {
+        if (lap > 0 && !mbar_wait_limited<LIMIT>(bar(MB_EMPTY, s), (lap - 1) & 1, abort_flag, a.wait_limit)) {
           bad = true;
           break;
         }
@@ -715,11 +716,11 @@ __global__ void __launch_bounds__(M_THREADS, 1)
       uint32_t s = 0, lap = 0;
       int slot = 0, turn = 0, at = 0;                    // accumulator, times round them, chunks of its part so far
       for (int kc = k_from; kc < k_to; ++kc) {
-        if (!mbar_wait_or_abort(bar(MB_FULL, s), lap & 1, abort_flag)) {
+        if (!mbar_wait_limited<LIMIT>(bar(MB_FULL, s), lap & 1, abort_flag, a.wait_limit)) {
           bad = true;
           break;
         }
-        if (PARTS && at == 0 && turn > 0 && !mbar_wait_or_abort(bar(MB_ACC_EMPTY, slot), (turn - 1) & 1, abort_flag)) {
+        if (PARTS && at == 0 && turn > 0 && !mbar_wait_limited<LIMIT>(bar(MB_ACC_EMPTY, slot), (turn - 1) & 1, abort_flag, a.wait_limit)) {
           bad = true;
           break;
         }
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half16;
     int slot = 0, turn = 0;
     for (int k = k_from; k < k_to; k += per_part) {
-      if (!mbar_wait_or_abort(bar(MB_ACC_FULL, slot), turn & 1, abort_flag)) bad = true;
+      if (!mbar_wait_limited<LIMIT>(bar(MB_ACC_FULL, slot), turn & 1, abort_flag, a.wait_limit)) bad = true;
       bad = __any_sync(0xffffffffu, bad);
       if (bad) break;
       tc_fence_after();
@@ -776,7 +777,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     }
   }
   // Every warp: the products are done (and with them every copy has been read).
-  if (!bad && !mbar_wait_or_abort(bar(MB_DONE, 0), 0, abort_flag)) bad = true;
+  if (!bad && !mbar_wait_limited<LIMIT>(bar(MB_DONE, 0), 0, abort_flag, a.wait_limit)) bad = true;
   bad = __any_sync(0xffffffffu, bad);
   if (bad && lane == 0) {
     st_shared_u32(abort_flag, 1u);
@@ -1048,7 +1049,7 @@ cudaLaunchConfig_t dependent_config(cudaLaunchAttribute* attr, int grid, int thr
   return cfg;
 }
 
-// Once per device and kernel (the template arguments name the kernel): its dynamic shared memory.
+// Once per device and kernel (the template arguments name the kernel; NT: groups of rows, or below 0 the kernel's variant): its dynamic shared memory.
 template <typename Tin, typename Tout, int NT, typename K>
 cudaError_t allow_smem(K kernel, int bytes) {
   constexpr int kMaxDevices = 64;
@@ -1067,11 +1068,11 @@ cudaError_t allow_smem(K kernel, int bytes) {
   return cudaSuccess;
 }
 
-template <typename Tin, typename Tout, bool PARTS>
+template <typename Tin, typename Tout, bool PARTS, bool LIMIT>
 cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
-  auto kernel = linear_pair_kernel<Tin, Tout, PARTS>;
-  cudaError_t e = allow_smem<Tin, Tout, PARTS ? -2 : 0>(kernel, L_SMEM);
+  auto kernel = linear_pair_kernel<Tin, Tout, PARTS, LIMIT>;
+  cudaError_t e = allow_smem<Tin, Tout, -1 - PARTS - 2 * LIMIT>(kernel, L_SMEM);
   if (e != cudaSuccess) return e;
   const bool bf16 = IsBf16<Tin>::value == 1;
   CUtensorMap ma, mw[3];
@@ -1107,11 +1108,11 @@ MidCut cut_mid(const LinearEpiArgs& a, int num_sms) {
   return m;
 }
 
-template <typename Tin, typename Tout>
+template <typename Tin, typename Tout, bool LIMIT>
 cudaError_t launch_mid(const LinearEpiArgs& a, int act, const MidCut& cut, cudaStream_t stream) {
   if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
-  auto kernel = linear_mid_kernel<Tin, Tout>;
-  cudaError_t e = allow_smem<Tin, Tout, -1>(kernel, M_SMEM);
+  auto kernel = linear_mid_kernel<Tin, Tout, LIMIT>;
+  cudaError_t e = allow_smem<Tin, Tout, -5 - LIMIT>(kernel, M_SMEM);
   if (e != cudaSuccess) return e;
   const bool bf16 = IsBf16<Tin>::value == 1;
   CUtensorMap ma, mw;
@@ -1136,20 +1137,26 @@ cudaError_t launch_few(const LinearEpiArgs& a, int act, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, a, act);
 }
 
-template <typename Tin, typename Tout>
-cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
-  if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
-  if (a.cap <= 16) return launch_few<Tin, Tout, 2>(a, act, stream);
+template <typename Tin, typename Tout, bool LIMIT>
+cudaError_t launch_tiles(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   // The way that takes less, by the shared memory that the products read in turn (make_tiling's cost for pairs).
   // 4096 x 4096: 64 rows 11.2 us with W as the M operand against 16.6, 200 rows 15.6 / 16.1, 256 rows 17.4 / 16.3; 768 x
   // 2304: 64 rows 5.8 / 6.1, 128 rows 7.0 / 6.2; 16384 x 4096: 256 rows 36.7 / 48.3; 7440 x 72: 392 rows 12.4 / 23.8.
   // (Only where all of its clusters run at once: further rounds repeat a cluster's set-up.)
   const MidCut cut = cut_mid(a, num_sms);
   const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * ((a.K + LK - 1) / LK);
-  if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) return launch_mid<Tin, Tout>(a, act, cut, stream);
+  if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) return launch_mid<Tin, Tout, LIMIT>(a, act, cut, stream);
   if constexpr (sizeof(Tout) == 4)
-    if (a.K > L_PART * LK) return launch_pair<Tin, Tout, true>(a, act, num_sms, stream);
-  return launch_pair<Tin, Tout, false>(a, act, num_sms, stream);
+    if (a.K > L_PART * LK) return launch_pair<Tin, Tout, true, LIMIT>(a, act, num_sms, stream);
+  return launch_pair<Tin, Tout, false, LIMIT>(a, act, num_sms, stream);
+}
+
+template <typename Tin, typename Tout>
+cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
+  if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
+  if (a.cap <= 16) return launch_few<Tin, Tout, 2>(a, act, stream);
+  return a.wait_limit > 0 ? launch_tiles<Tin, Tout, true>(a, act, num_sms, stream)
+                          : launch_tiles<Tin, Tout, false>(a, act, num_sms, stream);
 }
 
 template <typename Tin>
