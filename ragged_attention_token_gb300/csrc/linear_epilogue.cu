@@ -33,9 +33,9 @@
 // in shared memory.  The K order inside a 32-wide step is the one in which the 16-byte
 // loads arrive, the same for both operands (a dot product does not mind).
 //
-// Every wait is bounded; a CTA that gives up tells its peer, records
+// Every wait is bounded; a CTA that gives up tells its peer or its cluster, records
 // RRA_DEVERR_WAIT_TIMEOUT, lets copies and products in flight land, frees its
-// TMEM and returns.
+// TMEM and returns; what its tile lacks then is not written.
 #include <mutex>
 
 #include "block.cuh"
@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");   // this CTA's words are set; waited for ahead of the join
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
   dependent_launch();
@@ -820,11 +821,15 @@ __global__ void __launch_bounds__(M_THREADS, 1)
     tc_fence_before();
   }
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (aborted && tid < splits) st_cluster_u32(map_rank(abort_flag, static_cast<uint32_t>(tid)), 1u);
+  __syncwarp();
   cluster_sync_all();
   // Four neighbouring outputs a thread, two such at a time, the cluster's rows
-  // shared out, sums in rank order.
+  // shared out, sums in rank order.  Where a CTA gave up, its ring holds no sums: the tile is not written.
   const int step = splits * M_THREADS;
-  for (int e0 = rank * M_THREADS + tid; !aborted && e0 < rows * 32; e0 += 2 * step) {
+  const bool gave_up = ld_shared_volatile_u32(abort_flag) != 0u;
+  for (int e0 = rank * M_THREADS + tid; !gave_up && e0 < rows * 32; e0 += 2 * step) {
     float4 y[2][M_SPLIT];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {

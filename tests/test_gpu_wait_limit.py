@@ -88,3 +88,21 @@ def test_what_a_call_that_gave_up_wrote_is_right(name):
         seen.add(_limited(call, cycles))
         assert bool(((out == want) | torch.isnan(out)).all()), cycles
     assert rra.DEVERR_WAIT_TIMEOUT in seen
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n.startswith("mid")])
+def test_no_cta_joins_the_sums_of_one_that_gave_up(name):
+    """A cluster shares K of a tile: where one of its CTAs gave up, the tile is as it was.  The limits go past the time
+    of the whole call, and memory traffic ahead of each call spreads the CTAs' times, so that some clusters end in parts."""
+    out, call = CALLS[name]()
+    call()
+    torch.cuda.synchronize()
+    want = out.clone()
+    busy = torch.zeros(1 << 26, device="cuda")
+    seen = set()
+    for cycles in range(5000, 60000, 250):
+        out.fill_(float("nan"))
+        busy.add_(1.0)
+        seen.add(_limited(call, cycles))
+        assert bool(((out == want) | torch.isnan(out)).all()), cycles
+    assert seen == {0, rra.DEVERR_WAIT_TIMEOUT}
