@@ -566,7 +566,8 @@ RRA_API rra_status rra_attend_cache(const void* q, long long q_stride, const voi
 
 /* Bound, in clock cycles, on any one on-chip wait of the tcgen05 kernels of the image
  * attention, rra_linear_epilogue and rra_attend_prompt (0, the initial value: about one second,
- * which rra_linear_packed's kernel always keeps).  A wait that runs out
+ * which rra_linear_packed's kernel always keeps).  A wait of rra_attend_prompt that lasts as long as the
+ * other warps' walk over a sequence's keys has the limit for each 128 of them.  A wait that runs out
  * makes the CTA record RRA_DEVERR_WAIT_TIMEOUT, give its own copies and
  * products a short grace period, release its tensor memory and return, its
  * output incomplete; the device stays usable.  A test hook for that failure

@@ -64,6 +64,9 @@ constexpr int P_REGS_SOFTMAX = 200, P_REGS_OTHER = 104;
 static_assert(8 * P_REGS_SOFTMAX + 4 * P_REGS_OTHER <= 12 * 168, "register split exceeds the launch's registers");
 constexpr uint32_t P_TMEM_COLS = 512;
 constexpr uint32_t P_SUB = PT * 128;         // one 64-element column group of a tile: 128 rows x 128 B
+// Bound on a wait that lasts a whole unit, of up to 2^23 blocks (the loading and the product warp, whose waits
+// are of single steps, keep the usual one, and the flag they set ends this one too).
+constexpr long long P_UNIT_WAIT_CYCLES = 1LL << 36;
 constexpr float P_MOVE = 8.f;                // log2 units by which a maximum may exceed the reference
 
 template <int D>
@@ -352,6 +355,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     bad = __any_sync(0xffffffffu, bad);
     return !bad;
   };
+  // A wait that may last a whole unit: of the warp for the tails, and of the softmax warps of a tile
+  // without rows for the next unit.
+  auto wait_unit = [&](uint32_t b, uint32_t parity) {
+    if (!mbar_wait_limited<LIMIT, P_UNIT_WAIT_CYCLES>(b, parity, abort_flag, a.unit_wait_limit)) bad = true;
+    bad = __any_sync(0xffffffffu, bad);
+    return !bad;
+  };
   auto read_unit = [&](int i) {
     const uint32_t d = bars + P_DESC + 32u * static_cast<uint32_t>(i & 1);
     PromptUnit u;
@@ -423,14 +433,14 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       // block over once it has landed and gets it back before its P V.
       uint32_t kv0 = 0, done = 0;
       for (int i = 0;; ++i) {
-        if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
+        if (!wait_unit(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
         const PromptUnit u = read_unit(i);
         if (u.q0 < 0) break;
         const int nb = u.blocks(us, a.causal);
         const int keys = min(PT, u.n - (nb - 1) * PT), pad = -keys & 15;
         kv0 += 2 * static_cast<uint32_t>(nb);
         if (pad > 0) {
-          if (!wait(bar(PB_TAIL, 0), done & 1)) break;
+          if (!wait_unit(bar(PB_TAIL, 0), done & 1)) break;
           ++done;
           const uint32_t sv = s_kv(static_cast<int>((kv0 - 1) % C::SLOTS)) + keys * 128;
           for (int z = lane; z < pad * 8 * (D / 64); z += 32) {
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint32_t count = 0;                     // blocks of this tile so far
     uint32_t joins = 0;                     // units joined so far
     for (int i = 0;; ++i) {
-      if (!wait(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
+      if (!wait_unit(bar(PB_U_FULL, i & 1), (i >> 1) & 1)) break;
       const PromptUnit u = read_unit(i);
       if (u.q0 < 0) break;
       const int nbw = u.blocks(w, us, a.causal), last = (SPLIT ? u.seen(w, us, a.causal) : nbw) - 1;
@@ -854,7 +864,9 @@ cudaError_t launch_lim(const PromptArgs& a, int num_sms, cudaStream_t stream) {
 }
 
 template <typename T, int D>
-cudaError_t launch_d(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_d(PromptArgs a, int num_sms, cudaStream_t stream) {
+  const long long each = std::min(a.wait_limit > 0 ? a.wait_limit : WAIT_LIMIT_CYCLES, 1LL << 38);
+  a.unit_wait_limit = each * (1 + std::min(a.max_seqlen, a.cap) / PT);          // at most 2^38 x 2^23
   return a.wait_limit > 0 ? launch_lim<T, D, true>(a, num_sms, stream) : launch_lim<T, D, false>(a, num_sms, stream);
 }
 

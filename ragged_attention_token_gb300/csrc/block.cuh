@@ -17,9 +17,9 @@ __device__ __forceinline__ void dependent_launch() {
 
 // A bounded wait: by the default bound, or, in the kernels for launches made with a limit set (rra_set_wait_limit), by
 // that one, polling, so that a bound below the hardware's suspension of a wait holds too.
-template <bool LIMIT>
+template <bool LIMIT, long long DEFAULT = WAIT_LIMIT_CYCLES>
 __device__ __forceinline__ bool mbar_wait_limited(uint32_t bar, uint32_t parity, uint32_t abort_flag, long long limit) {
-  if constexpr (!LIMIT) return mbar_wait_or_abort(bar, parity, abort_flag);
+  if constexpr (!LIMIT) return mbar_wait_or_abort(bar, parity, abort_flag, DEFAULT);
   const long long t0 = clock64();
   while (!mbar_test_wait(bar, parity)) {
     if (ld_shared_volatile_u32(abort_flag) != 0u || clock64() - t0 > limit) return false;
@@ -71,6 +71,7 @@ struct PromptArgs {
   void* o;
   int32_t* err;
   long long wait_limit;                    // as above
+  long long unit_wait_limit;               // the same for one that lasts a whole unit (set by the launch)
 };
 cudaError_t launch_attend_prompt(const PromptArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream);
 

@@ -106,3 +106,22 @@ def test_no_cta_joins_the_sums_of_one_that_gave_up(name):
         seen.add(_limited(call, cycles))
         assert bool(((out == want) | torch.isnan(out)).all()), cycles
     assert seen == {0, rra.DEVERR_WAIT_TIMEOUT}
+
+
+@pytest.mark.parametrize("n", [131064, 131072, 131073])
+@pytest.mark.parametrize("d,causal", [(64, False), (128, True)])
+def test_a_long_unit_is_no_long_wait(n, d, causal):
+    """The bound is for one wait of a block: a sequence whose units take longer than it (a unit walks over a thousand blocks
+    of keys, 2 to 4 million cycles) still passes, whether its last block of values ends in a tail or not (the warp
+    for the tails idles until then) and whether its last unit has rows for its second tile or not."""
+    out, call = _prompt([n], 1, 1, d, causal)
+    out.fill_(float("nan"))
+    rra.get_device_error(clear=True)
+    call()
+    torch.cuda.synchronize()
+    assert rra.get_device_error() == 0
+    want = out.clone()
+    assert bool(torch.isfinite(want.float()).all())
+    out.fill_(float("nan"))
+    assert _limited(call, 500000) == 0
+    assert torch.equal(out, want)
