@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2)
   const int G = a.Hq / a.Hkv;
   const int rows = min(C_ROWS, a.nq * G - rb * C_ROWS);            // row r: token r / G, head hk * G + r % G (r from rb * 16)
   dependent_launch();
-  const int len = __ldg(a.kv_len + b);
+  const int len = a.kv_len[b];
   const bool valid = len >= 0 && len <= a.cap;
   if (!valid && split == 0 && rb == 0 && hk == 0 && threadIdx.x == 0)
     record_error(a.err, len < 0 ? RRA_DEVERR_SEQ_NEGATIVE : RRA_DEVERR_SEQ_TOO_LONG);

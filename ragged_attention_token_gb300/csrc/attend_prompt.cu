@@ -171,8 +171,8 @@ struct UnitWalk {
   // Rows of sequence b, 0 for one that is not there or not valid (`record`: its code is recorded).
   __device__ int rows_of(const PromptArgs& a, int b, int& s0, int& n, bool record) const {
     if (b >= a.B) return 0;
-    s0 = __ldg(a.cu + b);
-    n = __ldg(a.cu + b + 1) - s0;
+    s0 = a.cu[b];
+    n = a.cu[b + 1] - s0;
     if (n < 0 || n > a.max_seqlen || s0 < 0 || s0 > a.cap - n) {
       if (record)
         record_error(a.err, n < 0 ? RRA_DEVERR_SEQ_NEGATIVE

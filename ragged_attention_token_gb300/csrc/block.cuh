@@ -10,6 +10,8 @@ namespace rra {
 // stream start its set-up as soon as every CTA of this one is running, then waits for the
 // kernels before it, which precedes every access to global memory.  Every CTA
 // calls it, so that no kernel completes before those it depends on.
+// The kernels run while those before them may still write what they read behind the wait, so they read it by ordinary loads:
+// __ldg is for memory that nothing writes as long as the kernel lives, and the compiler may move it ahead of the wait.
 __device__ __forceinline__ void dependent_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

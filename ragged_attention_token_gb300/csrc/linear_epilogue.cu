@@ -338,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
   dependent_launch();
-  const int T = __ldg(a.cu + a.B);
+  const int T = a.cu[a.B];
   bool bad = false;
   if (T < 0 || T > a.cap) {
     if (blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
@@ -430,8 +430,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
       float bias0 = 0.f, bias1 = 0.f;
       auto load_bias = [&](int col0) {
         if (a.bias == nullptr || col0 >= a.N) return;
-        bias0 = __ldg(a.bias + min(col0 + lane, a.N - 1));
-        if (CPP > 32) bias1 = __ldg(a.bias + min(col0 + 32 + lane, a.N - 1));
+        bias0 = a.bias[min(col0 + lane, a.N - 1)];
+        if (CPP > 32) bias1 = a.bias[min(col0 + 32 + lane, a.N - 1)];
       };
       for (long long t = pair; t < g.all; t += pairs) {
         int m0, n0, width;
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
   dependent_launch();
-  const int T = __ldg(a.cu + a.B);
+  const int T = a.cu[a.B];
   const bool valid = T >= 0 && T <= a.cap;
   if (!valid && blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
   const int rows = valid ? max(0, min(T - t0, row_step)) : 0, boxes = (rows + 31) / 32, cols = (rows + 15) & ~15;
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         }
       }
       if (a.bias != nullptr) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + n));
+        const float4 b = *reinterpret_cast<const float4*>(a.bias + n);
         v[0] += b.x;
         v[1] += b.y;
         v[2] += b.z;
@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   dependent_launch();
   // Needed at the end only: rows of a from T to cap are multiplied too (each gives its
   // own outputs, which are not stored), so that no copy waits for T.
-  const int T = __ldg(a.cu + a.B);
+  const int T = a.cu[a.B];
   const Tin* W = static_cast<const Tin*>(a.w);
   const Tin* X = static_cast<const Tin*>(a.a);
   // Rows past N repeat the last one, rows past cap are zeros: their results are not stored.
@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
     float v[1] = {0.f};
 #pragma unroll
     for (int w = 0; w < FEW_WARPS; ++w) v[0] += part[w][j][t];
-    if (a.bias != nullptr) v[0] += __ldg(a.bias + n);
+    if (a.bias != nullptr) v[0] += a.bias[n];
     activate(v, act);
     const size_t at = static_cast<size_t>(t) * a.N + n;
     if (a.residual != nullptr) v[0] += static_cast<float>(static_cast<const Tout*>(a.residual)[at]);

@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t from_f2(uint64_t v, __half) {
 }
 
 __device__ __forceinline__ void load_weights(const float* w, float* v) {
-  const float4 x = __ldg(reinterpret_cast<const float4*>(w)), y = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  const float4 x = *reinterpret_cast<const float4*>(w), y = reinterpret_cast<const float4*>(w)[1];
   v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
 }
 
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
   constexpr int U = RopeCfg<D>::UNROLL;
   const int lane = threadIdx.x & 31, p = lane % LPH, sub = lane / LPH;
   dependent_launch();
-  const int rows_used = __ldg(a.cu + a.B);
+  const int rows_used = a.cu[a.B];
   if (rows_used < 0 || rows_used > a.cap) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
     return;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
     }
     int pos = 0;
     if (a.positions != nullptr) {
-      pos = __ldg(a.positions + t);
+      pos = a.positions[t];
       if (pos < 0 || pos >= (1 << 24)) {
         if (lane == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
         continue;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
     }
     long long row = t;
     if (a.kv_rows != nullptr && to > full_q) {
-      row = __ldg(a.kv_rows + t);
+      row = a.kv_rows[t];
       if (row < 0 || row >= a.kv_out_rows) {
         if (lane == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
         row = -1;                                             // the token's queries are still written
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * R_WARPS, RopeCfg<D>::CTAS) qk_norm_rope_k
       for (int j = 0; j < OWN; ++j) {
         oc[j] = 1.f;
         os[j] = 0.f;
-        if (turned) rotation(static_cast<float>(pos), __ldg(a.inv_freq + 8 * p + sub * OWN + j), oc[j], os[j]);
+        if (turned) rotation(static_cast<float>(pos), a.inv_freq[8 * p + sub * OWN + j], oc[j], os[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
