@@ -4,7 +4,7 @@
 
 Each .cu file in csrc/ compiles to an object in parallel; the objects link
 into ragged_attention_token_gb300/librra.so against the shared CUDA runtime.
-csrc/fastcall.cpp becomes the Python extension _rra_fast.so beside it.  A rebuild happens only when a source or header is newer than the library.
+csrc/fastcall.cpp becomes a Python extension beside it (fast_path()).  A rebuild happens only when a source or header is newer than the library.
 """
 from __future__ import annotations
 
@@ -50,18 +50,25 @@ def _deps() -> list[str]:
 # The block operators' argument marshalling in C++ (a Python extension against
 # torch's headers).  Without it rra.py marshals those calls itself.
 FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
-FAST_PATH = os.path.join(PKG_DIR, "_rra_fast.so")
+
+
+def fast_path() -> str:
+    """Where the extension for this torch and this Python lies: one built against another is another file, never loaded here."""
+    import torch
+    return os.path.join(PKG_DIR, f"_rra_fast-torch{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 
 def _fast_up_to_date() -> bool:
+    path = fast_path()
     deps = [FAST_SRC, os.path.join(INCLUDE, "rra.h"), os.path.abspath(__file__)]
-    return os.path.exists(FAST_PATH) and all(os.path.getmtime(p) <= os.path.getmtime(FAST_PATH) for p in deps)
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
 
 
 def build_fast(verbose: bool = False, force: bool = False) -> str:
     """Compile the marshalling extension with the host compiler; returns its path."""
+    path = fast_path()
     if not force and _fast_up_to_date():
-        return FAST_PATH
+        return path
     import sysconfig
 
     import torch
@@ -69,13 +76,15 @@ def build_fast(verbose: bool = False, force: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(troot, "include"),
            os.path.join(troot, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    tmp = FAST_PATH + ".tmp"
+    tmp = path + ".tmp"
+    if os.path.exists(path):
+        os.remove(path)                    # should the build fail, an extension of older sources is not to be used
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[x for d in inc for x in ("-isystem", d)],
           FAST_SRC, "-o", tmp, "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"],
          verbose)
-    os.replace(tmp, FAST_PATH)
-    return FAST_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def up_to_date() -> bool:

@@ -8,10 +8,14 @@ Loading fails loudly when librra.so is missing -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
+import warnings
 
 import torch
+
+from . import build as _build
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "librra.so")
@@ -81,7 +85,7 @@ _SIGNATURES = {
 }
 
 _LIB = None
-# The block operators' marshalling in C++ (_rra_fast.so), or None: then this module marshals those calls.
+# The block operators' marshalling in C++ (csrc/fastcall.cpp), or None: then this module marshals those calls.
 _FAST = None
 
 
@@ -97,6 +101,22 @@ def header_symbols(path: str = HEADER_PATH) -> list[str]:
     return sorted(set(re.findall(r"RRA_API\s+[\w\s\*]*?\b(rra_\w+)\s*\(", text)))
 
 
+def _load_fast(L: ctypes.CDLL):
+    """The marshalling extension built for this torch and Python, bound to `L`; None, with a warning, without one."""
+    path = _build.fast_path()
+    try:
+        spec = importlib.util.spec_from_file_location("_rra_fast", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError as e:
+        warnings.warn(f"the block operators' calls are marshalled in Python, at three to four times the host time: {e}; "
+                      "`python -m ragged_attention_token_gb300.build` builds the extension", RuntimeWarning, stacklevel=3)
+        return None
+    mod.bind(*(ctypes.cast(getattr(L, f), _vp).value
+               for f in ("rra_linear_epilogue", "rra_qk_norm_rope", "rra_attend_prompt", "rra_attend_cache")))
+    return mod
+
+
 def lib() -> ctypes.CDLL:
     """Load librra.so once (raises if it has not been built)."""
     global _LIB, _FAST
@@ -109,14 +129,7 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        try:
-            from . import _rra_fast
-            _rra_fast.bind(*(ctypes.cast(getattr(L, f), _vp).value
-                             for f in ("rra_linear_epilogue", "rra_qk_norm_rope", "rra_attend_prompt",
-                                       "rra_attend_cache")))
-            _FAST = _rra_fast
-        except ImportError:
-            pass
+        _FAST = _load_fast(L)
         _LIB = L
     return _LIB
 
@@ -348,7 +361,7 @@ def _typed(t, dtype, name: str, shape, dev: int):
     """Pointer of a contiguous tensor with this dtype and shape (None: any) on device `dev`, or None.
 
     The block operators' smallest calls take a few microseconds on the GPU, so a tensor
-    costs one line of attribute reads here (and less in _rra_fast)."""
+    costs one line of attribute reads here (and less in the extension)."""
     if t is None:
         return None
     if t.dtype is not dtype or (shape is not None and t.shape != shape) or t.get_device() != dev or not t.is_contiguous():
