@@ -382,8 +382,9 @@ cudaError_t launch_d(const CacheArgs& a, int num_sms, cudaStream_t stream) {
   // it evens out (4 x 4096 keys, 8 heads: 8 CTAs a unit 11.5 us, 16 25.7 us).  Units
   // that nearly fill them over a long cache: up to four CTAs with at least 32 chunks a
   // warp even out sequences of different lengths (32 x up to 16384 keys, 8 heads: 1 CTA
-  // a unit 167 us, 4 155 us, 16 216 us).  More units even out by themselves (48 x 1000 keys,
-  // 12 heads, in a cache of 32768: 1 CTA a unit 26 us, 2 40 us).
+  // a unit 167 us, 4 155 us, 16 216 us).  More units are not split: lengths that are alike or spread evenly even out
+  // by themselves (48 x 1000 keys, 12 heads, in a cache of 32768: 1 CTA a unit 26 us, 2 40 us; 40 x 1 to 16384 keys, 8 heads,
+  // 226 to 231 us in any order, 203 for the bytes), a few long ones among short ones do not (2 x 16384 among 38 x 100 120 us, 22).
   const int chunks = (a.cap - 1) / CK + 1;
   int cluster = 1, min_chunks = 4;
   while (2 * cluster <= most && units * 2 * cluster <= 2LL * num_sms && chunks >= 2 * cluster * C_WARPS * min_chunks)

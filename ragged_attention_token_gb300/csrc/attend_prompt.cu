@@ -146,7 +146,7 @@ inline double prompt_time(const PromptArgs& a, const UnitShape& us, int d, int n
 // neither tile ever works alone, which the last rows of many sequences would; two
 // successive tiles end one after the other, so that one's output leaves under the other's last
 // block.  32 / 8 heads, d = 128, causal, heads paired against rows: 16 x 1024 tokens 127 / 140 us,
-// 8 x 2048 207 / 222, eight of 1 to 4096 212 / 228, 8192 369 / 370, 16384 1406 / 1399; d = 64: 8192 281 / 263.
+// 8 x 2048 207 / 222, eight of 1 to 4096 212 / 228; 8192 369 / 370, 16384 1406 / 1399 (within what two runs differ by); d = 64: 8192 281 / 263.
 __host__ __device__ inline UnitShape whole_shape(int group, int d, int max_seqlen) {
   return group % 2 == 0 && d == 128 && max_seqlen <= 8192 ? UnitShape{2, PT, 0} : UnitShape{1, 2 * PT, 0};
 }

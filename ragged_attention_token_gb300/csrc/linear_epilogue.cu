@@ -129,11 +129,12 @@ __device__ __forceinline__ float exp2f_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 1 / (1 + e^-x): within a few 2^-23 of its value; 0 where e^-x overflows.
+// 1 / (1 + e^-x): relative to its value within a few 2^-23 for x >= 0 and (4 + 1.2 |x|) 2^-23 below (__expf is off by
+// 2 + 1.17 |x| units in the last place); 0 below about -87.3, where the reciprocal of 1 + e^-x would be subnormal.
 __device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.f + __expf(-x)); }
 // x/2 (1 + erf(x / sqrt 2)) of two values, by Abramowitz and Stegun, Handbook of
 // Mathematical Functions, 7.1.26: erfc(z) = (a1 t + ... + a5 t^5) e^{-z^2}, t = 1 / (1 + p z),
-// z >= 0, within 1.5e-7.  With h = erfc(|x| / sqrt 2) / 2 the result is
+// z >= 0, within 1.5e-7 (absolute; in fp32 the result is off by up to 6e-7 |x|, 1e-7 |x| below -3).  With h = erfc(|x| / sqrt 2) / 2 the result is
 // x (1/2 + copysign(1/2 - h, x)).  (With erff the epilogue of a K = 384 layer took
 // 2.5 times as long as its products.)
 __device__ __forceinline__ void act_gelu2(float& x, float& y) {
