@@ -71,7 +71,12 @@ typedef enum {
   RRA_ERR_DEVICE = 5       /* a kernel recorded a device-side error code */
 } rra_status;
 
-typedef enum { RRA_F16 = 0, RRA_BF16 = 1, RRA_F32 = 2 } rra_dtype;
+typedef enum {
+  RRA_F16 = 0,
+  RRA_BF16 = 1,
+  RRA_F32 = 2,
+  RRA_E4M3 = 3 /* 8 bits, largest 448: rra_rms_norm's output, rra_linear_scaled's operands */
+} rra_dtype;
 
 /* Device-side error codes reported by rra_get_device_error(). */
 enum {
@@ -574,6 +579,55 @@ RRA_API rra_status rra_attend_prompt(const void* q, long long q_stride, const vo
 RRA_API rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
                                     const int32_t* kv_len, int B, int nq, int cap, int Hq, int Hkv, int d,
                                     float scale, rra_dtype dtype, void* o, void* stream);
+
+/* Root-mean-square norm of rows, with the residual's addition ahead of it and an output in 16 or 8 bits, in one pass.
+ * For row t < T = cu_seqlens[B], in fp32:
+ *   r = x[t] + residual[t] (residual not NULL);  sum_out[t] = r, rounded once;
+ *   y[t] = r * rsqrt(mean(r^2) + eps) * weight (weight float [N]; NULL: ones), r as it is before sum_out's rounding.
+ * out_dtype == dtype: y is rounded once.  out_dtype == RRA_E4M3: scale[t] = max(max |y[t]| / 448, 2^-100) and
+ * y[t] / scale[t] is rounded once to 8 bits, ties to even (a row of zeros: zeros); a NaN in a row makes its scale NaN.
+ *   x [cap, N] of dtype (F16 or BF16); residual and sum_out [cap, N], both or neither, of residual_dtype: dtype or
+ *   RRA_F32; y [cap, N]; scale float [cap], with RRA_E4M3 only.  sum_out may be residual, or x where the types are one;
+ *   y in 16 bits may be x.  Other overlaps are refused (RRA_ERR_INVALID_ARG).
+ * N a multiple of 8, 8 <= N <= 32768 (else RRA_ERR_UNSUPPORTED).  Rows from T on are neither read nor written.  A sum of
+ * squares beyond fp32's range makes its row's y zeros.  A cu_seqlens[B] outside [0, cap] records RRA_DEVERR_INDEX_RANGE
+ * and writes nothing. */
+RRA_API rra_status rra_rms_norm(const void* x, const void* residual, rra_dtype residual_dtype, const float* weight,
+                                float eps, const int32_t* cu_seqlens, int B, int cap, int N, rra_dtype dtype,
+                                void* sum_out, void* y, rra_dtype out_dtype, float* scale, void* stream);
+
+/* rra_linear_epilogue on operands in 8 bits, with a scale for each row of a and of w:
+ *   c[t, n] = act(a_scale[t] w_scale[n] sum_k a[t, k] w[n, k] + bias[n]) + residual[t, n] for t < T = cu_seqlens[B].
+ *   a [cap, K], w [N, K] of RRA_E4M3; a_scale float [cap], w_scale float [N]; bias float [N] or NULL; residual [cap, N]
+ *   of out_dtype or NULL (it may be c itself); c [cap, N] of out_dtype (F16, BF16 or F32).
+ * K a multiple of 16, 16 <= K <= 65536; N a multiple of 8, N <= 65535 * 128 (else RRA_ERR_UNSUPPORTED); cap <= 65535 *
+ * 128.  Everything else as there: sums in fp32 (F32 outputs in parts, of K = 1024), the epilogue in fp32 with
+ * one rounding, the kernel chosen by cap. */
+RRA_API rra_status rra_linear_scaled(const void* a, const float* a_scale, const void* w, const float* w_scale,
+                                     const float* bias, const void* residual, const int32_t* cu_seqlens, int B, int cap,
+                                     int K, int N, rra_activation act, void* c, rra_dtype out_dtype, void* stream);
+
+/* Attention of the new tokens of each of B sequences, one or a chunk, over a cache in pages.  Sequence b has the packed
+ * rows cu_seqlens[b] .. cu_seqlens[b+1] of q, n of them (0: none), and kv_len[b] keys, the new tokens' own among them,
+ * the last ones: key j is row j % page_size of page page_table[b, j / page_size].  Its row i attends to the keys
+ * j < kv_len[b] - (n - 1 - i); a row that sees no key gets zeros.
+ *   q [cap, Hq, d]; k_pages and v_pages [num_pages, page_size, Hkv, d], their pages page_stride elements apart (a
+ *   multiple of 8, at least page_size * Hkv * d: the keys' and values' halves of one pool [num_pages, 2, page_size, Hkv,
+ *   d] are used where they are); page_size a multiple of 16 up to 65536 (else RRA_ERR_UNSUPPORTED); page_table int32
+ *   [B, table_width]; o [cap, Hq, d] contiguous, of the same dtype.
+ *   max_new and max_kv bound every sequence's n and kv_len (max_new <= 2^30, max_kv <= min(table_width * page_size,
+ *   2^30)); they also decide how the work is cut up: loose bounds cost time.
+ * 1e-30 <= scale <= 1e30.  Rows of q and o that belong to no sequence are neither read into a result nor written; rows of
+ * a page from kv_len[b] on, entries of the table behind the last page in use and pages in no table may hold anything.
+ * Offsets into the pool are 64-bit.  Several sequences may share pages.  A negative n or kv_len records
+ * RRA_DEVERR_SEQ_NEGATIVE, one above its bound RRA_DEVERR_SEQ_TOO_LONG, rows outside [0, cap] RRA_DEVERR_INDEX_RANGE;
+ * such a sequence is not written.  A table entry in use outside [0, num_pages) records RRA_DEVERR_INDEX_RANGE, and page 0
+ * is read in its place.  Products, sums and the values' limits as in rra_attend_prompt; a call repeated gives the same bits. */
+RRA_API rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
+                                    long long page_stride, int num_pages, int page_size, const int32_t* page_table,
+                                    int table_width, const int32_t* kv_len, const int32_t* cu_seqlens, int B, int cap,
+                                    int max_new, int max_kv, int Hq, int Hkv, int d, float scale, rra_dtype dtype, void* o,
+                                    void* stream);
 
 /* Bound, in clock cycles, on any one on-chip wait of the tcgen05 kernels of the image
  * attention, rra_linear_epilogue and rra_attend_prompt (0, the initial value: about one second,

@@ -77,3 +77,31 @@ def attend_rows(q, k, v, scale, last):
             o[i, h] = p @ v[:m, h // G]
             mag[i, h] = p @ np.abs(v[:m, h // G])
     return o, mag
+
+
+def to_e4m3(v):
+    """Each v rounded to the nearest value in 8 bits (e4m3: normal from 2^-6, steps of 2^-9 below, up to 448), ties to even."""
+    v = np.asarray(v, dtype=np.float64)
+    _, e = np.frexp(v)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.clip(np.rint(v / step) * step, -448.0, 448.0)
+
+
+def rms_norm(x, residual, weight, eps):
+    """(sum, y): x + residual (or x), and its RMS norm by rows, times weight."""
+    r = np.asarray(x, dtype=np.float64)
+    if residual is not None:
+        r = r + np.asarray(residual, dtype=np.float64)
+    y = r / np.sqrt((r * r).sum(-1, keepdims=True) / r.shape[-1] + eps)
+    return r, y if weight is None else y * np.asarray(weight, dtype=np.float64)
+
+
+def row_scale(y):
+    """The scale of each row in 8 bits."""
+    return np.maximum(np.abs(y).max(-1) / 448.0, 2.0 ** -100)
+
+
+def cached_rows(pages, table, n):
+    """The first n rows of a sequence whose pages [num_pages, page, ...] its row of the table lists."""
+    page = pages.shape[1]
+    return np.stack([pages[int(table[j // page]), j % page] for j in range(n)]) if n else pages[0, :0]

@@ -645,31 +645,56 @@ rra_status rra_linear_packed(const void* a, const void* w, const float* bias, co
   return RRA_OK;
 }
 
-rra_status rra_linear_epilogue(const void* a, const void* w, const float* bias, const void* residual,
-                               const int32_t* cu_seqlens, int B, int cap, int K, int N, rra_dtype in_dtype,
-                               rra_activation act, void* c, rra_dtype out_dtype, void* stream) {
-  if (B < 1 || B > 65535) return fail(RRA_ERR_INVALID_ARG, "B=%d outside [1, 65535]", B);
+namespace {
+
+// rra_linear_epilogue and rra_linear_scaled (e4m3: operands of one byte, with scales).
+rra_status linear_layer(const LinearEpiArgs& l, rra_dtype in_dtype, rra_activation act, rra_dtype out_dtype, void* stream) {
+  const bool e4m3 = in_dtype == RRA_E4M3;
+  const int unit = e4m3 ? 16 : 8;                        // K by 16 bytes
+  const void *a = l.a, *w = l.w, *c = l.c, *residual = l.residual;
+  const int cap = l.cap, K = l.K, N = l.N;
+  const int32_t* cu_seqlens = l.cu;
+  if (l.B < 1 || l.B > 65535) return fail(RRA_ERR_INVALID_ARG, "B=%d outside [1, 65535]", l.B);
   if (cap < 1 || cap > 65535 * 128) return fail(RRA_ERR_INVALID_ARG, "cap=%d outside [1, 65535*128]", cap);
-  if (K < 8 || K % 8 != 0 || K > 65536) return fail(RRA_ERR_UNSUPPORTED, "K=%d: a multiple of 8 up to 65536", K);
+  if (K < unit || K % unit != 0 || K > 65536) return fail(RRA_ERR_UNSUPPORTED, "K=%d: a multiple of %d up to 65536", K, unit);
   if (N < 8 || N % 8 != 0 || N > 65535 * 128) return fail(RRA_ERR_UNSUPPORTED, "N=%d: a multiple of 8", N);
-  if (!valid_in(in_dtype)) return fail(RRA_ERR_INVALID_ARG, "input dtype invalid");
+  if (!e4m3 && !valid_in(in_dtype)) return fail(RRA_ERR_INVALID_ARG, "input dtype invalid");
   if (!valid_out(out_dtype)) return fail(RRA_ERR_INVALID_ARG, "output dtype invalid");
   if (act < RRA_ACT_NONE || act > RRA_ACT_SILU) return fail(RRA_ERR_INVALID_ARG, "activation %d unknown", static_cast<int>(act));
   RRA_CHECK_PTR(a);
   RRA_CHECK_PTR(w);
   RRA_CHECK_PTR(c);
   RRA_CHECK_I32(cu_seqlens);
-  if (bias != nullptr && !aligned16(bias)) return fail(RRA_ERR_MISALIGNED, "bias not 16-byte aligned");
+  if (l.bias != nullptr && !aligned16(l.bias)) return fail(RRA_ERR_MISALIGNED, "bias not 16-byte aligned");
   if (residual != nullptr && !aligned16(residual)) return fail(RRA_ERR_MISALIGNED, "residual not 16-byte aligned");
-  const long long eo = dtype_bytes(out_dtype);
-  const RowSpan sc{c, cap, N * eo, N * eo}, sa{a, cap, 2LL * K, 2LL * K}, sw{w, N, 2LL * K, 2LL * K};
-  const RowSpan sb{bias, 1, 4LL * N, 4LL * N}, sr{residual, cap, N * eo, N * eo};
-  if (!disjoint(sc, sa) || !disjoint(sc, sw) || (bias != nullptr && !disjoint(sc, sb)))
+  const long long eo = dtype_bytes(out_dtype), ei = e4m3 ? 1 : 2;
+  const RowSpan sc{c, cap, N * eo, N * eo}, sa{a, cap, ei * K, ei * K}, sw{w, N, ei * K, ei * K};
+  const RowSpan sb{l.bias, 1, 4LL * N, 4LL * N}, sr{residual, cap, N * eo, N * eo};
+  if (!disjoint(sc, sa) || !disjoint(sc, sw) || (l.bias != nullptr && !disjoint(sc, sb)))
     return fail(RRA_ERR_INVALID_ARG, "c overlaps an input");
   if (residual != nullptr && residual != c && !disjoint(sc, sr))
     return fail(RRA_ERR_INVALID_ARG, "c overlaps residual without being it");
+  if (e4m3) {
+    const float *a_scale = l.a_scale, *w_scale = l.w_scale;
+    RRA_CHECK_PTR(a_scale);
+    RRA_CHECK_PTR(w_scale);
+    if (!disjoint(sc, {a_scale, 1, 4LL * cap, 4LL * cap}) || !disjoint(sc, {w_scale, 1, 4LL * N, 4LL * N}))
+      return fail(RRA_ERR_INVALID_ARG, "c overlaps the scales");
+  }
   DeviceState* st = nullptr;
   RRA_TRY(device_state(&st));
+  LinearEpiArgs g = l;
+  g.err = error_word(*st);
+  g.wait_limit = g_wait_limit.load();
+  cudaError_t e = e4m3 ? launch_linear_scaled(g, out_dtype, act, st->num_sms, static_cast<cudaStream_t>(stream))
+                       : launch_linear_epilogue(g, in_dtype, out_dtype, act, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, e4m3 ? "linear_scaled launch" : "linear_epilogue launch");
+  g_launches += 1;
+  return RRA_OK;
+}
+
+LinearEpiArgs linear_args(const void* a, const void* w, const float* bias, const void* residual, const int32_t* cu_seqlens,
+                          int B, int cap, int K, int N, void* c) {
   LinearEpiArgs g{};
   g.cu = cu_seqlens;
   g.B = B;
@@ -681,10 +706,83 @@ rra_status rra_linear_epilogue(const void* a, const void* w, const float* bias, 
   g.bias = bias;
   g.residual = residual;
   g.c = c;
+  return g;
+}
+
+}  // namespace
+
+rra_status rra_linear_epilogue(const void* a, const void* w, const float* bias, const void* residual,
+                               const int32_t* cu_seqlens, int B, int cap, int K, int N, rra_dtype in_dtype,
+                               rra_activation act, void* c, rra_dtype out_dtype, void* stream) {
+  if (!valid_in(in_dtype)) return fail(RRA_ERR_INVALID_ARG, "input dtype invalid");
+  return linear_layer(linear_args(a, w, bias, residual, cu_seqlens, B, cap, K, N, c), in_dtype, act, out_dtype, stream);
+}
+
+rra_status rra_linear_scaled(const void* a, const float* a_scale, const void* w, const float* w_scale, const float* bias,
+                             const void* residual, const int32_t* cu_seqlens, int B, int cap, int K, int N,
+                             rra_activation act, void* c, rra_dtype out_dtype, void* stream) {
+  LinearEpiArgs g = linear_args(a, w, bias, residual, cu_seqlens, B, cap, K, N, c);
+  g.a_scale = a_scale;
+  g.w_scale = w_scale;
+  return linear_layer(g, RRA_E4M3, act, out_dtype, stream);
+}
+
+rra_status rra_rms_norm(const void* x, const void* residual, rra_dtype residual_dtype, const float* weight, float eps,
+                        const int32_t* cu_seqlens, int B, int cap, int N, rra_dtype dtype, void* sum_out, void* y,
+                        rra_dtype out_dtype, float* scale, void* stream) {
+  if (B < 1 || B > 65535) return fail(RRA_ERR_INVALID_ARG, "B=%d outside [1, 65535]", B);
+  if (cap < 1) return fail(RRA_ERR_INVALID_ARG, "cap=%d < 1", cap);
+  if (N < 8 || N % 8 != 0 || N > 32768) return fail(RRA_ERR_UNSUPPORTED, "N=%d: a multiple of 8 up to 32768", N);
+  if (!valid_in(dtype)) return fail(RRA_ERR_INVALID_ARG, "dtype invalid");
+  if (out_dtype != dtype && out_dtype != RRA_E4M3) return fail(RRA_ERR_INVALID_ARG, "output dtype: that of x, or E4M3");
+  if (!(eps >= 0.f) || !finite(eps)) return fail(RRA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((residual == nullptr) != (sum_out == nullptr)) return fail(RRA_ERR_INVALID_ARG, "residual and sum_out go together");
+  if (residual != nullptr && residual_dtype != dtype && residual_dtype != RRA_F32)
+    return fail(RRA_ERR_INVALID_ARG, "residual dtype: that of x, or F32");
+  if ((out_dtype == RRA_E4M3) != (scale != nullptr)) return fail(RRA_ERR_INVALID_ARG, "scale goes with an output of E4M3");
+  RRA_CHECK_PTR(x);
+  RRA_CHECK_PTR(y);
+  RRA_CHECK_I32(cu_seqlens);
+  if (weight != nullptr && !aligned16(weight)) return fail(RRA_ERR_MISALIGNED, "weight not 16-byte aligned");
+  const long long ey = out_dtype == RRA_E4M3 ? 1 : 2, er = residual_dtype == RRA_F32 ? 4 : 2;
+  const RowSpan sx{x, cap, 2LL * N, 2LL * N}, sy{y, cap, ey * N, ey * N}, sw{weight, 1, 4LL * N, 4LL * N};
+  const RowSpan ss{scale, 1, 4LL * cap, 4LL * cap};
+  if (!(ey == 2 && y == x) && !disjoint(sy, sx)) return fail(RRA_ERR_INVALID_ARG, "y overlaps x");
+  if (weight != nullptr && !disjoint(sy, sw)) return fail(RRA_ERR_INVALID_ARG, "y overlaps the weight");
+  if (residual != nullptr) {
+    RRA_CHECK_PTR(residual);
+    RRA_CHECK_PTR(sum_out);
+    const RowSpan sr{residual, cap, er * N, er * N}, so{sum_out, cap, er * N, er * N};
+    if (sum_out != residual && !disjoint(so, sr)) return fail(RRA_ERR_INVALID_ARG, "sum_out overlaps residual without being it");
+    if (!(er == 2 && sum_out == x) && !disjoint(so, sx)) return fail(RRA_ERR_INVALID_ARG, "sum_out overlaps x");
+    if (!disjoint(sy, sr) || !disjoint(sy, so)) return fail(RRA_ERR_INVALID_ARG, "y overlaps residual or sum_out");
+    if (weight != nullptr && !disjoint(so, sw)) return fail(RRA_ERR_INVALID_ARG, "sum_out overlaps the weight");
+    if (scale != nullptr && (!disjoint(ss, so) || !disjoint(ss, sr)))
+      return fail(RRA_ERR_INVALID_ARG, "scale overlaps residual or sum_out");
+  }
+  if (scale != nullptr) {
+    if (reinterpret_cast<uintptr_t>(scale) & 3u) return fail(RRA_ERR_MISALIGNED, "scale not 4-byte aligned");
+    if (!disjoint(ss, sx) || !disjoint(ss, sy) || (weight != nullptr && !disjoint(ss, sw)))
+      return fail(RRA_ERR_INVALID_ARG, "scale overlaps another tensor");
+  }
+  DeviceState* st = nullptr;
+  RRA_TRY(device_state(&st));
+  NormRowsArgs g{};
+  g.x = x;
+  g.residual = residual;
+  g.sum = sum_out;
+  g.weight = weight;
+  g.eps = eps;
+  g.cu = cu_seqlens;
+  g.B = B;
+  g.cap = cap;
+  g.N = N;
+  g.y = y;
+  g.scale = scale;
   g.err = error_word(*st);
-  g.wait_limit = g_wait_limit.load();
-  cudaError_t e = launch_linear_epilogue(g, in_dtype, out_dtype, act, st->num_sms, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "linear_epilogue launch");
+  cudaError_t e = launch_rms_norm(g, dtype, residual != nullptr ? residual_dtype : dtype, out_dtype == RRA_E4M3, st->num_sms,
+                                  static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rms_norm launch");
   g_launches += 1;
   return RRA_OK;
 }
@@ -862,6 +960,66 @@ rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cac
   g.err = error_word(*st);
   cudaError_t e = launch_attend_cache(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "attend_cache launch");
+  g_launches += 1;
+  return RRA_OK;
+}
+
+rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
+                            long long page_stride, int num_pages, int page_size, const int32_t* page_table,
+                            int table_width, const int32_t* kv_len, const int32_t* cu_seqlens, int B, int cap, int max_new,
+                            int max_kv, int Hq, int Hkv, int d, float scale, rra_dtype dtype, void* o, void* stream) {
+  RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
+  if (page_size < 16 || page_size % 16 != 0 || page_size > 65536)
+    return fail(RRA_ERR_UNSUPPORTED, "page_size=%d: a multiple of 16 up to 65536", page_size);
+  if (num_pages < 1 || table_width < 1) return fail(RRA_ERR_INVALID_ARG, "num_pages=%d, table_width=%d", num_pages, table_width);
+  if (max_new < 1 || max_kv < 1) return fail(RRA_ERR_INVALID_ARG, "max_new=%d, max_kv=%d", max_new, max_kv);
+  if (max_new > (1 << 30) || max_kv > (1 << 30)) return fail(RRA_ERR_UNSUPPORTED, "max_new or max_kv > 2^30");
+  if (max_kv > static_cast<long long>(table_width) * page_size)
+    return fail(RRA_ERR_INVALID_ARG, "max_kv=%d keys do not fit %d pages of %d", max_kv, table_width, page_size);
+  if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
+  RRA_CHECK_PTR(q);
+  RRA_CHECK_PTR(k_pages);
+  RRA_CHECK_PTR(v_pages);
+  RRA_CHECK_PTR(o);
+  RRA_CHECK_I32(page_table);
+  RRA_CHECK_I32(kv_len);
+  RRA_CHECK_I32(cu_seqlens);
+  RRA_TRY(check_stride("q", q_stride, Hq, d));
+  const long long page_elems = static_cast<long long>(page_size) * Hkv * d;
+  if (page_stride < page_elems || page_stride >= (1LL << 36))
+    return fail(RRA_ERR_INVALID_ARG, "page stride %lld below page_size*Hkv*d or too large", page_stride);
+  if (page_stride % 8 != 0) return fail(RRA_ERR_MISALIGNED, "page stride %lld not a multiple of 8", page_stride);
+  const long long wq = 2LL * Hq * d;
+  const RowSpan so{o, cap, wq, wq};
+  if (!disjoint(so, {q, cap, wq, 2 * q_stride}) || !disjoint(so, {k_pages, num_pages, 2 * page_elems, 2 * page_stride}) ||
+      !disjoint(so, {v_pages, num_pages, 2 * page_elems, 2 * page_stride}))
+    return fail(RRA_ERR_INVALID_ARG, "o overlaps an input");
+  DeviceState* st = nullptr;
+  RRA_TRY(device_state(&st));
+  PagedArgs g{};
+  g.q = q;
+  g.k = k_pages;
+  g.v = v_pages;
+  g.q_stride = q_stride;
+  g.page_stride = page_stride;
+  g.table = page_table;
+  g.kv_len = kv_len;
+  g.cu = cu_seqlens;
+  g.B = B;
+  g.cap = cap;
+  g.max_new = max_new < cap ? max_new : cap;
+  g.max_kv = max_kv;
+  g.num_pages = num_pages;
+  g.page = page_size;
+  g.table_width = table_width;
+  g.Hq = Hq;
+  g.Hkv = Hkv;
+  g.scale_log2 = scale * 1.4426950408889634f;
+  g.o = o;
+  g.err = error_word(*st);
+  g.wait_limit = g_wait_limit.load();
+  cudaError_t e = launch_attend_paged(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "attend_paged launch");
   g_launches += 1;
   return RRA_OK;
 }

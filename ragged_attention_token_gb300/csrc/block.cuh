@@ -17,6 +17,9 @@ __device__ __forceinline__ void dependent_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The same for the kernels of the norm of rows and of the paged cache.
+__device__ __forceinline__ void start_dependent() { dependent_launch(); }
+
 // A bounded wait: by the default bound, or, in the kernels for launches made with a limit set (rra_set_wait_limit), by
 // that one, polling, so that a bound below the hardware's suspension of a wait holds too.
 template <bool LIMIT, long long DEFAULT = WAIT_LIMIT_CYCLES>
@@ -29,12 +32,15 @@ __device__ __forceinline__ bool mbar_wait_limited(uint32_t bar, uint32_t parity,
   return true;
 }
 
-// Linear layer with its epilogue: c = act(a W^T + bias) + residual for the T = cu[B] rows.
+// Linear layer with its epilogue: c = act(a W^T + bias) + residual for the T = cu[B] rows; in 8 bits the products are
+// scaled first: a_scale[t] w_scale[n] (a W^T).
 struct LinearEpiArgs {
   const int32_t* cu;
   int B, cap, K, N;
   const void* a;
   const void* w;
+  const float* a_scale;    // [cap], 8-bit operands only
+  const float* w_scale;    // [N]
   const float* bias;       // [N] or null
   const void* residual;    // [cap, N] of the output type, or null; may be c
   void* c;
@@ -43,6 +49,24 @@ struct LinearEpiArgs {
 };
 cudaError_t launch_linear_epilogue(const LinearEpiArgs& a, rra_dtype in, rra_dtype out, rra_activation act,
                                    int num_sms, cudaStream_t stream);
+cudaError_t launch_linear_scaled(const LinearEpiArgs& a, rra_dtype out, rra_activation act, int num_sms,
+                                 cudaStream_t stream);
+
+// Norm of rows: r = x (+ residual), sum = r, y = r rsqrt(mean r^2 + eps) (weight), in 16 bits or in 8 with a scale a row.
+struct NormRowsArgs {
+  const void* x;
+  const void* residual;    // [cap, N] or null
+  void* sum;               // [cap, N] of the residual's type; may be it
+  const float* weight;     // [N] or null
+  float eps;
+  const int32_t* cu;
+  int B, cap, N;
+  void* y;
+  float* scale;            // [cap], 8-bit outputs only
+  int32_t* err;
+};
+cudaError_t launch_rms_norm(const NormRowsArgs& a, rra_dtype dt, rra_dtype residual, bool eight_bits, int num_sms,
+                            cudaStream_t stream);
 
 // Norm + rotation of query and key heads (+ copy of values); strides in elements.
 struct NormRopeArgs {
@@ -87,5 +111,20 @@ struct CacheArgs {
   int32_t* err;
 };
 cudaError_t launch_attend_cache(const CacheArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream);
+
+// Attention of the new tokens of each sequence over a paged cache.
+struct PagedArgs {
+  const void *q, *k, *v;
+  long long q_stride, page_stride;         // elements between rows of q, between pages of k and of v
+  const int32_t* table;                    // [B, table_width]
+  const int32_t* kv_len;
+  const int32_t* cu;
+  int B, cap, max_new, max_kv, num_pages, page, table_width, Hq, Hkv;
+  float scale_log2;
+  void* o;
+  int32_t* err;
+  long long wait_limit;
+};
+cudaError_t launch_attend_paged(const PagedArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream);
 
 }  // namespace rra

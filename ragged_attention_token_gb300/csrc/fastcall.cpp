@@ -22,6 +22,9 @@ decltype(&rra_linear_epilogue) f_linear = nullptr;
 decltype(&rra_qk_norm_rope) f_rope = nullptr;
 decltype(&rra_attend_prompt) f_prompt = nullptr;
 decltype(&rra_attend_cache) f_cache = nullptr;
+decltype(&rra_rms_norm) f_norm = nullptr;
+decltype(&rra_linear_scaled) f_scaled = nullptr;
+decltype(&rra_attend_paged) f_paged = nullptr;
 
 // One call's arguments, taken in order; `ok` turns false at the first that is not plain.
 struct Args {
@@ -278,14 +281,129 @@ PyObject* cache(PyObject*, PyObject* const* v, Py_ssize_t n) {
   }
 }
 
-// bind(linear, rope, prompt, cache): the addresses of librra's functions.
+// norm(x, cu_seqlens, B, y, weight, residual, sum_out, scale, eps, stream)
+PyObject* norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  try {
+    Args a{v, n};
+    const at::Tensor *x = a.tensor(), *cu = a.tensor();
+    const long long B = a.integer();
+    const at::Tensor *y = a.tensor(), *w = a.tensor(true), *res = a.tensor(true), *sum = a.tensor(true), *sc = a.tensor(true);
+    const float eps = a.real();
+    void* s = a.stream();
+    rra_dtype dt, out = RRA_E4M3, rdt;
+    if (!a.ok || x->dim() != 2 || !code(*x, dt) || (res == nullptr) != (sum == nullptr)) return result(-1);
+    if (y->scalar_type() == at::kFloat8_e4m3fn ? sc == nullptr : sc != nullptr || !code(*y, out)) return result(-1);
+    rdt = dt;
+    if (res != nullptr && !code(*res, rdt)) return result(-1);
+    const int64_t cap = x->size(0), N = x->size(1);
+    const void* px = dense(a, x, x->scalar_type(), {-1, -1});
+    void* py = const_cast<void*>(dense(a, y, y->scalar_type(), {cap, N}));
+    const float* pw = dense<float>(a, w, at::kFloat, {N});
+    const void* pr = res != nullptr ? dense(a, res, res->scalar_type(), {cap, N}) : nullptr;
+    void* psum = sum != nullptr ? const_cast<void*>(dense(a, sum, res->scalar_type(), {cap, N})) : nullptr;
+    float* psc = const_cast<float*>(dense<float>(a, sc, at::kFloat, {cap}));
+    const int32_t* pcu = offsets(a, cu, B);
+    if (!a.ok || !fits(cap) || !fits(N)) return result(-1);
+    rra_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_norm(px, pr, rdt, pw, eps, pcu, static_cast<int>(B), static_cast<int>(cap), static_cast<int>(N), dt, psum, py, out,
+                psc, s);
+    Py_END_ALLOW_THREADS
+    return result(st);
+  } catch (...) {
+    return result(-1);
+  }
+}
+
+// scaled(a, a_scale, w, w_scale, cu_seqlens, B, c, bias, act, residual, stream)
+PyObject* scaled(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  try {
+    Args a{v, n};
+    const at::Tensor *x = a.tensor(), *xs = a.tensor(), *w = a.tensor(), *ws = a.tensor(), *cu = a.tensor();
+    const long long B = a.integer();
+    const at::Tensor *c = a.tensor(), *bias = a.tensor(true);
+    const long long act = a.integer();
+    const at::Tensor* res = a.tensor(true);
+    void* s = a.stream();
+    rra_dtype out;
+    if (!a.ok || x->dim() != 2 || w->dim() != 2 || !code(*c, out)) return result(-1);
+    const int64_t cap = x->size(0), K = x->size(1), N = w->size(0);
+    const void* px = dense(a, x, at::kFloat8_e4m3fn, {-1, -1});
+    const float* pxs = dense<float>(a, xs, at::kFloat, {cap});
+    const void* pw = dense(a, w, at::kFloat8_e4m3fn, {-1, K});
+    const float* pws = dense<float>(a, ws, at::kFloat, {N});
+    const float* pb = dense<float>(a, bias, at::kFloat, {N});
+    const void* pr = dense(a, res, c->scalar_type(), {cap, N});
+    void* pc = const_cast<void*>(dense(a, c, c->scalar_type(), {cap, N}));
+    const int32_t* pcu = offsets(a, cu, B);
+    if (!a.ok || !fits(cap) || !fits(K) || !fits(N)) return result(-1);
+    rra_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_scaled(px, pxs, pw, pws, pb, pr, pcu, static_cast<int>(B), static_cast<int>(cap), static_cast<int>(K),
+                  static_cast<int>(N), static_cast<rra_activation>(act), pc, out, s);
+    Py_END_ALLOW_THREADS
+    return result(st);
+  } catch (...) {
+    return result(-1);
+  }
+}
+
+// [pages, page, Hkv, d] whose pages are contiguous and may lie apart.
+Rows pages_of(Args& a, const at::Tensor* t, at::ScalarType st, int64_t n, int64_t page, int64_t H, int64_t d) {
+  Rows r;
+  if (t == nullptr || !a.take(t->scalar_type() == st && t->dim() == 4 && t->size(0) == n && t->size(1) == page && t->size(2) == H &&
+                              t->size(3) == d && (d <= 1 || t->stride(3) == 1) && (H <= 1 || t->stride(2) == d) &&
+                              (page <= 1 || t->stride(1) == H * d)))
+    return r;
+  r.p = t->data_ptr();
+  r.stride = n > 1 ? t->stride(0) : page * H * d;
+  return r;
+}
+
+// paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B, max_new, max_kv, o, scale, stream)
+PyObject* paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  try {
+    Args a{v, n};
+    const at::Tensor *q = a.tensor(), *k = a.tensor(), *vc = a.tensor(), *table = a.tensor(), *len = a.tensor(), *cu = a.tensor();
+    const long long B = a.integer(), most_new = a.integer(), most_kv = a.integer();
+    const at::Tensor* o = a.tensor();
+    const float scale = a.real();
+    void* s = a.stream();
+    rra_dtype dt;
+    if (!a.ok || q->dim() != 3 || k->dim() != 4 || table->dim() != 2 || !code(*q, dt)) return result(-1);
+    const at::ScalarType t = q->scalar_type();
+    const int64_t cap = q->size(0), Hq = q->size(1), d = q->size(2), pages = k->size(0), page = k->size(1), Hkv = k->size(2);
+    const int64_t width = table->size(1);
+    const Rows rq = spread(a, q, t, cap, Hq, d);
+    const Rows rk = pages_of(a, k, t, pages, page, Hkv, d), rv = pages_of(a, vc, t, pages, page, Hkv, d);
+    const int32_t* pt = dense<int32_t>(a, table, at::kInt, {B, width});
+    const int32_t* pl = dense<int32_t>(a, len, at::kInt, {B});
+    const int32_t* pcu = offsets(a, cu, B);
+    void* po = const_cast<void*>(dense(a, o, t, {cap, Hq, d}));
+    if (!a.ok || rk.stride != rv.stride || !fits(cap) || !fits(Hq) || !fits(Hkv) || !fits(d) || !fits(pages) || !fits(page) ||
+        !fits(width))
+      return result(-1);
+    rra_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = f_paged(rq.p, rq.stride, rk.p, rv.p, rk.stride, static_cast<int>(pages), static_cast<int>(page), pt,
+                 static_cast<int>(width), pl, pcu, static_cast<int>(B), static_cast<int>(cap), static_cast<int>(most_new),
+                 static_cast<int>(most_kv), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d), scale, dt, po, s);
+    Py_END_ALLOW_THREADS
+    return result(st);
+  } catch (...) {
+    return result(-1);
+  }
+}
+
+// bind(linear, rope, prompt, cache, norm, scaled, paged): the addresses of librra's functions.
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  constexpr int COUNT = 7;
+  if (n != COUNT) {
+    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
     return nullptr;
   }
-  void* p[4];
-  for (int i = 0; i < 4; ++i) {
+  void* p[COUNT];
+  for (int i = 0; i < COUNT; ++i) {
     p[i] = PyLong_AsVoidPtr(v[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -296,6 +414,9 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   f_rope = reinterpret_cast<decltype(f_rope)>(p[1]);
   f_prompt = reinterpret_cast<decltype(f_prompt)>(p[2]);
   f_cache = reinterpret_cast<decltype(f_cache)>(p[3]);
+  f_norm = reinterpret_cast<decltype(f_norm)>(p[4]);
+  f_scaled = reinterpret_cast<decltype(f_scaled)>(p[5]);
+  f_paged = reinterpret_cast<decltype(f_paged)>(p[6]);
   Py_RETURN_NONE;
 }
 
@@ -305,6 +426,9 @@ PyMethodDef methods[] = {
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope)), METH_FASTCALL, nullptr},
     {"prompt", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prompt)), METH_FASTCALL, nullptr},
     {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cache)), METH_FASTCALL, nullptr},
+    {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm)), METH_FASTCALL, nullptr},
+    {"scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(scaled)), METH_FASTCALL, nullptr},
+    {"paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rra_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

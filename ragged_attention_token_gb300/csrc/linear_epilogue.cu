@@ -36,6 +36,8 @@
 // Every wait is bounded; a CTA that gives up tells its peer or its cluster, records
 // RRA_DEVERR_WAIT_TIMEOUT, lets copies and products in flight land, frees its
 // TMEM and returns; what its tile lacks then is not written.
+#include <cuda_fp8.h>
+
 #include <mutex>
 
 #include "block.cuh"
@@ -47,7 +49,10 @@ namespace {
 
 constexpr int LM = 128;                                  // rows of a CTA's half tile
 constexpr int LN_MAX = 256;                              // columns of a tile
-constexpr int LK = 64;                                   // K per stage (one 128-byte swizzled row)
+// K per stage: one 128-byte swizzled row (64 elements, in 8 bits 128).  In bytes, the 8-bit layer (rra_linear_scaled) is the
+// 16-bit one: a product reads 32 bytes of each row either way, so all of the shapes and rules here hold for it too.
+template <typename Tin> constexpr int LK = 128 / static_cast<int>(sizeof(Tin));
+template <typename Tin> constexpr bool SCALED = sizeof(Tin) == 1;   // rows and columns carry scales
 constexpr int L_MAX_STAGES = 9;                          // ring: 6 stages at LN = 256, 8 at 128, 9 at 64
 constexpr int L_EPI_WARPS = 8;                           // warps 2-9
 constexpr int L_THREADS = 64 + 32 * L_EPI_WARPS;
@@ -99,6 +104,28 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, u
       " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Both operands K-major, fp32 sums.  E4M3 is format 0 of its kind, as F16 is of its own.
+template <typename Tin>
+__device__ __forceinline__ uint32_t idesc_in(int M, int N) {
+  if constexpr (SCALED<Tin>) return idesc_f16(0u, 0, M, N);
+  else return idesc_f16(IsBf16<Tin>::value, 0, M, N);
 }
 // Arrives on `bar` of both CTAs once every product issued so far has completed.
 __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
@@ -345,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     if (blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
   } else {
     const int pairs = static_cast<int>(gridDim.x) / 2, pair = static_cast<int>(blockIdx.x) / 2;
-    const int kchunks = (a.K + LK - 1) / LK;
+    const int kchunks = (a.K + LK<Tin> - 1) / LK<Tin>;
     const int parts = PARTS ? (kchunks + L_PART - 1) / L_PART : 1;
     const Tiling g = make_tiling(T, a.N, pairs, PARTS ? LN_PARTS : LN_MAX);
     const uint32_t stage_bytes = L_A_BYTES + static_cast<uint32_t>(g.ln / 2) * 128u;   // A rows, then W rows
@@ -369,8 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
             }
             if (rank == 0) mbar_expect_tx(bar(LB_FULL, s), bytes);
             const uint32_t full = map_rank(bar(LB_FULL, s), 0), dst = base + s * stage_bytes;
-            tma_load_2d_pair(dst, &map_a, kc * LK, m0, full);       // rows past cap, columns past K: zeros
-            tma_load_2d_pair(dst + L_A_BYTES, mw, kc * LK, n0, full);
+            tma_load_2d_pair(dst, &map_a, kc * LK<Tin>, m0, full);       // rows past cap, columns past K: zeros
+            tma_load_2d_pair(dst + L_A_BYTES, mw, kc * LK<Tin>, n0, full);
             if (++s == stages) {
               s = 0;
               ++lap;
@@ -388,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           int m0, n0, width;
           piece_at(g, t, a.N, m0, n0, width);
           if (width == 0) continue;
-          const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 2 * LM, width);
+          const uint32_t idesc = idesc_in<Tin>(2 * LM, width);
           for (int part = 0; part < parts && !bad; ++part, ++i) {
             const uint32_t b = i & 1;
             if (i >= 2 && !mbar_wait_limited<LIMIT>(bar(LB_ACC_EMPTY, b), ((i >> 1) - 1) & 1, abort_flag, a.wait_limit)) {
@@ -406,8 +433,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
               tc_fence_after();
               const uint64_t off = s * (stage_bytes >> 4);
 #pragma unroll
-              for (int kk = 0; kk < LK / 16; ++kk)
-                umma_f16_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, (kc > k_from || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t add = (kc > k_from || kk > 0) ? 1u : 0u;
+                if constexpr (SCALED<Tin>) umma_f8_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, add);
+                else umma_f16_pair(acc, da0 + off + 2 * kk, dw0 + off + 2 * kk, idesc, add);
+              }
               umma_commit_pair(bar(LB_EMPTY, s));
               if (++s == stages) {
                 s = 0;
@@ -428,11 +458,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
       const uint32_t acc_empty[2] = {map_rank(bar(LB_ACC_EMPTY, 0), 0), map_rank(bar(LB_ACC_EMPTY, 1), 0)};
       uint32_t i = 0;
       // This lane's columns of the bias of piece p (of the tile at column n0): lane, and lane + 32 of a 64-column piece.
-      float bias0 = 0.f, bias1 = 0.f;
+      float bias0 = 0.f, bias1 = 0.f, ws0 = 0.f, ws1 = 0.f, row_scale = 0.f;   // the same columns' scales; this lane's row's
       auto load_bias = [&](int col0) {
-        if (a.bias == nullptr || col0 >= a.N) return;
-        bias0 = a.bias[min(col0 + lane, a.N - 1)];
-        if (CPP > 32) bias1 = a.bias[min(col0 + 32 + lane, a.N - 1)];
+        if (col0 >= a.N) return;
+        const int c0 = min(col0 + lane, a.N - 1), c1 = min(col0 + 32 + lane, a.N - 1);
+        if constexpr (SCALED<Tin>) {
+          ws0 = a.w_scale[c0];
+          if (CPP > 32) ws1 = a.w_scale[c1];
+        }
+        if (a.bias == nullptr) return;
+        bias0 = a.bias[c0];
+        if (CPP > 32) bias1 = a.bias[c1];
       };
       for (long long t = pair; t < g.all; t += pairs) {
         int m0, n0, width;
@@ -440,6 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         if (width == 0) continue;
         m0 = m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
         load_bias(n0 + half * CPP);
+        if (SCALED<Tin> && m0 < T) row_scale = a.a_scale[min(m0 + lane, T - 1)];
         const int cols = m0 < T ? min(width, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
         // The tile's partial products, into registers: the sum of those before the last, fp32 outputs only.
         constexpr int SUMS = PARTS ? LN_PARTS / CPP / 2 : 1;
@@ -503,6 +540,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty[b]);
           }
+          if constexpr (SCALED<Tin>) {
+            // As the bias below, in the staging rows behind its own.
+            st_shared_u32(stg + 256 + lane * 4, __float_as_uint(ws0));
+            if (CPP > 32) st_shared_u32(stg + 384 + lane * 4, __float_as_uint(ws1));
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < CPP / 4; ++j) {
+              const uint4 ww = ld_shared_v4(stg + 256 + 16 * j);
+              v[4 * j] *= row_scale * __uint_as_float(ww.x);
+              v[4 * j + 1] *= row_scale * __uint_as_float(ww.y);
+              v[4 * j + 2] *= row_scale * __uint_as_float(ww.z);
+              v[4 * j + 3] *= row_scale * __uint_as_float(ww.w);
+            }
+            __syncwarp();
+          }
           if (a.bias != nullptr) {
             // From a column per lane to every lane through the staging rows (16
             // broadcast loads from global memory came one after another: 3600 cycles a piece).
@@ -518,8 +570,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
               v[4 * j + 3] += __uint_as_float(bb.w);
             }
             __syncwarp();
-            load_bias(n0 + (p + 2) * CPP);
           }
+          if (SCALED<Tin> || a.bias != nullptr) load_bias(n0 + (p + 2) * CPP);
           activate(v, act);
           if (a.residual != nullptr) {
             // The residual turns from row pieces into rows through the staging rows.
@@ -682,7 +734,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   const int rows = valid ? max(0, min(T - t0, row_step)) : 0, boxes = (rows + 31) / 32, cols = (rows + 15) & ~15;
   const uint32_t stage_bytes = M_W_BYTES + static_cast<uint32_t>(boxes) * 4096u;
   const uint32_t stages = min(static_cast<uint32_t>(M_MAX_STAGES), M_RING_BYTES / stage_bytes);
-  const int kchunks = (a.K + LK - 1) / LK;
+  const int kchunks = (a.K + LK<Tin> - 1) / LK<Tin>;
   const int k_from = static_cast<int>(static_cast<long long>(kchunks) * rank / splits);
   const int k_to = rows > 0 ? static_cast<int>(static_cast<long long>(kchunks) * (rank + 1) / splits) : k_from;
   const int part_cols = cols > 128 ? 256 : 128;
@@ -701,8 +753,8 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         }
         const uint32_t dst = base + s * stage_bytes;
         mbar_expect_tx(bar(MB_FULL, s), stage_bytes);
-        tma_load_2d(dst, &map_w, kc * LK, n0, bar(MB_FULL, s));          // rows past N, columns past K: zeros
-        for (int b = 0; b < boxes; ++b) tma_load_2d(dst + M_W_BYTES + b * 4096, &map_a, kc * LK, t0 + 32 * b, bar(MB_FULL, s));
+        tma_load_2d(dst, &map_w, kc * LK<Tin>, n0, bar(MB_FULL, s));          // rows past N, columns past K: zeros
+        for (int b = 0; b < boxes; ++b) tma_load_2d(dst + M_W_BYTES + b * 4096, &map_a, kc * LK<Tin>, t0 + 32 * b, bar(MB_FULL, s));
         if (++s == stages) {
           s = 0;
           ++lap;
@@ -713,7 +765,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------- products
     if (elect_one()) {
-      const uint32_t idesc = idesc_f16(IsBf16<Tin>::value, 0, 128, cols);
+      const uint32_t idesc = idesc_in<Tin>(128, cols);
       const uint64_t dw0 = sdesc(base, 16, 1024), dx0 = sdesc(base + M_W_BYTES, 16, 1024);
       uint32_t s = 0, lap = 0;
       int slot = 0, turn = 0, at = 0;                    // accumulator, times round them, chunks of its part so far
@@ -729,8 +781,11 @@ __global__ void __launch_bounds__(M_THREADS, 1)
         tc_fence_after();
         const uint64_t off = s * (stage_bytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < LK / 16; ++kk)
-          umma_f16(tmem + slot * part_cols, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, (at > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t add = (at > 0 || kk > 0) ? 1u : 0u;
+          if constexpr (SCALED<Tin>) umma_f8(tmem + slot * part_cols, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, add);
+          else umma_f16(tmem + slot * part_cols, dw0 + off + 2 * kk, dx0 + off + 2 * kk, idesc, add);
+        }
         umma_commit(bar(MB_EMPTY, s));
         if (++at == per_part || kc + 1 == k_to) {
           if (PARTS) umma_commit(bar(MB_ACC_FULL, slot));
@@ -854,6 +909,14 @@ __global__ void __launch_bounds__(M_THREADS, 1)
           v[3] += y[u][p].w;
         }
       }
+      if constexpr (SCALED<Tin>) {
+        const float4 ws = *reinterpret_cast<const float4*>(a.w_scale + n);
+        const float sa = a.a_scale[t0 + t];
+        v[0] *= sa * ws.x;
+        v[1] *= sa * ws.y;
+        v[2] *= sa * ws.z;
+        v[3] *= sa * ws.w;
+      }
       if (a.bias != nullptr) {
         const float4 b = *reinterpret_cast<const float4*>(a.bias + n);
         v[0] += b.x;
@@ -893,6 +956,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_fp8_e4m3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -924,7 +993,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
 #pragma unroll
     for (int j = 0; j < 4; ++j) d[t][j] = sum[t][j] = 0.f;
   }
-  // Steps of 32 in K, taken by the warps in turn.  Each lane copies its own
+  // Steps of 64 bytes in K (32 elements, 64 in 8 bits), taken by the warps in turn.  Each lane copies its own
   // chunks into its own slots of shared memory and reads them back, U steps
   // later: no other lane waits for them, and the copies in flight need no
   // registers (as register loads the compiler kept one step in flight).
@@ -933,16 +1002,17 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
   // A warp takes pairs of steps (whole 128-byte lines of W), starting at a
   // place that differs from CTA to CTA: all CTAs read the same rows of a, and
   // in step they would all ask one L2 line at a time.
-  const int units = (a.K + 63) / 64, mine = 2 * ((units - warp + FEW_WARPS - 1) / FEW_WARPS);
+  constexpr int E16 = 16 / static_cast<int>(sizeof(Tin));   // elements of a 16-byte chunk
+  const int units = (a.K + LK<Tin> - 1) / LK<Tin>, mine = 2 * ((units - warp + FEW_WARPS - 1) / FEW_WARPS);
   const int turn = mine > 0 ? 2 * (static_cast<int>(blockIdx.x) % (mine / 2)) : 0;
   auto k_of = [&](int i) {
     int j = i + turn;
     if (j >= mine) j -= mine;
-    return (warp + (j >> 1) * FEW_WARPS) * 64 + (j & 1) * 32 + q * 8;
+    return (warp + (j >> 1) * FEW_WARPS) * LK<Tin> + (j & 1) * (LK<Tin> / 2) + q * E16;
   };
   auto fetch = [&](int i, int u) {
-    // K is a multiple of 8: chunks are whole; past K the last one is copied and counts as zero.
-    const int k = min(k_of(i), a.K - 8);
+    // K is a multiple of 16 bytes: chunks are whole; past K the last one is copied and counts as zero.
+    const int k = min(k_of(i), a.K - E16);
     cp_async16(chunk(u, 0), w0 + k);
     cp_async16(chunk(u, 1), w1 + k);
 #pragma unroll
@@ -1001,6 +1071,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) linear_few_kernel(const Linear
     float v[1] = {0.f};
 #pragma unroll
     for (int w = 0; w < FEW_WARPS; ++w) v[0] += part[w][j][t];
+    if constexpr (SCALED<Tin>) v[0] *= a.a_scale[t] * a.w_scale[n];
     if (a.bias != nullptr) v[0] += a.bias[n];
     activate(v, act);
     const size_t at = static_cast<size_t>(t) * a.N + n;
@@ -1025,14 +1096,18 @@ PFN_cuTensorMapEncodeTiled_v12000 linear_encode_fn() {
   return fn;
 }
 
-// 2-D map over a row-major [rows, K] matrix: box = 64 columns x box_rows rows,
+// 2-D map over a row-major [rows, K] matrix: box = 128 bytes of columns x box_rows rows,
 // 128-byte swizzle (the canonical K-major operand layout).
-cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, long long rows, int K, bool bf16, uint32_t box_rows) {
+template <typename Tin>
+cudaError_t make_map_2d(CUtensorMap* map, const void* ptr, long long rows, int K, uint32_t box_rows) {
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * 2};
-  cuuint32_t box[2] = {LK, box_rows};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K) * sizeof(Tin)};
+  cuuint32_t box[2] = {LK<Tin>, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = linear_encode_fn()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+  CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if constexpr (!SCALED<Tin>)
+    type = IsBf16<Tin>::value == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUresult r = linear_encode_fn()(map, type, 2,
                                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1080,11 +1155,10 @@ cudaError_t launch_pair(const LinearEpiArgs& a, int act, int num_sms, cudaStream
   auto kernel = linear_pair_kernel<Tin, Tout, PARTS, LIMIT>;
   cudaError_t e = allow_smem<Tin, Tout, -1 - PARTS - 2 * LIMIT>(kernel, L_SMEM);
   if (e != cudaSuccess) return e;
-  const bool bf16 = IsBf16<Tin>::value == 1;
   CUtensorMap ma, mw[3];
-  if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, LM)) != cudaSuccess) return e;
+  if ((e = make_map_2d<Tin>(&ma, a.a, a.cap, a.K, LM)) != cudaSuccess) return e;
   for (int i = 0; i < 3; ++i)
-    if ((e = make_map_2d(&mw[i], a.w, a.N, a.K, bf16, 128u >> i)) != cudaSuccess) return e;
+    if ((e = make_map_2d<Tin>(&mw[i], a.w, a.N, a.K, 128u >> i)) != cudaSuccess) return e;
   const long long most = ((a.cap + 2LL * LM - 1) / (2 * LM)) * ((a.N + 63LL) / 64);   // tiles if every row is in use
   const int pairs = static_cast<int>(most < num_sms / 2 ? most : num_sms / 2);
   cudaLaunchAttribute attr;
@@ -1099,10 +1173,9 @@ struct MidCut {
   int splits, row_step;
   long long ctas, cycles;
 };
-MidCut cut_mid(const LinearEpiArgs& a, int num_sms) {
+MidCut cut_mid(const LinearEpiArgs& a, int kchunks, int num_sms) {
   MidCut m;
   const long long row_tiles = (a.cap - 1LL) / M_ROWS + 1, tiles = row_tiles * ((a.N + 127) / 128);
-  const int kchunks = (a.K + LK - 1) / LK;
   m.row_step = static_cast<int>((a.cap + row_tiles - 1) / row_tiles + 15) & ~15;
   m.splits = 1;
   const int at_once[] = {num_sms, num_sms * 18 / 19, num_sms * 15 / 19};  // clusters of 2, 4, 8
@@ -1120,10 +1193,9 @@ cudaError_t launch_mid(const LinearEpiArgs& a, int act, const MidCut& cut, cudaS
   auto kernel = linear_mid_kernel<Tin, Tout, LIMIT>;
   cudaError_t e = allow_smem<Tin, Tout, -5 - LIMIT>(kernel, M_SMEM);
   if (e != cudaSuccess) return e;
-  const bool bf16 = IsBf16<Tin>::value == 1;
   CUtensorMap ma, mw;
-  if ((e = make_map_2d(&ma, a.a, a.cap, a.K, bf16, 32)) != cudaSuccess) return e;
-  if ((e = make_map_2d(&mw, a.w, a.N, a.K, bf16, 128)) != cudaSuccess) return e;
+  if ((e = make_map_2d<Tin>(&ma, a.a, a.cap, a.K, 32)) != cudaSuccess) return e;
+  if ((e = make_map_2d<Tin>(&mw, a.w, a.N, a.K, 128)) != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = dependent_config(attr, static_cast<int>(cut.ctas), M_THREADS, M_SMEM, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -1149,11 +1221,12 @@ cudaError_t launch_tiles(const LinearEpiArgs& a, int act, int num_sms, cudaStrea
   // 4096 x 4096: 64 rows 11.2 us with W as the M operand against 16.6, 200 rows 15.6 / 16.1, 256 rows 17.4 / 16.3; 768 x
   // 2304: 64 rows 5.8 / 6.1, 128 rows 7.0 / 6.2; 16384 x 4096: 256 rows 36.7 / 48.3; 7440 x 72: 392 rows 12.4 / 23.8.
   // (Only where all of its clusters run at once: further rounds repeat a cluster's set-up.)
-  const MidCut cut = cut_mid(a, num_sms);
-  const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * ((a.K + LK - 1) / LK);
+  const int kchunks = (a.K + LK<Tin> - 1) / LK<Tin>;
+  const MidCut cut = cut_mid(a, kchunks, num_sms);
+  const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * kchunks;
   if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) return launch_mid<Tin, Tout, LIMIT>(a, act, cut, stream);
   if constexpr (sizeof(Tout) == 4)
-    if (a.K > L_PART * LK) return launch_pair<Tin, Tout, true, LIMIT>(a, act, num_sms, stream);
+    if (kchunks > L_PART) return launch_pair<Tin, Tout, true, LIMIT>(a, act, num_sms, stream);
   return launch_pair<Tin, Tout, false, LIMIT>(a, act, num_sms, stream);
 }
 
@@ -1178,6 +1251,10 @@ cudaError_t launch_linear_epilogue(const LinearEpiArgs& a, rra_dtype in, rra_dty
                                    int num_sms, cudaStream_t stream) {
   return in == RRA_BF16 ? launch_in<__nv_bfloat16>(a, out, act, num_sms, stream)
                         : launch_in<__half>(a, out, act, num_sms, stream);
+}
+
+cudaError_t launch_linear_scaled(const LinearEpiArgs& a, rra_dtype out, rra_activation act, int num_sms, cudaStream_t stream) {
+  return launch_in<__nv_fp8_e4m3>(a, out, act, num_sms, stream);
 }
 
 }  // namespace rra

@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "librra.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "rra.h")
 
 RRA_OK, RRA_ERR_INVALID_ARG, RRA_ERR_UNSUPPORTED, RRA_ERR_MISALIGNED, RRA_ERR_CUDA, RRA_ERR_DEVICE = range(6)
-RRA_F16, RRA_BF16, RRA_F32 = 0, 1, 2
+RRA_F16, RRA_BF16, RRA_F32, RRA_E4M3 = 0, 1, 2, 3
 ATTEND_TCGEN05, ATTEND_MMA_SYNC, ATTEND_AUTO, ATTEND_TCGEN05_LATENCY = 0, 1, 2, 3
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 DEVERR_NONE, DEVERR_SEQ_TOO_LONG, DEVERR_SEQ_NEGATIVE, DEVERR_INDEX_RANGE, DEVERR_WAIT_TIMEOUT = range(5)
@@ -79,6 +79,10 @@ _SIGNATURES = {
                               _i, _f, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp]),
     "rra_attend_prompt": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _i, _vp, _vp]),
     "rra_attend_cache": (_i, [_vp, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
+    "rra_rms_norm": (_i, [_vp, _vp, _i, _vp, _f, _vp, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp]),
+    "rra_linear_scaled": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
+    "rra_attend_paged": (_i, [_vp, _ll, _vp, _vp, _ll, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
+                              _vp]),
     "rra_status_string": (ctypes.c_char_p, [_i]),
     "rra_last_error_message": (ctypes.c_char_p, []),
     "rra_launch_count": (ctypes.c_uint64, []),
@@ -113,7 +117,8 @@ def _load_fast(L: ctypes.CDLL):
                       "`python -m ragged_attention_token_gb300.build` builds the extension", RuntimeWarning, stacklevel=3)
         return None
     mod.bind(*(ctypes.cast(getattr(L, f), _vp).value
-               for f in ("rra_linear_epilogue", "rra_qk_norm_rope", "rra_attend_prompt", "rra_attend_cache")))
+               for f in ("rra_linear_epilogue", "rra_qk_norm_rope", "rra_attend_prompt", "rra_attend_cache", "rra_rms_norm",
+                         "rra_linear_scaled", "rra_attend_paged")))
     return mod
 
 
@@ -496,6 +501,86 @@ def attend_cache(q, k_cache, v_cache, kv_len, o, scale: float, stream=None):
                                           _typed(kv_len, torch.int32, "kv_len", (B,), dev), B, rows // B, cap, Hq, Hkv,
                                           d, float(scale), _DTYPE[dt], _typed(o, dt, "o", (rows, Hq, d), dev),
                                           _on(stream, dev))
+    if st:
+        _check(st)
+
+
+def rms_norm(x, cu_seqlens, B: int, y, weight=None, residual=None, sum_out=None, scale=None, eps: float = 1e-6, stream=None):
+    """rra_rms_norm: y = rms norm of x [cap, N] (+ residual, whose sum goes to sum_out) for the T = cu_seqlens[B] rows, times
+    weight; y of x's dtype, or torch.float8_e4m3fn with a scale [cap] a row."""
+    if _FAST is not None and _done(_FAST.norm(x, cu_seqlens, B, y, weight, residual, sum_out, scale, eps,
+                                              None if stream is None else _stream(stream))):
+        return
+    dev, dt, out = _device(x), x.dtype, y.dtype
+    cap, N = x.shape
+    if (residual is None) != (sum_out is None):
+        raise ValueError("residual and sum_out go together")
+    if (out is torch.float8_e4m3fn) != (scale is not None):
+        raise ValueError("scale goes with a y of torch.float8_e4m3fn")
+    rdt = dt if residual is None else residual.dtype
+    st = (_LIB or lib()).rra_rms_norm(_typed(x, dt, "x", None, dev), _typed(residual, rdt, "residual", (cap, N), dev),
+                                      _DTYPE[rdt], _typed(weight, torch.float32, "weight", (N,), dev), float(eps),
+                                      _cu(cu_seqlens, B, dev), B, cap, N, _DTYPE[dt],
+                                      _typed(sum_out, rdt, "sum_out", (cap, N), dev), _typed(y, out, "y", (cap, N), dev),
+                                      RRA_E4M3 if scale is not None else _DTYPE[out],
+                                      _typed(scale, torch.float32, "scale", (cap,), dev), _on(stream, dev))
+    if st:
+        _check(st)
+
+
+def linear_scaled(a, a_scale, w, w_scale, cu_seqlens, B: int, c, bias=None, act: int = ACT_NONE, residual=None, stream=None):
+    """rra_linear_scaled: c[t] = act(a_scale[t] * w_scale * (a[t] @ w.T) + bias) + residual[t] for the T = cu_seqlens[B]
+    packed rows, a [cap, K] and w [N, K] of torch.float8_e4m3fn."""
+    if _FAST is not None and _done(_FAST.scaled(a, a_scale, w, w_scale, cu_seqlens, B, c, bias, act, residual,
+                                                None if stream is None else _stream(stream))):
+        return
+    dev, out, f32, e4m3 = _device(a), c.dtype, torch.float32, torch.float8_e4m3fn
+    cap, K = a.shape
+    N = w.shape[0]
+    st = (_LIB or lib()).rra_linear_scaled(_typed(a, e4m3, "a", None, dev), _typed(a_scale, f32, "a_scale", (cap,), dev),
+                                           _typed(w, e4m3, "w", (N, K), dev), _typed(w_scale, f32, "w_scale", (N,), dev),
+                                           _typed(bias, f32, "bias", (N,), dev),
+                                           _typed(residual, out, "residual", (cap, N), dev), _cu(cu_seqlens, B, dev), B, cap,
+                                           K, N, int(act), _typed(c, out, "c", (cap, N), dev), _DTYPE[out],
+                                           _on(stream, dev))
+    if st:
+        _check(st)
+
+
+def _pages(t, dtype, name: str, shape, dev: int):
+    """(pointer, page stride) of [num_pages, page_size, Hkv, d] whose pages are contiguous and may lie apart."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, name, shape)
+    n, page, H, d = shape
+    s0, s1, s2, s3 = t.stride()
+    if (d > 1 and s3 != 1) or (H > 1 and s2 != d) or (page > 1 and s1 != H * d):
+        raise ValueError(f"{name}: each page must be contiguous")
+    return t.data_ptr(), (s0 if n > 1 else page * H * d)
+
+
+def attend_paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B: int, max_new: int, max_kv: int, o, scale: float,
+                 stream=None):
+    """rra_attend_paged: attention of the new tokens of each sequence, packed rows cu_seqlens[b] .. cu_seqlens[b+1] of
+    q [cap, Hq, d] (up to max_new of them), over its kv_len[b] <= max_kv keys in k_pages and v_pages [num_pages, page_size,
+    Hkv, d], whose pages page_table [B, width] lists."""
+    if _FAST is not None and _done(_FAST.paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B, max_new, max_kv, o,
+                                               scale, None if stream is None else _stream(stream))):
+        return
+    dev, dt, shape = _device(q), q.dtype, q.shape
+    cap, Hq, d = shape
+    pages, page, Hkv, _ = k_pages.shape
+    qp, qs = _rows(q, dt, "q", shape, dev)
+    kp, ks = _pages(k_pages, dt, "k_pages", (pages, page, Hkv, d), dev)
+    vp, vs = _pages(v_pages, dt, "v_pages", (pages, page, Hkv, d), dev)
+    if ks != vs:
+        raise ValueError(f"k_pages and v_pages: pages {ks} and {vs} elements apart, expected the same")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, width)")
+    st = (_LIB or lib()).rra_attend_paged(qp, qs, kp, vp, ks, pages, page,
+                                          _typed(page_table, torch.int32, "page_table", None, dev), page_table.shape[1],
+                                          _typed(kv_len, torch.int32, "kv_len", (B,), dev), _cu(cu_seqlens, B, dev), B, cap,
+                                          int(max_new), int(max_kv), Hq, Hkv, d, float(scale), _DTYPE[dt],
+                                          _typed(o, dt, "o", shape, dev), _on(stream, dev))
     if st:
         _check(st)
 
