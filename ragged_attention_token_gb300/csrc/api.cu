@@ -964,10 +964,16 @@ rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cac
   return RRA_OK;
 }
 
+size_t rra_attend_paged_workspace_bytes(int max_new, int cap, int Hq, int Hkv, int d) {
+  if (check_block_heads(1, cap, Hq, Hkv, d, RRA_BF16) != RRA_OK || max_new < 1) return 0;
+  return attend_paged_space(max_new < cap ? max_new : cap, Hq / Hkv, d);
+}
+
 rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
                             long long page_stride, int num_pages, int page_size, const int32_t* page_table,
                             int table_width, const int32_t* kv_len, const int32_t* cu_seqlens, int B, int cap, int max_new,
-                            int max_kv, int Hq, int Hkv, int d, float scale, rra_dtype dtype, void* o, void* stream) {
+                            int max_kv, int Hq, int Hkv, int d, float scale, rra_dtype dtype, void* o, void* workspace,
+                            size_t workspace_bytes, void* stream) {
   RRA_TRY(check_block_heads(B, cap, Hq, Hkv, d, dtype));
   if (page_size < 16 || page_size % 16 != 0 || page_size > 65536)
     return fail(RRA_ERR_UNSUPPORTED, "page_size=%d: a multiple of 16 up to 65536", page_size);
@@ -991,6 +997,16 @@ rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pag
   if (page_stride % 8 != 0) return fail(RRA_ERR_MISALIGNED, "page stride %lld not a multiple of 8", page_stride);
   const long long wq = 2LL * Hq * d;
   const RowSpan so{o, cap, wq, wq};
+  const size_t need = rra_attend_paged_workspace_bytes(max_new, cap, Hq, Hkv, d);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(RRA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(RRA_ERR_MISALIGNED, "workspace not 256-byte aligned");
+    const RowSpan sw{workspace, 1, static_cast<long long>(need), static_cast<long long>(need)};
+    if (!disjoint(sw, so) || !disjoint(sw, {q, cap, wq, 2 * q_stride}) || !disjoint(sw, {k_pages, num_pages, 2 * page_elems, 2 * page_stride}) ||
+        !disjoint(sw, {v_pages, num_pages, 2 * page_elems, 2 * page_stride}))
+      return fail(RRA_ERR_INVALID_ARG, "workspace overlaps another tensor");
+  }
   if (!disjoint(so, {q, cap, wq, 2 * q_stride}) || !disjoint(so, {k_pages, num_pages, 2 * page_elems, 2 * page_stride}) ||
       !disjoint(so, {v_pages, num_pages, 2 * page_elems, 2 * page_stride}))
     return fail(RRA_ERR_INVALID_ARG, "o overlaps an input");
@@ -1018,9 +1034,11 @@ rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pag
   g.o = o;
   g.err = error_word(*st);
   g.wait_limit = g_wait_limit.load();
-  cudaError_t e = launch_attend_paged(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream));
+  g.space = workspace;
+  int launches = 0;
+  cudaError_t e = launch_attend_paged(g, d, dtype, st->num_sms, static_cast<cudaStream_t>(stream), &launches);
+  g_launches += launches;
   if (e != cudaSuccess) return cuda_fail(e, "attend_paged launch");
-  g_launches += 1;
   return RRA_OK;
 }
 

@@ -124,7 +124,10 @@ struct PagedArgs {
   void* o;
   int32_t* err;
   long long wait_limit;
+  void* space;                             // workspace of attend_paged_space() bytes (0: not used)
+  long long unit_wait_limit;               // set by the launch
 };
-cudaError_t launch_attend_paged(const PagedArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream);
+size_t attend_paged_space(int max_new, int G, int d);
+cudaError_t launch_attend_paged(const PagedArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream, int* launches);
 
 }  // namespace rra

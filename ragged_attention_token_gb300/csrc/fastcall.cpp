@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -25,6 +26,7 @@ decltype(&rra_attend_cache) f_cache = nullptr;
 decltype(&rra_rms_norm) f_norm = nullptr;
 decltype(&rra_linear_scaled) f_scaled = nullptr;
 decltype(&rra_attend_paged) f_paged = nullptr;
+decltype(&rra_attend_paged_workspace_bytes) f_paged_bytes = nullptr;
 
 // One call's arguments, taken in order; `ok` turns false at the first that is not plain.
 struct Args {
@@ -360,7 +362,7 @@ Rows pages_of(Args& a, const at::Tensor* t, at::ScalarType st, int64_t n, int64_
   return r;
 }
 
-// paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B, max_new, max_kv, o, scale, stream)
+// paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B, max_new, max_kv, o, scale, workspace, stream)
 PyObject* paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
   try {
     Args a{v, n};
@@ -368,6 +370,8 @@ PyObject* paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const long long B = a.integer(), most_new = a.integer(), most_kv = a.integer();
     const at::Tensor* o = a.tensor();
     const float scale = a.real();
+    const at::Tensor* given = a.tensor(true);
+    const bool own_stream = a.i < n && v[a.i] == Py_None;
     void* s = a.stream();
     rra_dtype dt;
     if (!a.ok || q->dim() != 3 || k->dim() != 4 || table->dim() != 2 || !code(*q, dt)) return result(-1);
@@ -380,14 +384,26 @@ PyObject* paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int32_t* pl = dense<int32_t>(a, len, at::kInt, {B});
     const int32_t* pcu = offsets(a, cu, B);
     void* po = const_cast<void*>(dense(a, o, t, {cap, Hq, d}));
+    const void* space = dense(a, given, at::kByte, {-1});
     if (!a.ok || rk.stride != rv.stride || !fits(cap) || !fits(Hq) || !fits(Hkv) || !fits(d) || !fits(pages) || !fits(page) ||
         !fits(width))
       return result(-1);
+    size_t space_bytes = given != nullptr ? static_cast<size_t>(given->numel()) : 0;
+    at::Tensor made;                         // from the current stream's memory, so not for a call on another stream
+    if (given == nullptr) {
+      space_bytes = f_paged_bytes(static_cast<int>(most_new), static_cast<int>(cap), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d));
+      if (space_bytes > 0) {
+        if (!own_stream) return result(-1);
+        made = at::empty({static_cast<int64_t>(space_bytes)}, q->options().dtype(at::kByte));
+        space = made.data_ptr();
+      }
+    }
     rra_status st;
     Py_BEGIN_ALLOW_THREADS
     st = f_paged(rq.p, rq.stride, rk.p, rv.p, rk.stride, static_cast<int>(pages), static_cast<int>(page), pt,
                  static_cast<int>(width), pl, pcu, static_cast<int>(B), static_cast<int>(cap), static_cast<int>(most_new),
-                 static_cast<int>(most_kv), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d), scale, dt, po, s);
+                 static_cast<int>(most_kv), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d), scale, dt, po,
+                 const_cast<void*>(space), space_bytes, s);
     Py_END_ALLOW_THREADS
     return result(st);
   } catch (...) {
@@ -395,11 +411,11 @@ PyObject* paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
   }
 }
 
-// bind(linear, rope, prompt, cache, norm, scaled, paged): the addresses of librra's functions.
+// bind(linear, rope, prompt, cache, norm, scaled, paged, paged_bytes): the addresses of librra's functions.
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  constexpr int COUNT = 7;
+  constexpr int COUNT = 8;
   if (n != COUNT) {
-    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+    PyErr_SetString(PyExc_TypeError, "bind takes eight addresses");
     return nullptr;
   }
   void* p[COUNT];
@@ -417,6 +433,7 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   f_norm = reinterpret_cast<decltype(f_norm)>(p[4]);
   f_scaled = reinterpret_cast<decltype(f_scaled)>(p[5]);
   f_paged = reinterpret_cast<decltype(f_paged)>(p[6]);
+  f_paged_bytes = reinterpret_cast<decltype(f_paged_bytes)>(p[7]);
   Py_RETURN_NONE;
 }
 

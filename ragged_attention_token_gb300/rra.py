@@ -82,7 +82,8 @@ _SIGNATURES = {
     "rra_rms_norm": (_i, [_vp, _vp, _i, _vp, _f, _vp, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp]),
     "rra_linear_scaled": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
     "rra_attend_paged": (_i, [_vp, _ll, _vp, _vp, _ll, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
-                              _vp]),
+                              _vp, _sz, _vp]),
+    "rra_attend_paged_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "rra_status_string": (ctypes.c_char_p, [_i]),
     "rra_last_error_message": (ctypes.c_char_p, []),
     "rra_launch_count": (ctypes.c_uint64, []),
@@ -118,7 +119,7 @@ def _load_fast(L: ctypes.CDLL):
         return None
     mod.bind(*(ctypes.cast(getattr(L, f), _vp).value
                for f in ("rra_linear_epilogue", "rra_qk_norm_rope", "rra_attend_prompt", "rra_attend_cache", "rra_rms_norm",
-                         "rra_linear_scaled", "rra_attend_paged")))
+                         "rra_linear_scaled", "rra_attend_paged", "rra_attend_paged_workspace_bytes")))
     return mod
 
 
@@ -558,13 +559,20 @@ def _pages(t, dtype, name: str, shape, dev: int):
     return t.data_ptr(), (s0 if n > 1 else page * H * d)
 
 
+def attend_paged_workspace(max_new: int, cap: int, Hq: int, Hkv: int, d: int, device="cuda"):
+    """A workspace for rra_attend_paged calls of these sizes (calls that may run at once need one each); None where none is used."""
+    n = int(lib().rra_attend_paged_workspace_bytes(int(max_new), cap, Hq, Hkv, d))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
 def attend_paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B: int, max_new: int, max_kv: int, o, scale: float,
-                 stream=None):
+                 workspace=None, stream=None):
     """rra_attend_paged: attention of the new tokens of each sequence, packed rows cu_seqlens[b] .. cu_seqlens[b+1] of
     q [cap, Hq, d] (up to max_new of them), over its kv_len[b] <= max_kv keys in k_pages and v_pages [num_pages, page_size,
-    Hkv, d], whose pages page_table [B, width] lists."""
+    Hkv, d], whose pages page_table [B, width] lists.  Without a workspace (attend_paged_workspace) the call takes one from
+    torch's allocator, on its stream."""
     if _FAST is not None and _done(_FAST.paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B, max_new, max_kv, o,
-                                               scale, None if stream is None else _stream(stream))):
+                                               scale, workspace, None if stream is None else _stream(stream))):
         return
     dev, dt, shape = _device(q), q.dtype, q.shape
     cap, Hq, d = shape
@@ -576,11 +584,18 @@ def attend_paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B: int, ma
         raise ValueError(f"k_pages and v_pages: pages {ks} and {vs} elements apart, expected the same")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, width)")
+    if workspace is None and q.is_cuda:
+        if stream is None:
+            workspace = attend_paged_workspace(max_new, cap, Hq, Hkv, d, q.device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=q.device)):
+                workspace = attend_paged_workspace(max_new, cap, Hq, Hkv, d, q.device)
     st = (_LIB or lib()).rra_attend_paged(qp, qs, kp, vp, ks, pages, page,
                                           _typed(page_table, torch.int32, "page_table", None, dev), page_table.shape[1],
                                           _typed(kv_len, torch.int32, "kv_len", (B,), dev), _cu(cu_seqlens, B, dev), B, cap,
                                           int(max_new), int(max_kv), Hq, Hkv, d, float(scale), _DTYPE[dt],
-                                          _typed(o, dt, "o", shape, dev), _on(stream, dev))
+                                          _typed(o, dt, "o", shape, dev), _typed(workspace, torch.uint8, "workspace", None, dev),
+                                          0 if workspace is None else workspace.numel(), _on(stream, dev))
     if st:
         _check(st)
 

@@ -65,7 +65,7 @@ def test_linear_scaled_refusals(L, kw, want):
 
 PAGED = dict(q=0x1000000, qs=2048, k=0x20000000, v=0x30000000, ps=64 * 2 * 128, pages=9, page=64, table=0x400, width=4,
              lens=0x300, cu=0x500, B=2, cap=64, new=64, kv=256, Hq=16, Hkv=2, d=128, scale=0.1, dt=rra.RRA_F16, o=0x4000000,
-             stream=None)
+             ws=0x50000000, wsb=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -77,9 +77,20 @@ PAGED = dict(q=0x1000000, qs=2048, k=0x20000000, v=0x30000000, ps=64 * 2 * 128, 
     (dict(table=None), INV), (dict(o=None), INV), (dict(lens=0x301), MIS), (dict(table=0x402), MIS), (dict(cu=0x501), MIS),
     (dict(k=0x20000004), MIS), (dict(v=0x30000008), MIS), (dict(qs=2052), MIS), (dict(qs=2040), INV),
     (dict(ps=64 * 2 * 128 - 8), INV), (dict(ps=64 * 2 * 128 + 4), MIS), (dict(ps=1 << 36), INV), (dict(o=0x20000000), INV),
-    (dict(o=0x30000000 + 9 * 64 * 2 * 128 * 2 - 16), INV), (dict(o=0x1000000 + 2048), INV)])
+    (dict(o=0x30000000 + 9 * 64 * 2 * 128 * 2 - 16), INV), (dict(o=0x1000000 + 2048), INV), (dict(ws=None), INV),
+    (dict(wsb=1000), INV), (dict(ws=0x50000010), MIS), (dict(ws=0x4000000 - 256), INV), (dict(ws=0x1000000), INV),
+    (dict(ws=0x20000100), INV), (dict(ws=0x30000000 - 256), INV)])
 def test_attend_paged_refusals(L, kw, want):
     assert _call(L.rra_attend_paged, PAGED, kw) == want
+
+
+def test_attend_paged_workspace_bytes(L):
+    f = L.rra_attend_paged_workspace_bytes
+    assert f(1, 4, 16, 2, 128) == 0 and f(2, 64, 16, 2, 128) == 0          # a few rows need none
+    assert 0 < f(3, 64, 16, 2, 128) < f(64, 64, 16, 2, 128) == f(1 << 30, 64, 16, 2, 128)
+    assert f(64, 1, 16, 2, 128) == 0                                        # no more new tokens than rows
+    assert f(64, 64, 256, 1, 64) == 0                                       # more heads to a group than a tile has rows
+    assert f(0, 64, 16, 2, 128) == 0 and f(64, 64, 16, 3, 128) == 0 and f(64, 64, 16, 2, 96) == 0
 
 
 def test_binding_refuses_before_the_library():
