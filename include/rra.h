@@ -624,9 +624,9 @@ RRA_API rra_status rra_linear_scaled(const void* a, const float* a_scale, const 
  * such a sequence is not written.  A table entry in use outside [0, num_pages) records RRA_DEVERR_INDEX_RANGE, and page 0
  * is read in its place.  Products, sums and the values' limits as in rra_attend_prompt; a call repeated gives the same bits. */
 /* workspace: rra_attend_paged_workspace_bytes() bytes of device memory, 256-byte aligned, which the call writes and reads and
- * which need not be set to anything; NULL where that is 0 (a few new tokens).  Where keys of one sequence are shared
+ * which need not be set to anything; NULL where that is 0 (a few new tokens on short caches).  Where keys of one sequence are shared
  * out among SMs their sums meet there, and the call is two launches.  Calls that may run at once need one each. */
-RRA_API size_t rra_attend_paged_workspace_bytes(int max_new, int cap, int Hq, int Hkv, int d);
+RRA_API size_t rra_attend_paged_workspace_bytes(int B, int cap, int max_new, int max_kv, int Hq, int Hkv, int d);
 RRA_API rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
                                     long long page_stride, int num_pages, int page_size, const int32_t* page_table,
                                     int table_width, const int32_t* kv_len, const int32_t* cu_seqlens, int B, int cap,

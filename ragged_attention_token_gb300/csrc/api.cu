@@ -964,9 +964,9 @@ rra_status rra_attend_cache(const void* q, long long q_stride, const void* k_cac
   return RRA_OK;
 }
 
-size_t rra_attend_paged_workspace_bytes(int max_new, int cap, int Hq, int Hkv, int d) {
-  if (check_block_heads(1, cap, Hq, Hkv, d, RRA_BF16) != RRA_OK || max_new < 1) return 0;
-  return attend_paged_space(max_new < cap ? max_new : cap, Hq / Hkv, d);
+size_t rra_attend_paged_workspace_bytes(int B, int cap, int max_new, int max_kv, int Hq, int Hkv, int d) {
+  if (check_block_heads(B, cap, Hq, Hkv, d, RRA_BF16) != RRA_OK || max_new < 1 || max_kv < 1) return 0;
+  return attend_paged_space(B, max_new < cap ? max_new : cap, max_kv, Hkv, Hq / Hkv, d);
 }
 
 rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pages, const void* v_pages,
@@ -997,7 +997,7 @@ rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pag
   if (page_stride % 8 != 0) return fail(RRA_ERR_MISALIGNED, "page stride %lld not a multiple of 8", page_stride);
   const long long wq = 2LL * Hq * d;
   const RowSpan so{o, cap, wq, wq};
-  const size_t need = rra_attend_paged_workspace_bytes(max_new, cap, Hq, Hkv, d);
+  const size_t need = rra_attend_paged_workspace_bytes(B, cap, max_new, max_kv, Hq, Hkv, d);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
       return fail(RRA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace == nullptr ? 0 : workspace_bytes, need);

@@ -425,8 +425,8 @@ constexpr uint32_t GB_TAIL = 144;       // [2] a V block's tail to zero; zeroed
 constexpr uint32_t GB_DRAIN = 160;
 constexpr uint32_t GW_TMEM = 168, GW_ABORT = 172;
 constexpr uint32_t G_DESC = 192;        // [2] x 48 bytes
-constexpr uint32_t G_PLAN = 288;        // the CTA's first piece and its end, 40 bytes
-constexpr uint32_t G_SCAN = 336;        // [8] x 8 bytes, one a warp
+constexpr uint32_t G_PLAN = 288;        // the CTA's first piece and its end, 40 bytes each
+constexpr uint32_t G_SCAN = 368;        // [8] x 8 bytes, one a warp
 
 // What a CTA does at a time: key blocks b0 .. b1 of a unit of up to 128 rows (tokens q0 .. of a sequence times the G heads of
 // key/value head hk).  slot < 0: the unit's only piece, whose rows are written out; else where its sums go.
@@ -477,8 +477,10 @@ __device__ __forceinline__ long long paged_work(int n, int len, int tokens) {
 // ends); the unit starts at work `start` of all.
 struct PagedCut {
   int b, hk, q0, off;
+  int s0, n, len;                            // of sequence b
   long long start;
 };
+static_assert(2 * sizeof(PagedCut) <= G_SCAN - G_PLAN, "the plan's place");
 
 // The cut after snapping, as work of its unit of w: not so near one of the unit's ends that a piece would be of a block or two.
 __device__ __forceinline__ int paged_snap(int off, int w) {
@@ -599,6 +601,9 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
           const long long per = in / a.Hkv;
           PagedCut c;
           c.b = b;
+          c.s0 = sq.s0;
+          c.n = sq.n;
+          c.len = sq.len;
           c.hk = static_cast<int>((x - seq_from) / per);
           long long at = seq_from + c.hk * per;
           c.q0 = 0;
@@ -662,31 +667,31 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
         bool more = cut.b < a.B && !(cut.b == end.b && cut.hk == end.hk && cut.q0 == end.q0 && cut.off >= end.off);
         if (more && (cut.b > end.b || (cut.b == end.b && (cut.hk > end.hk || (cut.hk == end.hk && cut.q0 > end.q0))))) more = false;
         if (more) {
-          const PagedSeq sq(a, cut.b, false);
-          if (!sq.valid || cut.q0 >= sq.n) {                 // to the next head, or the next sequence with rows
+          if (cut.q0 >= cut.n) {                             // to the next head, or the next sequence with rows
             cut.q0 = 0;
             cut.off = 0;
-            if (!sq.valid || sq.n == 0 || ++cut.hk == a.Hkv) {
+            if (++cut.hk == a.Hkv) {
               cut.hk = 0;
-              ++cut.b;
-              while (cut.b < a.B) {
-                const int b = cut.b + lane;
-                const unsigned live = __ballot_sync(0xffffffffu, b < a.B && a.cu[min(b, a.B - 1) + 1] > a.cu[min(b, a.B - 1)]);
-                if (live != 0u) {
-                  cut.b += __ffs(live) - 1;
-                  break;
-                }
-                cut.b += 32;
+              for (++cut.b; cut.b < a.B; cut.b += 32) {
+                const PagedSeq sq(a, min(cut.b + lane, a.B - 1), false);
+                const unsigned live = __ballot_sync(0xffffffffu, cut.b + lane < a.B && sq.valid && sq.n > 0);
+                if (live == 0u) continue;
+                const int src = __ffs(live) - 1;
+                cut.b += src;
+                cut.s0 = __shfl_sync(0xffffffffu, sq.s0, src);
+                cut.n = __shfl_sync(0xffffffffu, sq.n, src);
+                cut.len = __shfl_sync(0xffffffffu, sq.len, src);
+                break;
               }
             }
             continue;
           }
-          const int nb = paged_blocks(sq.n, sq.len, cut.q0, tokens), w = PG_START + nb;
+          const int nb = paged_blocks(cut.n, cut.len, cut.q0, tokens), w = PG_START + nb;
           const bool last = cut.b == end.b && cut.hk == end.hk && cut.q0 == end.q0;
           const int off1 = last ? end.off : w;
-          u.s0 = sq.s0;
-          u.n = sq.n;
-          u.len = sq.len;
+          u.s0 = cut.s0;
+          u.n = cut.n;
+          u.len = cut.len;
           u.q0 = cut.q0;
           u.hk = cut.hk;
           u.b = cut.b;
@@ -701,8 +706,8 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
               if (x >= w || paged_snap(static_cast<int>(x), w) == w) break;
             }
             int* j = space.join + me * 8;
-            j[1] = sq.s0 + cut.q0;
-            j[2] = min(tokens, sq.n - cut.q0);
+            j[1] = cut.s0 + cut.q0;
+            j[2] = min(tokens, cut.n - cut.q0);
             j[3] = cut.hk;
             j[0] = pieces;
           }
@@ -1000,32 +1005,49 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
   }
 }
 
-// Few rows of a head group go as rows of a warp's tile, others as tiles of 128.
-bool paged_by_chunks(int max_new, int G) { return G <= PT && static_cast<long long>(max_new) * G > C_ROWS; }
+// Up to 16 rows of a head group go as rows of a warp's tile where the bounds leave little to read: there the fewer steps count
+// (next tokens, 32 / 8 heads, d = 128: 4 short contexts of 12 heads 4.7 us, as tiles of 128 rows 11.8; 4 x 4096 keys 17.4
+// / 25.3; one of 16384 25 / 28).  A longer cache's time is its bytes', and the tiles' even shares fit contexts of all lengths
+// (32 of 1 to 16384 168 / 168; one of 131072 136 / 91; 2 of 16384 among 38 of 100 187 / 39).
+bool paged_by_chunks(int B, int max_new, int max_kv, int Hkv, int G, int d) {
+  if (G > PT) return false;
+  if (static_cast<long long>(max_new) * G > C_ROWS) return true;
+  return static_cast<double>(B) * max_kv * Hkv * d * 4 > 128e6;
+}
 
-// Joins the pieces of the unit that CTA blockIdx.x began and the CTAs behind it went on with, in their order.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int space_rows) {
+// Joins the pieces of the unit that CTA blockIdx.x began and the CTAs behind it went on with: 8 neighbouring columns of a row at
+// a time.  Where the pieces are many, eight lanes share them (every eighth each), so that no chain of loads is as long as
+// they are; where they are few, a lane has them all, and a warp reads 512 bytes at a time.  (2048 tokens on 16384 keys, 512
+// units in 2 or 3 pieces: 384 us in all, 423 with eight lanes; 5 tokens on 16384 keys, 8 units in 22: 31 and 36.)  The
+// order of additions is that of the pieces by lane, then of the lanes.
+constexpr int PJ_THREADS = 128, PJ_SPLIT = 8, PJ_MANY = 5;
+template <typename T, int D, int LANES>
+__device__ __forceinline__ void paged_join(const PagedArgs& a, const PagedSpace& space, const int4 j) {
   constexpr bool BF = IsBf16<T>::value == 1;
-  start_dependent();
-  const PagedSpace space = paged_space(a.space, space_rows);
-  const int me = static_cast<int>(blockIdx.x);
-  const int* j = space.join + me * 8;
-  const int pieces = j[0];
-  if (pieces < 2) return;
-  const int t0 = j[1], G = a.Hq / a.Hkv, rows = j[2] * G, hk = j[3];
+  const int me = static_cast<int>(blockIdx.x), pieces = j.x, G = a.Hq / a.Hkv, rows = j.z * G, hk = j.w;
+  const int l = static_cast<int>(threadIdx.x) % LANES;
   auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * me + 1 : 2 * (me + p)); };
-  for (int e = static_cast<int>(blockIdx.y) * 128 + static_cast<int>(threadIdx.x); e < rows * (D / 8); e += 128 * static_cast<int>(gridDim.y)) {
-    const int row = e % rows, c = e / rows;
+  constexpr int PER_WARP = 32 / LANES, PER_CTA = PJ_THREADS / LANES;
+  const int items = rows * (D / 8);
+  // Whole warps go round together: their items may end before the round does.
+  for (int e0 = static_cast<int>(blockIdx.y) * PER_CTA + static_cast<int>(threadIdx.x) / 32 * PER_WARP; e0 < items; e0 += PER_CTA * PJ_SPLIT) {
+    const int e = min(e0 + static_cast<int>(threadIdx.x) % 32 / LANES, items - 1);
+    const int c = e / rows, row = e - c * rows;
     float top = -INFINITY, sum = 0.f, y[8] = {};
     bool whole = true;                       // a CTA that gave up a wait has written no sums
-    for (int p = 0; p < pieces; ++p) {
+#pragma unroll 4
+    for (int p = l; p < pieces; p += LANES) {
       whole = whole && space.state[slot_of(p) * 4 + (row >> 5)] == 1;
       top = fmaxf(top, space.ml[slot_of(p) * space.rows + row].x);
     }
-    if (!whole) continue;
+#pragma unroll
+    for (int k = 1; k < LANES; k <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      whole = __shfl_xor_sync(0xffffffffu, static_cast<int>(whole), k) != 0 && whole;
+    }
     const float ref = top == -INFINITY ? 0.f : top;
-    for (int p = 0; p < pieces; ++p) {
+#pragma unroll 2
+    for (int p = l; p < pieces; p += LANES) {
       const float2 ml = space.ml[slot_of(p) * space.rows + row];
       const float* o = space.o + ((slot_of(p) * (D / 4) + 2 * c) * space.rows + row) * 4;
       const float4 u = *reinterpret_cast<const float4*>(o), v = *reinterpret_cast<const float4*>(o + static_cast<size_t>(space.rows) * 4);
@@ -1040,15 +1062,30 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int 
       y[6] = fmaf(f, v.z, y[6]);
       y[7] = fmaf(f, v.w, y[7]);
     }
+#pragma unroll
+    for (int k = 1; k < LANES; k <<= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], k);
+    }
+    if (l != 0 || !whole) continue;
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = BF ? pack2<__nv_bfloat162>(y[2 * i] * inv, y[2 * i + 1] * inv) : pack2<__half2>(y[2 * i] * inv, y[2 * i + 1] * inv);
     const int t = row / G;
-    T* out = static_cast<T*>(a.o) + ((static_cast<long long>(t0) + t) * a.Hq + hk * G + (row - t * G)) * D + 8 * c;
+    T* out = static_cast<T*>(a.o) + ((static_cast<long long>(j.y) + t) * a.Hq + hk * G + (row - t * G)) * D + 8 * c;
     *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+template <typename T, int D>
+__global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PagedArgs a, int space_rows) {
+  start_dependent();
+  const PagedSpace space = paged_space(a.space, space_rows);
+  const int4 j = *reinterpret_cast<const int4*>(space.join + blockIdx.x * 8);   // pieces, first row of q, tokens, hk
+  if (j.x >= PJ_MANY) paged_join<T, D, 8>(a, space, j);
+  else if (j.x > 1) paged_join<T, D, 1>(a, space, j);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 paged_encode_fn() {
@@ -1136,8 +1173,8 @@ cudaError_t launch_chunk(const PagedArgs& a, int num_sms, cudaStream_t stream, i
   if ((e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, box_rows, rows)) != cudaSuccess) return e;
   *launches += 1;
   if (grid == 1) return cudaSuccess;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), PJ_SPLIT);
+  cfg.blockDim = dim3(PJ_THREADS);
   cfg.dynamicSmemBytes = 0;
   if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D>, a, rows)) != cudaSuccess) return e;
   *launches += 1;
@@ -1146,7 +1183,7 @@ cudaError_t launch_chunk(const PagedArgs& a, int num_sms, cudaStream_t stream, i
 
 template <typename T, int D>
 cudaError_t launch_d(PagedArgs a, int num_sms, cudaStream_t stream, int* launches) {
-  if (!paged_by_chunks(a.max_new, a.Hq / a.Hkv)) return launch_few<T, D>(a, num_sms, stream, launches);
+  if (!paged_by_chunks(a.B, a.max_new, a.max_kv, a.Hkv, a.Hq / a.Hkv, D)) return launch_few<T, D>(a, num_sms, stream, launches);
   const long long each = std::min(a.wait_limit > 0 ? a.wait_limit : WAIT_LIMIT_CYCLES, 1LL << 38);
   a.unit_wait_limit = each * (1 + a.max_kv / PT);            // at most 2^38 x 2^23
   return a.wait_limit > 0 ? launch_chunk<T, D, true>(a, num_sms, stream, launches) : launch_chunk<T, D, false>(a, num_sms, stream, launches);
@@ -1154,8 +1191,8 @@ cudaError_t launch_d(PagedArgs a, int num_sms, cudaStream_t stream, int* launche
 
 }  // namespace
 
-size_t attend_paged_space(int max_new, int G, int d) {
-  return paged_by_chunks(max_new, G) ? paged_space_bytes(paged_space_rows(max_new, G), d) : 0;
+size_t attend_paged_space(int B, int max_new, int max_kv, int Hkv, int G, int d) {
+  return paged_by_chunks(B, max_new, max_kv, Hkv, G, d) ? paged_space_bytes(paged_space_rows(max_new, G), d) : 0;
 }
 
 cudaError_t launch_attend_paged(const PagedArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream, int* launches) {

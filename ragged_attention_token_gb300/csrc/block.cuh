@@ -127,7 +127,7 @@ struct PagedArgs {
   void* space;                             // workspace of attend_paged_space() bytes (0: not used)
   long long unit_wait_limit;               // set by the launch
 };
-size_t attend_paged_space(int max_new, int G, int d);
+size_t attend_paged_space(int B, int max_new, int max_kv, int Hkv, int G, int d);
 cudaError_t launch_attend_paged(const PagedArgs& a, int d, rra_dtype dt, int num_sms, cudaStream_t stream, int* launches);
 
 }  // namespace rra

@@ -391,7 +391,7 @@ PyObject* paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
     size_t space_bytes = given != nullptr ? static_cast<size_t>(given->numel()) : 0;
     at::Tensor made;                         // from the current stream's memory, so not for a call on another stream
     if (given == nullptr) {
-      space_bytes = f_paged_bytes(static_cast<int>(most_new), static_cast<int>(cap), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d));
+      space_bytes = f_paged_bytes(static_cast<int>(B), static_cast<int>(cap), static_cast<int>(most_new), static_cast<int>(most_kv), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(d));
       if (space_bytes > 0) {
         if (!own_stream) return result(-1);
         made = at::empty({static_cast<int64_t>(space_bytes)}, q->options().dtype(at::kByte));

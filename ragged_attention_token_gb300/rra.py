@@ -83,7 +83,7 @@ _SIGNATURES = {
     "rra_linear_scaled": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp]),
     "rra_attend_paged": (_i, [_vp, _ll, _vp, _vp, _ll, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
                               _vp, _sz, _vp]),
-    "rra_attend_paged_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "rra_attend_paged_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "rra_status_string": (ctypes.c_char_p, [_i]),
     "rra_last_error_message": (ctypes.c_char_p, []),
     "rra_launch_count": (ctypes.c_uint64, []),
@@ -559,9 +559,9 @@ def _pages(t, dtype, name: str, shape, dev: int):
     return t.data_ptr(), (s0 if n > 1 else page * H * d)
 
 
-def attend_paged_workspace(max_new: int, cap: int, Hq: int, Hkv: int, d: int, device="cuda"):
+def attend_paged_workspace(B: int, cap: int, max_new: int, max_kv: int, Hq: int, Hkv: int, d: int, device="cuda"):
     """A workspace for rra_attend_paged calls of these sizes (calls that may run at once need one each); None where none is used."""
-    n = int(lib().rra_attend_paged_workspace_bytes(int(max_new), cap, Hq, Hkv, d))
+    n = int(lib().rra_attend_paged_workspace_bytes(B, cap, int(max_new), int(max_kv), Hq, Hkv, d))
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
@@ -586,10 +586,10 @@ def attend_paged(q, k_pages, v_pages, page_table, kv_len, cu_seqlens, B: int, ma
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, width)")
     if workspace is None and q.is_cuda:
         if stream is None:
-            workspace = attend_paged_workspace(max_new, cap, Hq, Hkv, d, q.device)
+            workspace = attend_paged_workspace(B, cap, max_new, max_kv, Hq, Hkv, d, q.device)
         else:
             with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=q.device)):
-                workspace = attend_paged_workspace(max_new, cap, Hq, Hkv, d, q.device)
+                workspace = attend_paged_workspace(B, cap, max_new, max_kv, Hq, Hkv, d, q.device)
     st = (_LIB or lib()).rra_attend_paged(qp, qs, kp, vp, ks, pages, page,
                                           _typed(page_table, torch.int32, "page_table", None, dev), page_table.shape[1],
                                           _typed(kv_len, torch.int32, "kv_len", (B,), dev), _cu(cu_seqlens, B, dev), B, cap,

@@ -85,12 +85,12 @@ def test_attend_paged_refusals(L, kw, want):
 
 
 def test_attend_paged_workspace_bytes(L):
-    f = L.rra_attend_paged_workspace_bytes
-    assert f(1, 4, 16, 2, 128) == 0 and f(2, 64, 16, 2, 128) == 0          # a few rows need none
-    assert 0 < f(3, 64, 16, 2, 128) < f(64, 64, 16, 2, 128) == f(1 << 30, 64, 16, 2, 128)
-    assert f(64, 1, 16, 2, 128) == 0                                        # no more new tokens than rows
-    assert f(64, 64, 256, 1, 64) == 0                                       # more heads to a group than a tile has rows
-    assert f(0, 64, 16, 2, 128) == 0 and f(64, 64, 16, 3, 128) == 0 and f(64, 64, 16, 2, 96) == 0
+    f = lambda B=2, cap=64, new=64, kv=256, Hq=16, Hkv=2, d=128: L.rra_attend_paged_workspace_bytes(B, cap, new, kv, Hq, Hkv, d)
+    assert f(new=1) == 0 and f(new=2) == 0                                  # a few rows on short caches need none
+    assert 0 < f(new=1, kv=1 << 20) <= f(new=3) < f(new=6) < f() == f(new=1 << 30)
+    assert f(cap=1) == 0                                                    # no more new tokens than rows
+    assert f(Hq=256, Hkv=1, d=64) == 0                                      # more heads to a group than a tile has rows
+    assert f(new=0) == 0 and f(kv=0) == 0 and f(B=0) == 0 and f(Hkv=3) == 0 and f(d=96) == 0
 
 
 def test_binding_refuses_before_the_library():

@@ -123,6 +123,27 @@ def test_attend_paged_batches_and_lengths(B, most):
     Paged([1] * B, kv, 4, 1, 128, 64, torch.bfloat16, seed=B).run()
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(8, 2, 128, 64), (1, 1, 64, 16), (12, 6, 64, 48)])
+def test_attend_paged_tokens_by_tiles(Hq, Hkv, d, page):
+    """Next tokens with loose or long bounds go as tiles too: contexts of very different lengths, some empty."""
+    kv = [9000, 0, 1, 100, 17, 4095, 4096, 4097, 128, 0, 33, 2000] * 3
+    p = Paged([1, 1, 1, 0] * 9, kv, Hq, Hkv, d, page, torch.bfloat16, seed=Hq, gap=1, joint=True)
+    p.table = torch.cat([p.table, p.table.new_full((36, (1 << 20) // page), -7)], 1)
+    p.run(max_kv=1 << 20)
+
+
+@pytest.mark.parametrize("B", [257, 700])
+def test_attend_paged_many_sequences(B):
+    """More sequences than a CTA has threads, with rows and without."""
+    rng = np.random.default_rng(B)
+    new = [int(x) for x in rng.choice([0, 0, 1, 1, 1, 9, 40], B)]
+    kv = [n + int(x) for n, x in zip(new, rng.integers(0, 90, B))]
+    Paged(new, kv, 4, 2, 64, 16, torch.bfloat16, seed=B).run()
+    new = [0] * B
+    new[B - 2] = 70
+    Paged(new, kv[:B - 2] + [500, 0], 4, 2, 128, 16, torch.bfloat16, seed=B).run()
+
+
 @pytest.mark.parametrize("n,m", [(5, 9000), (48, 20000), (150, 5000), (600, 3000), (1, 40000)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attend_paged_long_caches(n, m, d):
