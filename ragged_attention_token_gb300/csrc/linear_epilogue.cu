@@ -259,6 +259,66 @@ template <> struct Chunk<__half> {
   }
 };
 
+// 32 rows (this warp's lanes of TMEM) by C columns as fragments: v[C / 2 h + 4 n + e] is row g + 16 h + 8 (e >> 1), column
+// 8 n + 2 q + (e & 1), g = lane / 4, q = lane % 4.  A lane so meets C / 4 columns instead of C: their scales and
+// biases are that many fewer reads of shared memory.
+template <int C>
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[C]) {
+  static_assert(C == 32 || C == 64, "four or eight groups of 8 columns");
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t* x = r + h * (C / 2);
+    const uint32_t at = taddr + (static_cast<uint32_t>(16 * h) << 16);
+#pragma unroll
+    for (int k = 0; k < C / 32; ++k, x += 16)
+      asm volatile(
+          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+          : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+            "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+          : "r"(at + 32 * k)
+          : "memory");
+  }
+  // The wait is tied to the registers, so that no use of them is scheduled before it.
+#pragma unroll
+  for (int i = 0; i < C; i += 16)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]),
+                   "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]), "+r"(r[i + 12]),
+                   "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15])
+                 :
+                 : "memory");
+}
+// Two neighbouring outputs: added to floats from memory's form, and rounded to it.
+__device__ __forceinline__ void add_two(float& x, float& y, uint32_t at, float) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  x += v.x;
+  y += v.y;
+}
+__device__ __forceinline__ void add_two(float& x, float& y, uint32_t at, __nv_bfloat16) {
+  const uint32_t w = ld_shared_u32(at);
+  x += __uint_as_float(w << 16);
+  y += __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void add_two(float& x, float& y, uint32_t at, __half) {
+  const uint32_t w = ld_shared_u32(at);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x += f.x;
+  y += f.y;
+}
+__device__ __forceinline__ void put_two(uint32_t at, float x, float y, float) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void put_two(uint32_t at, float x, float y, __nv_bfloat16) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+  st_shared_u32(at, *reinterpret_cast<const uint32_t*>(&t));
+}
+__device__ __forceinline__ void put_two(uint32_t at, float x, float y, __half) {
+  const __half2 t = __floats2half2_rn(x, y);
+  st_shared_u32(at, *reinterpret_cast<const uint32_t*>(&t));
+}
+
 // How the T x N outputs are cut into tiles: `wide` tiles of ln columns in whole
 // rounds over the pairs, then those of the last round cut f ways (1, 2 or 4) where that
 // round has pairs to spare.
@@ -299,7 +359,8 @@ __host__ __device__ __forceinline__ Tiling make_tiling(int T, int N, int pairs, 
 // row tile read all of W again: 8192 x 4096 x 16384 took 780 us under load.
 constexpr int L_BAND = 8;
 __device__ __forceinline__ void tile_at(long long t, int mt, int nt, int& m, int& n) {
-  const int band = static_cast<int>(t / (static_cast<long long>(L_BAND) * nt));
+  const unsigned per = static_cast<unsigned>(L_BAND) * static_cast<unsigned>(nt);   // below 2^21
+  const int band = t < (1LL << 32) ? static_cast<int>(static_cast<unsigned>(t) / per) : static_cast<int>(t / per);
   const int rows = min(L_BAND, mt - band * L_BAND);
   const int r = static_cast<int>(t - static_cast<long long>(band) * L_BAND * nt);
   m = band * L_BAND + r % rows;
@@ -452,13 +513,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
     } else {
       // ------------------------------------------------------------ epilogue
       using Ch = Chunk<Tout>;
-      constexpr int CPP = 8 * Ch::N;                     // columns of a 128-byte piece
-      const int quad = warp & 3, half = (warp - 2) >> 2; // TMEM lane quadrant; which pieces
+      constexpr int CHUNKS = 8;
+      constexpr int CPP = CHUNKS * Ch::N;                // columns of a 128-byte piece
+      constexpr int GROUPS = L_EPI_WARPS / 4;
+      const int quad = warp & 3, group = (warp - 2) >> 2; // TMEM lane quadrant; which pieces
       const uint32_t stg = base + L_OFF_OUT + static_cast<uint32_t>(warp - 2) * L_OUT_BYTES;
+      // Chunk k of row r of the staging, turned by the row so that neither rows nor columns of chunks meet a bank twice.
+      auto staged = [&](int r, int k) { return stg + r * 128 + ((k ^ (r & 7)) << 4); };
       const uint32_t acc_empty[2] = {map_rank(bar(LB_ACC_EMPTY, 0), 0), map_rank(bar(LB_ACC_EMPTY, 1), 0)};
       uint32_t i = 0;
       // This lane's columns of the bias of piece p (of the tile at column n0): lane, and lane + 32 of a 64-column piece.
-      float bias0 = 0.f, bias1 = 0.f, ws0 = 0.f, ws1 = 0.f, row_scale = 0.f;   // the same columns' scales; this lane's row's
+      float bias0 = 0.f, bias1 = 0.f, ws0 = 0.f, ws1 = 0.f;   // ws: those columns' scales
+      float row_scale[4] = {}, next_scale = 0.f;         // of this lane's rows in fragments: g, g + 8, g + 16, g + 24; of row `lane` of the next tile
       auto load_bias = [&](int col0) {
         if (col0 >= a.N) return;
         const int c0 = min(col0 + lane, a.N - 1), c1 = min(col0 + 32 + lane, a.N - 1);
@@ -470,16 +536,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         bias0 = a.bias[c0];
         if (CPP > 32) bias1 = a.bias[c1];
       };
-      for (long long t = pair; t < g.all; t += pairs) {
-        int m0, n0, width;
-        piece_at(g, t, a.N, m0, n0, width);
-        if (width == 0) continue;
-        m0 = m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
-        load_bias(n0 + half * CPP);
-        if (SCALED<Tin> && m0 < T) row_scale = a.a_scale[min(m0 + lane, T - 1)];
+      // The next piece of work with columns, found and its scales asked for while this one is drained.
+      int m0 = 0, n0 = 0, width = 0, next_m0 = 0, next_n0 = 0, next_width = 0;
+      auto find_next = [&](long long& t) {
+        next_width = 0;
+        for (; t < g.all && next_width == 0; t += pairs) piece_at(g, t, a.N, next_m0, next_n0, next_width);
+        next_m0 = next_m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
+      };
+      auto ask_next = [&]() {
+        if (next_width == 0) return;
+        load_bias(next_n0 + group * CPP);
+        if constexpr (SCALED<Tin>)
+          if (next_m0 < T) next_scale = a.a_scale[min(next_m0 + lane, T - 1)];
+      };
+      long long t_next = pair;
+      find_next(t_next);
+      ask_next();
+      while (next_width > 0) {
+        m0 = next_m0;
+        n0 = next_n0;
+        width = next_width;
+        find_next(t_next);
+        if constexpr (SCALED<Tin>) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) row_scale[r] = __shfl_sync(0xffffffffu, next_scale, (lane >> 2) + 8 * r);
+        }
         const int cols = m0 < T ? min(width, a.N - n0) : 0; // columns of the tile to be written by this warp's rows
         // The tile's partial products, into registers: the sum of those before the last, fp32 outputs only.
-        constexpr int SUMS = PARTS ? LN_PARTS / CPP / 2 : 1;
+        constexpr int SUMS = PARTS ? LN_PARTS / CPP / GROUPS : 1;
         float sum[SUMS][CPP] = {};
         for (int part = 0; part + 1 < parts && !bad; ++part, ++i) {
           if (!mbar_wait_limited<LIMIT>(bar(LB_ACC_FULL, i & 1), (i >> 1) & 1, abort_flag, a.wait_limit)) bad = true;
@@ -489,9 +573,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
           if constexpr (PARTS) {
 #pragma unroll
             for (int y = 0; y < SUMS; ++y) {
-              if ((half + 2 * y) * CPP < cols) {
+              if ((group + GROUPS * y) * CPP < cols) {
                 float v[CPP];
-                tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + (i & 1) * LN_MAX + (half + 2 * y) * CPP, v);
+                const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (i & 1) * LN_MAX + (group + GROUPS * y) * CPP;
+                if constexpr (SCALED<Tin>) tmem_ld_fragments<CPP>(at, v);
+                else tmem_ld32(at, v);
 #pragma unroll
                 for (int k = 0; k < CPP; ++k) sum[y][k] += v[k];
               }
@@ -508,20 +594,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         if (bad) break;
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(b) * LN_MAX;
-        const int cc = lane & 7;                         // this lane's 16-byte chunk of a row piece
+        const int cc = lane & (CHUNKS - 1);              // this lane's 16-byte chunk of a row piece
+        auto row_of = [&](int r) { return (32 / CHUNKS) * r + lane / CHUNKS; };
+        // Piece p in fragments (8 bits); PARTS: v holds the sum of the parts before the last.
+        auto piece_scaled = [&](int p, auto& v) {
+          constexpr int E = static_cast<int>(sizeof(Tout)), ROW = 16 * CHUNKS;
+          const int col0 = n0 + p * CPP, g = lane >> 2, q = lane & 3;
+          const bool col_ok = col0 + cc * Ch::N < a.N;
+          uint4 res[CHUNKS];
+          if (a.residual != nullptr) {
+            const Tout* from = static_cast<const Tout*>(a.residual) + (col_ok ? col0 + cc * Ch::N : 0);
+#pragma unroll
+            for (int r = 0; r < CHUNKS; ++r)
+              res[r] = *reinterpret_cast<const uint4*>(from + static_cast<size_t>(min(m0 + row_of(r), T - 1)) * a.N);
+          }
+          // Scales and bias from a column per lane to the lanes that have it in their fragments.
+          st_shared_u32(stg + lane * 4, __float_as_uint(ws0));
+          st_shared_u32(stg + 256 + lane * 4, __float_as_uint(bias0));
+          if (CPP > 32) {
+            st_shared_u32(stg + 128 + lane * 4, __float_as_uint(ws1));
+            st_shared_u32(stg + 384 + lane * 4, __float_as_uint(bias1));
+          }
+          const bool more = (p + GROUPS) * CPP < cols;
+          if (more) load_bias(n0 + (p + GROUPS) * CPP);
+          else ask_next();
+          if constexpr (PARTS) {
+            float last[CPP];
+            tmem_ld_fragments<CPP>(taddr + p * CPP, last);
+#pragma unroll
+            for (int k = 0; k < CPP; ++k) v[k] += last[k];
+          } else {
+            tmem_ld_fragments<CPP>(taddr + p * CPP, v);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (!more && lane == 0) mbar_arrive_cluster(acc_empty[b]);   // this warp's share of the accumulator is in registers
+          const uint32_t at_col = stg + 8 * q;
+#pragma unroll
+          for (int n = 0; n < CPP / 8; ++n) {
+            uint64_t w, bb;
+            asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(at_col + 32 * n) : "memory");
+            asm volatile("ld.shared.b64 %0, [%1];" : "=l"(bb) : "r"(at_col + 256 + 32 * n) : "memory");
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {                // row g + 8 r
+              float* x = v + (r >> 1) * (CPP / 2) + 4 * n + 2 * (r & 1);
+              const float2 y = halves_f2(fma_pair(mul_pair(pair_f2(x[0], x[1]), w), pair_f2(row_scale[r], row_scale[r]), bb));
+              x[0] = y.x;
+              x[1] = y.y;
+            }
+          }
+          __syncwarp();
+          if (act != RRA_ACT_NONE) activate(v, act);
+          // Fragment (r, n)'s place in the staging: rows 8 apart are turned alike, so the places of a chunk differ by 8 rows.
+          uint32_t place[CPP / 8];
+#pragma unroll
+          for (int n = 0; n < CPP / 8; ++n) {
+            const int byte = (8 * n + 2 * q) * E;
+            place[n] = stg + g * ROW + (((byte >> 4) ^ g) << 4) + (byte & 15);
+          }
+          if (a.residual != nullptr) {
+#pragma unroll
+            for (int r = 0; r < CHUNKS; ++r) st_shared_v4(staged(row_of(r), cc), res[r].x, res[r].y, res[r].z, res[r].w);
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < CPP / 8; ++n) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                float* x = v + (r >> 1) * (CPP / 2) + 4 * n + 2 * (r & 1);
+                add_two(x[0], x[1], place[n] + 8 * r * ROW, Tout());
+              }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < CPP / 8; ++n) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float* x = v + (r >> 1) * (CPP / 2) + 4 * n + 2 * (r & 1);
+              put_two(place[n] + 8 * r * ROW, x[0], x[1], Tout());
+            }
+          }
+          __syncwarp();
+          Tout* to = static_cast<Tout*>(a.c) + static_cast<size_t>(m0 + lane / CHUNKS) * a.N + col0 + cc * Ch::N;
+          const size_t down = static_cast<size_t>(32 / CHUNKS) * a.N;
+#pragma unroll
+          for (int r = 0; r < CHUNKS; ++r) {
+            const uint4 w = ld_shared_v4(staged(row_of(r), cc));
+            if (col_ok && m0 + row_of(r) < T) *reinterpret_cast<uint4*>(to) = w;
+            to += down;
+          }
+          __syncwarp();                                  // read back before the next piece is written
+        };
         // Piece p; PARTS: v holds the sum of the parts before the last.
-        auto piece = [&](int p, float (&v)[CPP]) {
+        auto piece = [&](int p, auto& v) {
           const int col0 = n0 + p * CPP;
           const bool col_ok = col0 + cc * Ch::N < a.N;   // N is a multiple of 8: chunks are whole
           auto at = [&](int r) { return static_cast<size_t>(m0 + r) * a.N + col0 + cc * Ch::N; };
-          uint4 res[8];
+          uint4 res[CHUNKS];
           auto fetch_residual = [&]() {
             if (a.residual == nullptr) return;
             // Past T or N: some element that is in use, for outputs that are not stored.
             const Tout* from = static_cast<const Tout*>(a.residual) + (col_ok ? col0 + cc * Ch::N : 0);
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-              res[r] = *reinterpret_cast<const uint4*>(from + static_cast<size_t>(min(m0 + 4 * r + (lane >> 3), T - 1)) * a.N);
+            for (int r = 0; r < CHUNKS; ++r)
+              res[r] = *reinterpret_cast<const uint4*>(from + static_cast<size_t>(min(m0 + row_of(r), T - 1)) * a.N);
           };
           if constexpr (PARTS) {
             float last[CPP];
@@ -534,26 +709,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
 #pragma unroll
             for (int q = 0; q < CPP / 32; ++q) tmem_ld32(taddr + p * CPP + q * 32, v + q * 32);
           }
-          if ((p + 2) * CPP >= cols) {
+          if ((p + GROUPS) * CPP >= cols) {
             // This warp's share of the accumulator is in registers: the products of tile i + 2 may overwrite it.
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty[b]);
-          }
-          if constexpr (SCALED<Tin>) {
-            // As the bias below, in the staging rows behind its own.
-            st_shared_u32(stg + 256 + lane * 4, __float_as_uint(ws0));
-            if (CPP > 32) st_shared_u32(stg + 384 + lane * 4, __float_as_uint(ws1));
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < CPP / 4; ++j) {
-              const uint4 ww = ld_shared_v4(stg + 256 + 16 * j);
-              v[4 * j] *= row_scale * __uint_as_float(ww.x);
-              v[4 * j + 1] *= row_scale * __uint_as_float(ww.y);
-              v[4 * j + 2] *= row_scale * __uint_as_float(ww.z);
-              v[4 * j + 3] *= row_scale * __uint_as_float(ww.w);
-            }
-            __syncwarp();
           }
           if (a.bias != nullptr) {
             // From a column per lane to every lane through the staging rows (16
@@ -571,29 +731,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
             }
             __syncwarp();
           }
-          if (SCALED<Tin> || a.bias != nullptr) load_bias(n0 + (p + 2) * CPP);
+          if ((p + GROUPS) * CPP < cols) load_bias(n0 + (p + GROUPS) * CPP);
+          else ask_next();
           activate(v, act);
           if (a.residual != nullptr) {
             // The residual turns from row pieces into rows through the staging rows.
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int rr = 4 * r + (lane >> 3);
-              st_shared_v4(stg + rr * 128 + ((cc ^ (rr & 7)) << 4), res[r].x, res[r].y, res[r].z, res[r].w);
-            }
+            for (int r = 0; r < CHUNKS; ++r) st_shared_v4(staged(row_of(r), cc), res[r].x, res[r].y, res[r].z, res[r].w);
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) Ch::add(v + j * Ch::N, ld_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4)));
+            for (int j = 0; j < CHUNKS; ++j) Ch::add(v + j * Ch::N, ld_shared_v4(staged(lane, j)));
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < CHUNKS; ++j) {
             const uint4 w = Ch::pack(v + j * Ch::N);
-            st_shared_v4(stg + lane * 128 + ((j ^ (lane & 7)) << 4), w.x, w.y, w.z, w.w);
+            st_shared_v4(staged(lane, j), w.x, w.y, w.z, w.w);
           }
           __syncwarp();
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int rr = 4 * r + (lane >> 3);
-            const uint4 w = ld_shared_v4(stg + rr * 128 + ((cc ^ (rr & 7)) << 4));
+          for (int r = 0; r < CHUNKS; ++r) {
+            const int rr = row_of(r);
+            const uint4 w = ld_shared_v4(staged(rr, cc));
             if (col_ok && m0 + rr < T) *reinterpret_cast<uint4*>(static_cast<Tout*>(a.c) + at(rr)) = w;
           }
           __syncwarp();                                  // read back before the next piece is written
@@ -601,15 +759,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
         if constexpr (PARTS) {
 #pragma unroll
           for (int y = 0; y < SUMS; ++y)
-            if ((half + 2 * y) * CPP < cols) piece(half + 2 * y, sum[y]);
+            if ((group + GROUPS * y) * CPP < cols) {
+              if constexpr (SCALED<Tin>) piece_scaled(group + GROUPS * y, sum[y]);
+              else piece(group + GROUPS * y, sum[y]);
+            }
         } else {
 #pragma unroll 1
-          for (int p = half; p * CPP < cols; p += 2) {
+          for (int p = group; p * CPP < cols; p += GROUPS) {
             float v[CPP];
-            piece(p, v);
+            if constexpr (SCALED<Tin>) piece_scaled(p, v);
+            else piece(p, v);
           }
         }
-        if (half * CPP >= cols && lane == 0) mbar_arrive_cluster(acc_empty[b]);   // no piece for this warp
+        if (group * CPP >= cols) {                       // no piece for this warp
+          if (lane == 0) mbar_arrive_cluster(acc_empty[b]);
+          ask_next();
+        }
         ++i;
       }
     }
