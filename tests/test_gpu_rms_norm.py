@@ -76,6 +76,13 @@ def test_rms_norm_sizes(T, cap, N):
         _run(T, cap, N, BF, out, res, True, seed=T + N)
 
 
+@pytest.mark.parametrize("N", [8, 264, 520, 776, 1032, 4096, 4104, 6144, 6152])
+def test_rms_norm_many_rows(N):
+    """Enough rows that a thread has several, one after the other."""
+    for T, out, res in ((1999, E4, BF), (2001, BF, None), (1300, E4, F32)):
+        _run(T, 2001, N, BF, out, res, True, seed=N)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("eight", [False, True])
 @pytest.mark.parametrize("res", ["none", "same", "fp32"])
