@@ -395,7 +395,7 @@ constexpr uint32_t PG_SUB = PT * 128;        // one 64-element column group of a
 constexpr long long PG_UNIT_WAIT_CYCLES = 1LL << 36;   // a wait that lasts a whole piece (the warp for the tails)
 constexpr int PG_MAX_CTAS = 320;             // two an SM, up to 160 SMs
 // The walk in blocks: what a unit costs beside its blocks; the least share of a CTA; no piece is cut shorter than PG_SNAP - PG_START.
-constexpr int PG_START = 2, PG_SHARE = 6, PG_SNAP = 4;
+constexpr int PG_START = 1, PG_SHARE = 2, PG_SNAP = 2;
 
 template <int D>
 struct PagedCfg {
@@ -1172,7 +1172,7 @@ cudaError_t launch_chunk(const PagedArgs& a, int num_sms, cudaStream_t stream, i
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a, box_rows, rows)) != cudaSuccess) return e;
   *launches += 1;
-  if (grid == 1) return cudaSuccess;
+  if (grid == 1 || PG_START + (a.max_kv - 1) / PT + 1 < 2 * PG_SNAP) return cudaSuccess;   // no unit is cut
   cfg.gridDim = dim3(static_cast<unsigned>(grid), PJ_SPLIT);
   cfg.blockDim = dim3(PJ_THREADS);
   cfg.dynamicSmemBytes = 0;
