@@ -1017,10 +1017,9 @@ bool paged_by_chunks(int B, int max_new, int max_kv, int Hkv, int G, int d) {
 
 // Joins the pieces of the unit that CTA blockIdx.x began and the CTAs behind it went on with: 8 neighbouring columns of a row at
 // a time.  Where the pieces are many, eight lanes share them (every eighth each), so that no chain of loads is as long as
-// they are; where they are few, a lane has them all, and a warp reads 512 bytes at a time.  (2048 tokens on 16384 keys, 512
-// units in 2 or 3 pieces: 384 us in all, 423 with eight lanes; 5 tokens on 16384 keys, 8 units in 22: 31 and 36.)  The
+// they are; where they are few, a lane has them all, all of their loads at once, and a warp reads 512 bytes at a time.  The
 // order of additions is that of the pieces by lane, then of the lanes.
-constexpr int PJ_THREADS = 128, PJ_SPLIT = 8, PJ_MANY = 5;
+constexpr int PJ_THREADS = 256, PJ_SPLIT = 8, PJ_FEW = 4;
 template <typename T, int D, int LANES>
 __device__ __forceinline__ void paged_join(const PagedArgs& a, const PagedSpace& space, const int4 j) {
   constexpr bool BF = IsBf16<T>::value == 1;
@@ -1028,45 +1027,69 @@ __device__ __forceinline__ void paged_join(const PagedArgs& a, const PagedSpace&
   const int l = static_cast<int>(threadIdx.x) % LANES;
   auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * me + 1 : 2 * (me + p)); };
   constexpr int PER_WARP = 32 / LANES, PER_CTA = PJ_THREADS / LANES;
+  constexpr int AT_ONCE = LANES == 1 ? PJ_FEW : 2;             // pieces of a lane on their way together
   const int items = rows * (D / 8);
   // Whole warps go round together: their items may end before the round does.
   for (int e0 = static_cast<int>(blockIdx.y) * PER_CTA + static_cast<int>(threadIdx.x) / 32 * PER_WARP; e0 < items; e0 += PER_CTA * PJ_SPLIT) {
     const int e = min(e0 + static_cast<int>(threadIdx.x) % 32 / LANES, items - 1);
     const int c = e / rows, row = e - c * rows;
-    float top = -INFINITY, sum = 0.f, y[8] = {};
+    float m = -INFINITY, sum = 0.f, y[8] = {};   // this lane's pieces so far, against reference m
     bool whole = true;                       // a CTA that gave up a wait has written no sums
-#pragma unroll 4
-    for (int p = l; p < pieces; p += LANES) {
-      whole = whole && space.state[slot_of(p) * 4 + (row >> 5)] == 1;
-      top = fmaxf(top, space.ml[slot_of(p) * space.rows + row].x);
-    }
+    for (int p0 = l; p0 < pieces; p0 += AT_ONCE * LANES) {
+      float2 ml[AT_ONCE];
+      float4 u[AT_ONCE], v[AT_ONCE];
+      float top = m;
 #pragma unroll
-    for (int k = 1; k < LANES; k <<= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-      whole = __shfl_xor_sync(0xffffffffu, static_cast<int>(whole), k) != 0 && whole;
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 2
-    for (int p = l; p < pieces; p += LANES) {
-      const float2 ml = space.ml[slot_of(p) * space.rows + row];
-      const float* o = space.o + ((slot_of(p) * (D / 4) + 2 * c) * space.rows + row) * 4;
-      const float4 u = *reinterpret_cast<const float4*>(o), v = *reinterpret_cast<const float4*>(o + static_cast<size_t>(space.rows) * 4);
-      const float f = fast_exp2(ml.x - ref);
-      sum = fmaf(f, ml.y, sum);
-      y[0] = fmaf(f, u.x, y[0]);
-      y[1] = fmaf(f, u.y, y[1]);
-      y[2] = fmaf(f, u.z, y[2]);
-      y[3] = fmaf(f, u.w, y[3]);
-      y[4] = fmaf(f, v.x, y[4]);
-      y[5] = fmaf(f, v.y, y[5]);
-      y[6] = fmaf(f, v.z, y[6]);
-      y[7] = fmaf(f, v.w, y[7]);
-    }
+      for (int i = 0; i < AT_ONCE; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        u[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int p = p0 + i * LANES;
+        if (p < pieces) {
+          const size_t s = slot_of(p);
+          const float* o = space.o + ((s * (D / 4) + 2 * c) * space.rows + row) * 4;
+          whole = whole && space.state[s * 4 + (row >> 5)] == 1;
+          ml[i] = space.ml[s * space.rows + row];
+          u[i] = *reinterpret_cast<const float4*>(o);
+          v[i] = *reinterpret_cast<const float4*>(o + static_cast<size_t>(space.rows) * 4);
+        }
+      }
 #pragma unroll
-    for (int k = 1; k < LANES; k <<= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, ml[i].x);
+      const float ref = top == -INFINITY ? 0.f : top, old = fast_exp2(m - ref);
+      m = top;
+      sum *= old;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], k);
+      for (int k = 0; k < 8; ++k) y[k] *= old;
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        if (p0 + i * LANES >= pieces) continue;
+        const float f = fast_exp2(ml[i].x - ref);
+        sum = fmaf(f, ml[i].y, sum);
+        y[0] = fmaf(f, u[i].x, y[0]);
+        y[1] = fmaf(f, u[i].y, y[1]);
+        y[2] = fmaf(f, u[i].z, y[2]);
+        y[3] = fmaf(f, u[i].w, y[3]);
+        y[4] = fmaf(f, v[i].x, y[4]);
+        y[5] = fmaf(f, v[i].y, y[5]);
+        y[6] = fmaf(f, v[i].z, y[6]);
+        y[7] = fmaf(f, v[i].w, y[7]);
+      }
+    }
+    if constexpr (LANES > 1) {
+      float top = m;
+#pragma unroll
+      for (int k = 1; k < LANES; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float f = fast_exp2(m - (top == -INFINITY ? 0.f : top));
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= f;
+#pragma unroll
+      for (int k = 1; k < LANES; k <<= 1) {
+        whole = __shfl_xor_sync(0xffffffffu, static_cast<int>(whole), k) != 0 && whole;
+        sum += __shfl_xor_sync(0xffffffffu, sum, k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], k);
+      }
     }
     if (l != 0 || !whole) continue;
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
@@ -1084,7 +1107,7 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PagedArgs 
   start_dependent();
   const PagedSpace space = paged_space(a.space, space_rows);
   const int4 j = *reinterpret_cast<const int4*>(space.join + blockIdx.x * 8);   // pieces, first row of q, tokens, hk
-  if (j.x >= PJ_MANY) paged_join<T, D, 8>(a, space, j);
+  if (j.x > PJ_FEW) paged_join<T, D, 8>(a, space, j);
   else if (j.x > 1) paged_join<T, D, 1>(a, space, j);
 }
 
