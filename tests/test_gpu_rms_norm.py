@@ -130,6 +130,21 @@ def test_rms_norm_special_rows():
 
 
 @pytest.mark.parametrize("N", [64, 4096])
+def test_rms_norm_squares_past_the_range(N):
+    """A sum of squares beyond fp32's range: zeros, also where the product with the weight is beyond it, and its row alone."""
+    x = torch.ones((3, N), dtype=BF, device="cuda")
+    x[1, 5] = 3e38
+    for w in (1.0, 2.0):
+        weight = torch.full((N,), w, device="cuda")
+        y, sc = torch.empty((3, N), dtype=E4, device="cuda"), torch.empty(3, device="cuda")
+        rra.rms_norm(x, _cu(3), 2, y, weight=weight, scale=sc)
+        y16 = torch.empty((3, N), dtype=BF, device="cuda")
+        rra.rms_norm(x, _cu(3), 2, y16, weight=weight)
+        assert bool((y.float()[1] == 0).all() and (y16[1] == 0).all()) and sc[1].item() == 2.0 ** -100
+        assert bool((y.float()[::2] == 448).all() and (y16[::2] == w).all())
+
+
+@pytest.mark.parametrize("N", [64, 4096])
 def test_rms_norm_empty_and_bad_count(N):
     x = torch.ones((6, N), dtype=BF, device="cuda")
     for T, want in ((0, 0), (7, rra.DEVERR_INDEX_RANGE), (-1, rra.DEVERR_INDEX_RANGE)):
