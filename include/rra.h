@@ -477,8 +477,8 @@ RRA_API rra_status rra_read_error_word(int32_t* word, int32_t* code, int clear);
  * of a fused query/key/value projection are used where they are.  Counts of
  * rows are read on the device from cu_seqlens; rows past cu_seqlens[B] are
  * neither read into a result nor written.  int32 arrays are 4-byte aligned.
- * No workspace; every call is one launch, asynchronous on `stream`, and can be
- * captured.  Outputs may not overlap inputs except where said. */
+ * No workspace, and every call one launch (rra_attend_paged alone may use
+ * one, and take two); asynchronous on `stream`, and can be captured.  Outputs may not overlap inputs except where said. */
 
 typedef enum {
   RRA_ACT_NONE = 0,
@@ -623,7 +623,7 @@ RRA_API rra_status rra_linear_scaled(const void* a, const float* a_scale, const 
  * RRA_DEVERR_SEQ_NEGATIVE, one above its bound RRA_DEVERR_SEQ_TOO_LONG, rows outside [0, cap] RRA_DEVERR_INDEX_RANGE;
  * such a sequence is not written.  A table entry in use outside [0, num_pages) records RRA_DEVERR_INDEX_RANGE, and page 0
  * is read in its place.  Products, sums and the values' limits as in rra_attend_prompt; a call repeated gives the same bits. */
-/* workspace: rra_attend_paged_workspace_bytes() bytes of device memory, 256-byte aligned, which the call writes and reads and
+/* The same call's workspace: rra_attend_paged_workspace_bytes() bytes of device memory, 256-byte aligned, which the call writes and reads and
  * which need not be set to anything; NULL where that is 0 (a few new tokens on short caches).  Where keys of one sequence are shared
  * out among SMs their sums meet there, and the call is two launches.  Calls that may run at once need one each. */
 RRA_API size_t rra_attend_paged_workspace_bytes(int B, int cap, int max_new, int max_kv, int Hq, int Hkv, int d);
@@ -634,7 +634,7 @@ RRA_API rra_status rra_attend_paged(const void* q, long long q_stride, const voi
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bound, in clock cycles, on any one on-chip wait of the tcgen05 kernels of the image
- * attention, rra_linear_epilogue and rra_attend_prompt (0, the initial value: about one second,
+ * attention, rra_linear_epilogue, rra_linear_scaled, rra_attend_prompt and rra_attend_paged (0, the initial value: about one second,
  * which rra_linear_packed's kernel always keeps).  A wait of rra_attend_prompt that lasts as long as the
  * other warps' walk over a sequence's keys has the limit for each 128 of them.  A wait that runs out
  * makes the CTA record RRA_DEVERR_WAIT_TIMEOUT, give its own copies and

@@ -13,10 +13,27 @@
 // each looked up one chunk ahead, S = Q K^T, a running reference and sum per row, O += P V.  Then the
 // partial results of all warps are joined through distributed shared memory, each CTA a share of the output.
 //
-// The reference of a row moves only when a maximum exceeds it by more than 8 (log2 units); weights are
+// (4 x 4096 keys, 8 of 32 heads, d = 128: 17 us.)
+//
+// paged_chunk_kernel: tiles of 128 rows on tcgen05, the rows of a tile the G query heads of one key/value head for
+// 128 / G tokens, so that a K/V byte read serves all of them.  A CTA has one tile at a time, and an SM two CTAs: while one's
+// softmax runs the tensor core works for the other.  Warps of a CTA: 0-3 softmax, a row a thread; 4 loads (the Q tile, then K
+// and V blocks of 128 keys through a ring of 64 KB, by copies of as many rows as lie together in a page); 5 products (S = Q K^T,
+// O += P V, P read from TMEM); 6 zeroes the V rows behind a sequence's end.
+//
+// All tiles' key blocks laid end to end are cut into equal shares, one a CTA (each finds its own two cuts from cu_seqlens and
+// kv_len), so that contexts of all lengths, chunks and single tokens fill the SMs evenly: a tile cut between CTAs leaves
+// each part's sums, reference and normaliser in the workspace, and paged_join_kernel joins them.  32 contexts of 1 to 16384 keys, 8
+// of 32 heads, d = 128: 163 us (1.06 GB, 6.5 TB/s); 2048 new tokens on 16384 keys 381 to 405 us (515 GFLOP: 1350 TFLOP/s; the
+// tensor pipe is active 66 % of the time); 2 contexts of 16384 keys among 38 of 100 39 us.  What holds the chunk is the
+// chain S, softmax, P V of a block, which two CTAs overlap only in part: blocks of 64 keys with two S in turn, so that the softmax
+// never waits for a product, took 451 us (each block's own costs twice as often), a share of the exponentials by polynomials
+// 404 and more (the unit for them is a third in use here).
+//
+// In both, the reference of a row moves only when a maximum exceeds it by more than 8 (log2 units); weights are
 // rounded to the input type for the second product (relative 2^-8 in bf16, 2^-11 in fp16, where a factor 2^7
 // that cancels keeps them out of the subnormal range), their sum is taken unrounded in fp32.
-// Rows of a page from kv_len on are not read: zeros take their places.
+// What a page holds from kv_len on reaches no output.
 #include <algorithm>
 #include <mutex>
 
@@ -394,7 +411,8 @@ constexpr uint32_t PG_TMEM_COLS = 256;
 constexpr uint32_t PG_SUB = PT * 128;        // one 64-element column group of a tile: 128 rows x 128 B
 constexpr long long PG_UNIT_WAIT_CYCLES = 1LL << 36;   // a wait that lasts a whole piece (the warp for the tails)
 constexpr int PG_MAX_CTAS = 320;             // two an SM, up to 160 SMs
-// The walk in blocks: what a unit costs beside its blocks; the least share of a CTA; no piece is cut shorter than PG_SNAP - PG_START.
+// In blocks: what a unit costs beside its blocks; the least share of a CTA; no piece is cut shorter than PG_SNAP - PG_START.  (5 tokens on
+// 2048 keys 15 us, with 2, 6 and 4 17.5; a mixed batch 82 / 84.)
 constexpr int PG_START = 1, PG_SHARE = 2, PG_SNAP = 2;
 
 template <int D>
@@ -1005,10 +1023,10 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
   }
 }
 
-// Up to 16 rows of a head group go as rows of a warp's tile where the bounds leave little to read: there the fewer steps count
-// (next tokens, 32 / 8 heads, d = 128: 4 short contexts of 12 heads 4.7 us, as tiles of 128 rows 11.8; 4 x 4096 keys 17.4
-// / 25.3; one of 16384 25 / 28).  A longer cache's time is its bytes', and the tiles' even shares fit contexts of all lengths
-// (32 of 1 to 16384 168 / 168; one of 131072 136 / 91; 2 of 16384 among 38 of 100 187 / 39).
+// Up to 16 rows of a head group go as rows of a warp's tile where the bounds leave little to read (128 MB): there the fewer
+// steps count (next tokens, 32 / 8 heads, d = 128: 4 short contexts of 12 heads 4.7 us, as tiles of 128 rows 11.8; 4 x 4096 keys
+// 17.4 / 25.3).  A longer cache's time is its bytes', and the tiles' even shares fit contexts of all lengths (32 of 1 to 16384
+// 168 / 163 us; one of 131072 136 / 88; 2 of 16384 among 38 of 100 187 / 39).
 bool paged_by_chunks(int B, int max_new, int max_kv, int Hkv, int G, int d) {
   if (G > PT) return false;
   if (static_cast<long long>(max_new) * G > C_ROWS) return true;

@@ -2,6 +2,10 @@
 // the T = cu_seqlens[B] packed rows (T read on the device), a [cap, K] and
 // W [N, K] both K-major.
 //
+// In 8 bits (e4m3): c = act(a_scale w_scale (a W^T) + bias) + residual, a scale for each row of a and of W, applied to the
+// fp32 sums.  The kernels are the same, with K counted in bytes: 12608 rows of 768 -> 2304 22.6 us, 8192 of 4096 -> 16384
+// 299 us (3680 TFLOP/s), 4 of 4096 -> 4096 4.6 us.
+//
 // Three kernels, by the rows that a can hold.
 //
 // linear_pair_kernel: tcgen05 on pairs of SMs (cta_group::2).  A pair owns a
@@ -259,9 +263,11 @@ template <> struct Chunk<__half> {
   }
 };
 
+// The 8-bit epilogue.  The products of a tile take half the time there, and with a row a lane every lane needs every column's
+// scale and bias: 32 reads of shared memory for 64 columns, beside the staging, held a tile of small K at 3.5 us.
 // 32 rows (this warp's lanes of TMEM) by C columns as fragments: v[C / 2 h + 4 n + e] is row g + 16 h + 8 (e >> 1), column
-// 8 n + 2 q + (e & 1), g = lane / 4, q = lane % 4.  A lane so meets C / 4 columns instead of C: their scales and
-// biases are that many fewer reads of shared memory.
+// 8 n + 2 q + (e & 1), g = lane / 4, q = lane % 4.  A lane so meets C / 4 columns instead of C, in
+// neighbouring pairs, which one instruction scales: 2.3 us a tile (sixteen warps with rows of 64 bytes 3.0).
 template <int C>
 __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[C]) {
   static_assert(C == 32 || C == 64, "four or eight groups of 8 columns");
