@@ -813,18 +813,18 @@ constexpr int M_ROWS = 256;                              // most rows of a in a 
 constexpr int M_SPLIT = 8;                               // most CTAs of a cluster
 constexpr int M_THREADS = 320;                           // warp 0 loads, warp 1 products, warps 2-9 epilogue
 constexpr int M_MAX_STAGES = 9;
-constexpr uint32_t M_RING_BYTES = 192 * 1024;            // 4 to 9 stages; then the partial sums
+template <bool HALF> constexpr uint32_t M_RING_BYTES = (HALF ? 96 : 192) * 1024;   // 4 to 9 stages; then the partial sums
 constexpr uint32_t M_W_BYTES = 128 * 128;
-constexpr uint32_t M_OFF_BAR = M_RING_BYTES;
+template <bool HALF> constexpr uint32_t M_OFF_BAR = M_RING_BYTES<HALF>;
 constexpr uint32_t MB_FULL = 0, MB_EMPTY = 8 * M_MAX_STAGES, MB_DONE = 16 * M_MAX_STAGES;
 constexpr uint32_t MW_TMEM = MB_DONE + 8, MW_ABORT = MW_TMEM + 4;
 constexpr uint32_t MB_ACC_FULL = MW_ABORT + 4, MB_ACC_EMPTY = MB_ACC_FULL + 32;   // [4] each, fp32 outputs
 static_assert(MB_ACC_FULL % 8 == 0 && MB_ACC_EMPTY + 32 <= 256, "barriers behind the ring");
-constexpr uint32_t M_SMEM = M_OFF_BAR + 256;
+template <bool HALF> constexpr uint32_t M_SMEM = M_OFF_BAR<HALF> + 256;
 // Accumulators of 128 (or 256) columns that share K.  fp32 outputs (see L_PART): parts of 8 chunks take them in turn, and
 // the epilogue warps add each finished part to their sums in registers while the next ones run (256 rows of 16384 -> 4096
 // 37.5 us; 16-bit outputs 37.2).  16-bit outputs: one part of K each, added at the end.
-constexpr int M_TMEM_COLS = 512;
+template <bool HALF> constexpr int M_TMEM_COLS = HALF ? 256 : 512;
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -859,21 +859,22 @@ __device__ __forceinline__ void finish4(T* c, const T* residual, float4 v) {
 }
 
 // One cluster: `row_step` rows by 128 columns of c; its CTAs share K.  D[n, t] = sum_k W[n, k] a[t, k].
-template <typename Tin, typename Tout, bool LIMIT>
-__global__ void __launch_bounds__(M_THREADS, 1)
+// HALF: two CTAs an SM, for up to 128 rows.
+template <typename Tin, typename Tout, bool LIMIT, bool HALF>
+__global__ void __launch_bounds__(M_THREADS, HALF ? 2 : 1)
     linear_mid_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
                       const LinearEpiArgs a, int act, int splits, int row_step) {
   constexpr bool PARTS = sizeof(Tout) == 4;
   extern __shared__ __align__(1024) uint8_t smem_mid[];
-  const uint32_t base = smem_u32(smem_mid), bars = base + M_OFF_BAR;
+  const uint32_t base = smem_u32(smem_mid), bars = base + M_OFF_BAR<HALF>;
   auto bar = [&](uint32_t kind, uint32_t i) { return bars + kind + 8 * i; };
   const uint32_t abort_flag = bars + MW_ABORT;
-  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_mid + M_OFF_BAR + MW_TMEM);
+  const volatile uint32_t* tmem_ptr = reinterpret_cast<const volatile uint32_t*>(smem_mid + M_OFF_BAR<HALF> + MW_TMEM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
   const int ntiles = (a.N + 127) / 128, n0 = tile % ntiles * 128, t0 = tile / ntiles * row_step;
   if (warp == 1) {
-    tmem_alloc(bars + MW_TMEM, M_TMEM_COLS);
+    tmem_alloc(bars + MW_TMEM, M_TMEM_COLS<HALF>);
     tmem_relinquish();
   }
   if (tid == 0) {
@@ -904,12 +905,12 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   if (!valid && blockIdx.x == 0 && tid == 0) record_error(a.err, RRA_DEVERR_INDEX_RANGE);
   const int rows = valid ? max(0, min(T - t0, row_step)) : 0, boxes = (rows + 31) / 32, cols = (rows + 15) & ~15;
   const uint32_t stage_bytes = M_W_BYTES + static_cast<uint32_t>(boxes) * 4096u;
-  const uint32_t stages = min(static_cast<uint32_t>(M_MAX_STAGES), M_RING_BYTES / stage_bytes);
+  const uint32_t stages = min(static_cast<uint32_t>(M_MAX_STAGES), M_RING_BYTES<HALF> / stage_bytes);
   const int kchunks = (a.K + LK<Tin> - 1) / LK<Tin>;
   const int k_from = static_cast<int>(static_cast<long long>(kchunks) * rank / splits);
   const int k_to = rows > 0 ? static_cast<int>(static_cast<long long>(kchunks) * (rank + 1) / splits) : k_from;
   const int part_cols = cols > 128 ? 256 : 128;
-  const int slots = M_TMEM_COLS / part_cols, wanted = max(1, (k_to - k_from + L_PART - 1) / L_PART);
+  const int slots = M_TMEM_COLS<HALF> / part_cols, wanted = max(1, (k_to - k_from + L_PART - 1) / L_PART);
   const int parts = PARTS ? wanted : min(slots, wanted);
   const int per_part = (k_to - k_from + parts - 1) / parts;
   bool bad = false;
@@ -1103,7 +1104,7 @@ __global__ void __launch_bounds__(M_THREADS, 1)
   }
   cluster_sync_all();                                    // no CTA leaves while another may still read its sums
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, M_TMEM_COLS);
+  if (warp == 1) tmem_dealloc(tmem, M_TMEM_COLS<HALF>);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -1358,17 +1359,17 @@ MidCut cut_mid(const LinearEpiArgs& a, int kchunks, int num_sms) {
   return m;
 }
 
-template <typename Tin, typename Tout, bool LIMIT>
+template <typename Tin, typename Tout, bool LIMIT, bool HALF>
 cudaError_t launch_mid(const LinearEpiArgs& a, int act, const MidCut& cut, cudaStream_t stream) {
   if (linear_encode_fn() == nullptr) return cudaErrorNotSupported;
-  auto kernel = linear_mid_kernel<Tin, Tout, LIMIT>;
-  cudaError_t e = allow_smem<Tin, Tout, -5 - LIMIT>(kernel, M_SMEM);
+  auto kernel = linear_mid_kernel<Tin, Tout, LIMIT, HALF>;
+  cudaError_t e = allow_smem<Tin, Tout, -5 - LIMIT - 2 * HALF>(kernel, M_SMEM<HALF>);
   if (e != cudaSuccess) return e;
   CUtensorMap ma, mw;
   if ((e = make_map_2d<Tin>(&ma, a.a, a.cap, a.K, 32)) != cudaSuccess) return e;
   if ((e = make_map_2d<Tin>(&mw, a.w, a.N, a.K, 128)) != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = dependent_config(attr, static_cast<int>(cut.ctas), M_THREADS, M_SMEM, stream);
+  cudaLaunchConfig_t cfg = dependent_config(attr, static_cast<int>(cut.ctas), M_THREADS, M_SMEM<HALF>, stream);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = static_cast<unsigned>(cut.splits);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -1395,7 +1396,13 @@ cudaError_t launch_tiles(const LinearEpiArgs& a, int act, int num_sms, cudaStrea
   const int kchunks = (a.K + LK<Tin> - 1) / LK<Tin>;
   const MidCut cut = cut_mid(a, kchunks, num_sms);
   const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * kchunks;
-  if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) return launch_mid<Tin, Tout, LIMIT>(a, act, cut, stream);
+  if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) {
+    // In 8 bits, where several rounds of CTAs take turns on an SM, two at a time hide each other's set-up and output: 64 rows of
+    // 4096 -> 32768 29.0 us against 34.9, 24 rows of 4096 -> 65536 50.7 / 61.3 (in one round one at a time: -> 16384 17.7, two 20.4).
+    if constexpr (SCALED<Tin>)
+      if (cut.ctas > num_sms && cut.row_step <= 128) return launch_mid<Tin, Tout, LIMIT, true>(a, act, cut, stream);
+    return launch_mid<Tin, Tout, LIMIT, false>(a, act, cut, stream);
+  }
   if constexpr (sizeof(Tout) == 4)
     if (kchunks > L_PART) return launch_pair<Tin, Tout, true, LIMIT>(a, act, num_sms, stream);
   return launch_pair<Tin, Tout, false, LIMIT>(a, act, num_sms, stream);

@@ -5,6 +5,8 @@ fp32, each of the K additions is off by at most f = 2^-23 of the running size, t
 """
 from __future__ import annotations
 
+import itertools
+
 import numpy as np
 import pytest
 import torch
@@ -80,6 +82,14 @@ def test_linear_scaled_few_rows(cap, K, N):
         _run(T, cap, K, N, torch.bfloat16, "silu", True, True, seed=T * 31 + K + N)
 
 
+@pytest.mark.parametrize("cap", [1, 3, 8, 9, 16])
+@pytest.mark.parametrize("K,N", [(16, 5000), (80, 8200), (768, 16392), (2512, 9736), (8192, 5128)])
+def test_linear_scaled_few_rows_many_columns(cap, K, N):
+    """A CTA goes on from columns to columns (where the rows fit its shared memory)."""
+    for T in {1, cap}:
+        _run(T, cap, K, N, torch.bfloat16, "gelu", True, True, seed=T * 31 + K + N)
+
+
 @pytest.mark.parametrize("cap,T", [(5, 5), (200, 190), (600, 590)])
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
@@ -89,8 +99,8 @@ def test_linear_scaled_types(cap, T, act, out):
     _run(T, cap, 144, 264, out, act, True, True, seed=8, in_place=True)
 
 
-@pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (2569, 2600, 768, 2304),
-                                       (300, 300, 80, 8200), (700, 1200, 1552, 4104), (200, 256, 8208, 1032),
+@pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (40, 64, 1040, 20488), (61, 64, 2064, 40008), (2569, 2600, 768, 2304),
+                                       (300, 300, 80, 8200), (7, 8, 4096, 16384), (16, 16, 2064, 19464), (700, 1200, 1552, 4104), (200, 256, 8208, 1032),
                                        (161, 200, 4112, 4104), (392, 392, 7440, 72), (2, 281, 4784, 136),
                                        (513, 513, 2064, 520), (11000, 11008, 80, 264), (7000, 7000, 144, 1000)])
 def test_linear_scaled_exact_integers(T, cap, K, N):
@@ -129,10 +139,10 @@ def test_linear_scaled_every_value(cap):
 
 @pytest.mark.parametrize("cap", [8, 100, 400])
 def test_linear_scaled_empty_and_bad_count(cap):
-    a, w = torch.zeros((cap, 64), device="cuda").to(E4), torch.zeros((128, 64), device="cuda").to(E4)
-    sa, sw = torch.ones(cap, device="cuda"), torch.ones(128, device="cuda")
-    for T, want in ((0, 0), (cap + 1, rra.DEVERR_INDEX_RANGE), (-1, rra.DEVERR_INDEX_RANGE)):
-        c = torch.full((cap, 128), float("nan"), device="cuda")
+    for N, (T, want) in itertools.product((128, 8192), ((0, 0), (cap + 1, rra.DEVERR_INDEX_RANGE), (-1, rra.DEVERR_INDEX_RANGE))):
+        a, w = torch.zeros((cap, 64), device="cuda").to(E4), torch.zeros((N, 64), device="cuda").to(E4)
+        sa, sw = torch.ones(cap, device="cuda"), torch.ones(N, device="cuda")
+        c = torch.full((cap, N), float("nan"), device="cuda")
         rra.get_device_error(clear=True)
         rra.linear_scaled(a, sa, w, sw, torch.tensor([0, T], dtype=torch.int32, device="cuda"), 1, c)
         torch.cuda.synchronize()
@@ -140,7 +150,7 @@ def test_linear_scaled_empty_and_bad_count(cap):
         assert bool(torch.isnan(c).all())
 
 
-@pytest.mark.parametrize("cap,K,N", [(4, 65536, 64), (100, 16384, 9856), (64, 65536, 264), (200, 16384, 9728),
+@pytest.mark.parametrize("cap,K,N", [(4, 65536, 64), (2, 16384, 5000), (100, 16384, 9856), (64, 65536, 264), (24, 16384, 24584), (200, 16384, 9728),
                                      (257, 65536, 520), (1500, 16384, 1032)])
 def test_long_sums_of_fp32_outputs(cap, K, N):
     """Positive inputs, so that every truncation goes the same way.  A product of the tensor core over 32 elements truncates
