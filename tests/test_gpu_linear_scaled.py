@@ -99,7 +99,7 @@ def test_linear_scaled_types(cap, T, act, out):
     _run(T, cap, 144, 264, out, act, True, True, seed=8, in_place=True)
 
 
-@pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (40, 64, 1040, 20488), (61, 64, 2064, 40008), (2569, 2600, 768, 2304),
+@pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (40, 64, 1040, 20488), (13, 16, 4096, 8200), (9, 9, 1040, 30008), (61, 64, 2064, 40008), (2569, 2600, 768, 2304),
                                        (300, 300, 80, 8200), (7, 8, 4096, 16384), (16, 16, 2064, 19464), (700, 1200, 1552, 4104), (200, 256, 8208, 1032),
                                        (161, 200, 4112, 4104), (392, 392, 7440, 72), (2, 281, 4784, 136),
                                        (513, 513, 2064, 520), (11000, 11008, 80, 264), (7000, 7000, 144, 1000)])
