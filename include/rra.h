@@ -585,12 +585,13 @@ RRA_API rra_status rra_attend_cache(const void* q, long long q_stride, const voi
  *   r = x[t] + residual[t] (residual not NULL);  sum_out[t] = r, rounded once;
  *   y[t] = r * rsqrt(mean(r^2) + eps) * weight (weight float [N]; NULL: ones), r as it is before sum_out's rounding.
  * out_dtype == dtype: y is rounded once.  out_dtype == RRA_E4M3: scale[t] = max(max |y[t]| / 448, 2^-100) and
- * y[t] / scale[t] is rounded once to 8 bits, ties to even (a row of zeros: zeros); a NaN in a row makes its scale NaN.
+ * y[t] / scale[t] is rounded once to 8 bits, ties to even (a row of zeros, with eps > 0: zeros); a NaN in a row makes its
+ * scale NaN.
  *   x [cap, N] of dtype (F16 or BF16); residual and sum_out [cap, N], both or neither, of residual_dtype: dtype or
  *   RRA_F32; y [cap, N]; scale float [cap], with RRA_E4M3 only.  sum_out may be residual, or x where the types are one;
  *   y in 16 bits may be x.  Other overlaps are refused (RRA_ERR_INVALID_ARG).
- * N a multiple of 8, 8 <= N <= 32768 (else RRA_ERR_UNSUPPORTED).  Rows from T on are neither read nor written.  A sum of
- * squares beyond fp32's range makes its row's y zeros.  A cu_seqlens[B] outside [0, cap] records RRA_DEVERR_INDEX_RANGE
+ * N a multiple of 8, 8 <= N <= 32768 (else RRA_ERR_UNSUPPORTED).  Rows from T on are neither read into a result nor written;
+ * scale is 4-byte aligned.  A sum of squares beyond fp32's range makes its row's y zeros.  A cu_seqlens[B] outside [0, cap] records RRA_DEVERR_INDEX_RANGE
  * and writes nothing. */
 RRA_API rra_status rra_rms_norm(const void* x, const void* residual, rra_dtype residual_dtype, const float* weight,
                                 float eps, const int32_t* cu_seqlens, int B, int cap, int N, rra_dtype dtype,
@@ -598,8 +599,8 @@ RRA_API rra_status rra_rms_norm(const void* x, const void* residual, rra_dtype r
 
 /* rra_linear_epilogue on operands in 8 bits, with a scale for each row of a and of w:
  *   c[t, n] = act(a_scale[t] w_scale[n] sum_k a[t, k] w[n, k] + bias[n]) + residual[t, n] for t < T = cu_seqlens[B].
- *   a [cap, K], w [N, K] of RRA_E4M3; a_scale float [cap], w_scale float [N]; bias float [N] or NULL; residual [cap, N]
- *   of out_dtype or NULL (it may be c itself); c [cap, N] of out_dtype (F16, BF16 or F32).
+ *   a [cap, K], w [N, K] of RRA_E4M3; a_scale float [cap] (4-byte aligned), w_scale float [N]; bias float [N] or NULL;
+ *   residual [cap, N] of out_dtype or NULL (it may be c itself); c [cap, N] of out_dtype (F16, BF16 or F32).
  * K a multiple of 16, 16 <= K <= 65536; N a multiple of 8, N <= 65535 * 128 (else RRA_ERR_UNSUPPORTED); cap <= 65535 *
  * 128.  Everything else as there: sums in fp32 (F32 outputs in parts, of K = 1024), the epilogue in fp32 with
  * one rounding, the kernel chosen by cap. */
@@ -617,7 +618,8 @@ RRA_API rra_status rra_linear_scaled(const void* a, const float* a_scale, const 
  *   [B, table_width]; o [cap, Hq, d] contiguous, of the same dtype.
  *   max_new and max_kv bound every sequence's n and kv_len (max_new <= 2^30, max_kv <= min(table_width * page_size,
  *   2^30)); they also decide how the work is cut up: loose bounds cost time.
- * 1e-30 <= scale <= 1e30.  Rows of q and o that belong to no sequence are neither read into a result nor written; rows of
+ * 1e-30 <= scale <= 1e30; with over 128 heads to a group B * Hkv * ceil(max_new * Hq / Hkv / 16) < 2^27.  Rows of q and o that
+ * belong to no sequence are neither read into a result nor written; rows of
  * a page from kv_len[b] on, entries of the table behind the last page in use and pages in no table may hold anything.
  * Offsets into the pool are 64-bit.  Several sequences may share pages.  A negative n or kv_len records
  * RRA_DEVERR_SEQ_NEGATIVE, one above its bound RRA_DEVERR_SEQ_TOO_LONG, rows outside [0, cap] RRA_DEVERR_INDEX_RANGE;

@@ -676,7 +676,8 @@ rra_status linear_layer(const LinearEpiArgs& l, rra_dtype in_dtype, rra_activati
     return fail(RRA_ERR_INVALID_ARG, "c overlaps residual without being it");
   if (e4m3) {
     const float *a_scale = l.a_scale, *w_scale = l.w_scale;
-    RRA_CHECK_PTR(a_scale);
+    if (a_scale == nullptr) return fail(RRA_ERR_INVALID_ARG, "a_scale is null");
+    if (reinterpret_cast<uintptr_t>(a_scale) & 3u) return fail(RRA_ERR_MISALIGNED, "a_scale not 4-byte aligned");
     RRA_CHECK_PTR(w_scale);
     if (!disjoint(sc, {a_scale, 1, 4LL * cap, 4LL * cap}) || !disjoint(sc, {w_scale, 1, 4LL * N, 4LL * N}))
       return fail(RRA_ERR_INVALID_ARG, "c overlaps the scales");
@@ -982,6 +983,9 @@ rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pag
   if (max_new > (1 << 30) || max_kv > (1 << 30)) return fail(RRA_ERR_UNSUPPORTED, "max_new or max_kv > 2^30");
   if (max_kv > static_cast<long long>(table_width) * page_size)
     return fail(RRA_ERR_INVALID_ARG, "max_kv=%d keys do not fit %d pages of %d", max_kv, table_width, page_size);
+  const long long group = Hq / Hkv, most_rows = (max_new < cap ? max_new : cap) * group;
+  if (group > 128 && static_cast<long long>(B) * Hkv * ((most_rows + 15) / 16) >= (1LL << 27))
+    return fail(RRA_ERR_UNSUPPORTED, "over 128 heads to a group: B * Hkv * ceil(max_new * Hq / Hkv / 16) >= 2^27");
   if (!(scale >= 1e-30f && scale <= 1e30f)) return fail(RRA_ERR_INVALID_ARG, "scale outside [1e-30, 1e30]");
   RRA_CHECK_PTR(q);
   RRA_CHECK_PTR(k_pages);

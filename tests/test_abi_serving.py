@@ -55,7 +55,7 @@ LIN = dict(a=0x1000000, sa=0x8000, w=0x2000000, sw=0x9000, bias=0x100, res=None,
     (dict(K=392), UNS), (dict(K=0), UNS), (dict(K=65552), UNS), (dict(N=100), UNS), (dict(N=0), UNS), (dict(B=0), INV),
     (dict(cap=0), INV), (dict(cap=65535 * 128 + 1), INV), (dict(out=E4), INV), (dict(act=5), INV), (dict(act=-1), INV),
     (dict(a=None), INV), (dict(w=None), INV), (dict(c=None), INV), (dict(cu=None), INV), (dict(sa=None), INV),
-    (dict(sw=None), INV), (dict(cu=0x302), MIS), (dict(a=0x1000008), MIS), (dict(sa=0x8004), MIS), (dict(sw=0x9008), MIS),
+    (dict(sw=None), INV), (dict(cu=0x302), MIS), (dict(a=0x1000008), MIS), (dict(sa=0x8002), MIS), (dict(sw=0x9008), MIS),
     (dict(bias=0x104), MIS), (dict(res=0x5000008), MIS), (dict(c=0x1000000), INV),
     (dict(c=0x1000000 + 512 * 384 - 16), INV), (dict(c=0x2000000), INV), (dict(bias=0x4000000), INV),
     (dict(sa=0x4000000), INV), (dict(sw=0x4000010), INV), (dict(res=0x4000010), INV)])
@@ -79,7 +79,7 @@ PAGED = dict(q=0x1000000, qs=2048, k=0x20000000, v=0x30000000, ps=64 * 2 * 128, 
     (dict(ps=64 * 2 * 128 - 8), INV), (dict(ps=64 * 2 * 128 + 4), MIS), (dict(ps=1 << 36), INV), (dict(o=0x20000000), INV),
     (dict(o=0x30000000 + 9 * 64 * 2 * 128 * 2 - 16), INV), (dict(o=0x1000000 + 2048), INV), (dict(ws=None), INV),
     (dict(wsb=1000), INV), (dict(ws=0x50000010), MIS), (dict(ws=0x4000000 - 256), INV), (dict(ws=0x1000000), INV),
-    (dict(ws=0x20000100), INV), (dict(ws=0x30000000 - 256), INV)])
+    (dict(Hq=4000, Hkv=1, qs=4000 * 128, B=65535, cap=1 << 20, new=1 << 20), UNS), (dict(ws=0x20000100), INV), (dict(ws=0x30000000 - 256), INV)])
 def test_attend_paged_refusals(L, kw, want):
     assert _call(L.rra_attend_paged, PAGED, kw) == want
 

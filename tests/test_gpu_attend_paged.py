@@ -107,6 +107,12 @@ def test_attend_paged_chunks(n, Hq, Hkv, d):
     Paged([n] * 6, [0, 1, n - 1, n, n + 1, n + 333], Hq, Hkv, d, 32, torch.bfloat16, seed=n, gap=2, q_pad=3).run()
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(64, 1), (128, 1), (129, 1), (300, 2)])
+def test_attend_paged_large_groups(Hq, Hkv):
+    """Up to a head a row of a tile, and more heads to a group than a tile has rows."""
+    Paged([3, 0, 1, 20], [30, 5, 200, 20], Hq, Hkv, 64, 16, torch.bfloat16, seed=Hq).run()
+
+
 def test_attend_paged_mixed_batch():
     new = [1, 0, 200, 1, 33, 1, 1, 130, 0, 5, 1]
     kv = [1000, 50, 777, 1, 33, 2049, 0, 129, 0, 400, 16]

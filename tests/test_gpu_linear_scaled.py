@@ -137,6 +137,22 @@ def test_linear_scaled_every_value(cap):
     assert torch.equal(c[:2], want[:2]) and torch.equal(c[3:], want[3:]) and bool(torch.isnan(c[2]).all())
 
 
+@pytest.mark.parametrize("cap", [7, 50, 600])
+def test_linear_scaled_scales_of_a_slice(cap):
+    """Rows from the middle of a longer buffer: their scales start where they start."""
+    g = torch.Generator(device="cuda").manual_seed(cap)
+    a = (torch.randn((cap + 5, 128), generator=g, device="cuda") * 60).to(E4)
+    w = (torch.randn((72, 128), generator=g, device="cuda") * 60).to(E4)
+    sa, sw = torch.rand(cap + 5, generator=g, device="cuda"), torch.rand(72, generator=g, device="cuda")
+    whole, part = torch.empty((cap + 5, 72), device="cuda"), torch.empty((cap, 72), device="cuda")
+    cu = lambda n: torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    rra.linear_scaled(a, sa, w, sw, cu(cap + 5), 1, whole)
+    rra.linear_scaled(a[3:cap + 3], sa[3:cap + 3], w, sw, cu(cap), 1, part)
+    # (the two calls may take different kernels: sums of 128 products within 128 x 2^-23 of their size, and the scales)
+    size = (a[3:cap + 3].float().abs() @ w.float().abs().t()) * sa[3:cap + 3, None] * sw
+    assert bool(((whole[3:cap + 3] - part).abs() <= 2 * 131 * F * size).all())
+
+
 @pytest.mark.parametrize("cap", [8, 100, 400])
 def test_linear_scaled_empty_and_bad_count(cap):
     for N, (T, want) in itertools.product((128, 8192), ((0, 0), (cap + 1, rra.DEVERR_INDEX_RANGE), (-1, rra.DEVERR_INDEX_RANGE))):
