@@ -330,58 +330,60 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2)
   cluster_sync_all();                       // no CTA leaves while another may still read its result
 }
 
-// The CTAs a cluster may have here, 16 or 8 (set up once per device and kernel).
+// Clusters of 2, 4, 8 and 16 CTAs that run at once here (asked once per device and kernel; 152 SMs: 152, 74, 36, 14).
 template <typename T, int D>
-cudaError_t cluster_limit(int* most) {
+cudaError_t clusters_at_once(int (&most)[4]) {
   using C = FewCfg<D>;
   auto kernel = paged_few_kernel<T, D>;
   constexpr int kMaxDevices = 64;
-  static int limit[kMaxDevices] = {};
+  static int known[kMaxDevices][4] = {};
+  static bool asked[kMaxDevices] = {};
   static std::mutex m;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(m);
-  if (limit[dev] == 0) {
+  if (!asked[dev]) {
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
-    int clusters = 0;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = C_MAX_SPLIT;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(C_MAX_SPLIT);
-    cfg.blockDim = dim3(32 * C_WARPS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
-      (void)cudaGetLastError();
-      clusters = 0;
+    const bool wide = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (int i = 0; i < 4; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2u << i;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2u << i);
+      cfg.blockDim = dim3(32 * C_WARPS);
+      cfg.dynamicSmemBytes = C::SMEM;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if ((i == 3 && !wide) || cudaOccupancyMaxActiveClusters(&known[dev][i], kernel, &cfg) != cudaSuccess) known[dev][i] = 0;
     }
-    limit[dev] = clusters > 0 ? C_MAX_SPLIT : C_MAX_SPLIT / 2;
+    (void)cudaGetLastError();
+    asked[dev] = true;
   }
-  *most = limit[dev];
+  for (int i = 0; i < 4; ++i) most[i] = known[dev][i];
   return cudaSuccess;
 }
 
+// CTAs of a unit's cluster: as many as run at once (a second round of such small CTAs costs more than it evens out: 16 contexts of
+// 4096 keys, one head, in clusters of 16 21.7 us, of 8 14.7) and leave a warp C_LEAST chunks.
+constexpr int C_LEAST = 4;
+inline int few_cluster(long long units, int chunks, const int (&at_once)[4]) {
+  int c = 1;
+  for (int i = 0; i < 4 && units <= at_once[i] && chunks >= 2 * c * C_WARPS * C_LEAST; ++i) c *= 2;
+  return c;
+}
+
 template <typename T, int D>
-cudaError_t launch_few(const PagedArgs& a, int num_sms, cudaStream_t stream, int* launches) {
+cudaError_t launch_few(const PagedArgs& a, cudaStream_t stream, int* launches) {
   const int row_blocks = (a.max_new * (a.Hq / a.Hkv) + C_ROWS - 1) / C_ROWS;
   const long long units = static_cast<long long>(a.B) * a.Hkv * row_blocks;
-  int most = 0;
-  cudaError_t e = cluster_limit<T, D>(&most);
+  int at_once[4];
+  cudaError_t e = clusters_at_once<T, D>(at_once);
   if (e != cudaSuccess) return e;
-  const int chunks = (a.max_kv - 1) / CK + 1;
-  int cluster = 1, min_chunks = 4;
-  while (2 * cluster <= most && units * 2 * cluster <= 2LL * num_sms && chunks >= 2 * cluster * C_WARPS * min_chunks)
-    cluster *= 2;
-  while (cluster < 4 && units <= 2LL * num_sms && chunks >= 2 * cluster * C_WARPS * 32) {
-    cluster *= 2;
-    min_chunks = 32;
-  }
+  const int cluster = few_cluster(units, (a.max_kv - 1) / CK + 1, at_once);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -395,7 +397,7 @@ cudaError_t launch_few(const PagedArgs& a, int num_sms, cudaStream_t stream, int
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, paged_few_kernel<T, D>, a, cluster, min_chunks, row_blocks)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_few_kernel<T, D>, a, cluster, C_LEAST, row_blocks)) != cudaSuccess) return e;
   *launches += 1;
   return cudaSuccess;
 }
@@ -717,12 +719,14 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
           u.b1 = max(0, off1 - PG_START);
           u.slot = cut.off > 0 ? 2 * me : (off1 < w ? 2 * me + 1 : -1);
           if (u.slot == 2 * me + 1 && lane == 0) {
-            // The unit goes on in the next CTAs; its pieces are joined in their order.
-            int pieces = 1;
-            for (long long c = me + 1; c < active; ++c, ++pieces) {
+            // The unit goes on in the next CTAs, up to the last whose share begins inside it; its pieces are joined in
+            // their order.
+            long long c = min(active - 1, (end.start + w) * active / total + 1);
+            for (; c > me + 1; --c) {
               const long long x = total * c / active - end.start;
-              if (x >= w || paged_snap(static_cast<int>(x), w) == w) break;
+              if (x < w && paged_snap(static_cast<int>(x), w) != w) break;
             }
+            const int pieces = static_cast<int>(c - me) + 1;
             int* j = space.join + me * 8;
             j[1] = cut.s0 + cut.q0;
             j[2] = min(tokens, cut.n - cut.q0);
@@ -1023,14 +1027,19 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
   }
 }
 
-// Up to 16 rows of a head group go as rows of a warp's tile where the bounds leave little to read (128 MB): there the fewer
-// steps count (next tokens, 32 / 8 heads, d = 128: 4 short contexts of 12 heads 4.7 us, as tiles of 128 rows 11.8; 4 x 4096 keys
-// 17.4 / 25.3).  A longer cache's time is its bytes', and the tiles' even shares fit contexts of all lengths (32 of 1 to 16384
-// 168 / 163 us; one of 131072 136 / 88; 2 of 16384 among 38 of 100 187 / 39).
+// Up to 16 rows of a head group go as rows of a warp's tile where that takes less by this estimate, in us: the bytes within the
+// bounds at 6.2 TB/s, with 6 for the rest, or the chain of a warp's chunks; as tiles of 128 rows the bytes and 11, in
+// even shares.  (Next tokens, 32 / 8 heads, d = 128, few rows / tiles: 4 x 1024 keys 8.4 / 12.7, 4 x 8192 27.6 / 31.4, 32 x 2048
+// 43.7 / 53.7, 1 x 16384 23.5 / 22.3, 1 x 32768 39.7 / 33.1; 8 x 4096, 12 heads, d = 64 27.6 / 27.7.)  A chain of over 40 us is a
+// matter of lengths that are alike: 2 contexts of 16384 keys among 38 of 100 187 / 35.
 bool paged_by_chunks(int B, int max_new, int max_kv, int Hkv, int G, int d) {
   if (G > PT) return false;
   if (static_cast<long long>(max_new) * G > C_ROWS) return true;
-  return static_cast<double>(B) * max_kv * Hkv * d * 4 > 128e6;
+  constexpr int at_once[4] = {152, 74, 36, 14};
+  const int chunks = (max_kv - 1) / CK + 1, per_unit = C_WARPS * few_cluster(static_cast<long long>(B) * Hkv, chunks, at_once);
+  const double chain = ((chunks - 1) / per_unit + 1) * (d == 128 ? 1.0 : 0.7);
+  const double bytes = static_cast<double>(B) * max_kv * Hkv * d * 4 / 6.2e6;
+  return chain > 40 || std::max(bytes, chain) + 6 > bytes + 11;
 }
 
 // Joins the pieces of the unit that CTA blockIdx.x began and the CTAs behind it went on with: 8 neighbouring columns of a row at
@@ -1226,7 +1235,7 @@ cudaError_t launch_chunk(const PagedArgs& a, int num_sms, cudaStream_t stream, i
 
 template <typename T, int D>
 cudaError_t launch_d(PagedArgs a, int num_sms, cudaStream_t stream, int* launches) {
-  if (!paged_by_chunks(a.B, a.max_new, a.max_kv, a.Hkv, a.Hq / a.Hkv, D)) return launch_few<T, D>(a, num_sms, stream, launches);
+  if (!paged_by_chunks(a.B, a.max_new, a.max_kv, a.Hkv, a.Hq / a.Hkv, D)) return launch_few<T, D>(a, stream, launches);
   const long long each = std::min(a.wait_limit > 0 ? a.wait_limit : WAIT_LIMIT_CYCLES, 1LL << 38);
   a.unit_wait_limit = each * (1 + a.max_kv / PT);            // at most 2^38 x 2^23
   return a.wait_limit > 0 ? launch_chunk<T, D, true>(a, num_sms, stream, launches) : launch_chunk<T, D, false>(a, num_sms, stream, launches);
