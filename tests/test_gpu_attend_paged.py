@@ -150,6 +150,22 @@ def test_attend_paged_many_sequences(B):
     Paged(new, kv[:B - 2] + [500, 0], 4, 2, 128, 16, torch.bfloat16, seed=B).run()
 
 
+def test_attend_paged_thousands_of_sequences():
+    """A batch of thousands by tiles, most of them without new tokens; some of them looked at."""
+    rng = np.random.default_rng(1)
+    B = 6000
+    new = [int(x) for x in rng.choice([0, 0, 0, 1, 2], B)]
+    kv = [n + int(x) for n, x in zip(new, rng.integers(0, 60, B))]
+    new[4321], kv[4321] = 50, 700
+    p = Paged(new, kv, 4, 2, 64, 16, torch.bfloat16, seed=2)
+    rra.get_device_error(clear=True)
+    p.call()
+    torch.cuda.synchronize()
+    assert rra.get_device_error() == 0
+    p.check(seqs=[0, 1, 2, 255, 256, 257, 511, 512, 3000, 4320, 4321, 4322, B - 2, B - 1] + list(range(100, 140)))
+    assert bool(torch.isfinite(p.o.float()).all())
+
+
 @pytest.mark.parametrize("n,m", [(5, 9000), (48, 20000), (150, 5000), (600, 3000), (1, 40000)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attend_paged_long_caches(n, m, d):
