@@ -1020,6 +1020,59 @@ __global__ void __launch_bounds__(M_THREADS, HALF ? 2 : 1)
     }
   }
   __syncthreads();
+  if constexpr (SCALED<Tin>) {
+    if (splits == 1) {
+      // A tile of one CTA has no sums to join: from the accumulators to c, a column a lane, 16 rows at a time, not by way
+      // of the ring (64 rows of 4096 -> 16384: 17.5 -> 16.3 us, with a residual and SiLU 21.1 -> 18.5).
+      if (warp >= 2 && !aborted) {
+        tc_fence_after();
+        const int quad = warp & 3, n = n0 + quad * 32 + lane;
+        const bool in = n < a.N;
+        const float ws = in ? a.w_scale[n] : 0.f, bias = in && a.bias != nullptr ? a.bias[n] : 0.f;
+#pragma unroll
+        for (int y = 0; y < M_ROWS / 32; ++y) {
+          const int j = half16 + 32 * y;
+          if (j < rows) {                                // (of the warp: TMEM is read by all of its lanes)
+            const float sa = a.a_scale[t0 + min(j + (lane & 15), rows - 1)];
+            float v[16];
+            if constexpr (PARTS) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = sum[y][i];
+            } else {
+              tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + j, v);
+              for (int p = 1; p < parts && p * per_part < k_to - k_from; ++p) {
+                float x[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + p * part_cols + j, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += x[i];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], __shfl_sync(0xffffffffu, sa, i) * ws, bias);
+            activate(v, act);
+            const size_t at = static_cast<size_t>(t0 + j) * a.N + n;
+            if (a.residual != nullptr) {                 // (all 16 loads before the first store: c may be the residual)
+              Tout x[16] = {};
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (in && j + i < rows) x[i] = static_cast<const Tout*>(a.residual)[at + static_cast<size_t>(i) * a.N];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += static_cast<float>(x[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (in && j + i < rows) static_cast<Tout*>(a.c)[at + static_cast<size_t>(i) * a.N] = static_cast<Tout>(v[i]);
+          }
+        }
+        tc_fence_before();
+      }
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      __syncthreads();
+      tc_fence_after();
+      if (warp == 1) tmem_dealloc(tmem, M_TMEM_COLS<HALF>);
+      return;
+    }
+  }
   // Partial sums [row of a][128] over the ring.
   if (warp >= 2 && !aborted && k_from < k_to) {
     tc_fence_after();
@@ -1398,7 +1451,7 @@ cudaError_t launch_tiles(const LinearEpiArgs& a, int act, int num_sms, cudaStrea
   const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * kchunks;
   if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) {
     // In 8 bits, where several rounds of CTAs take turns on an SM, two at a time hide each other's set-up and output: 64 rows of
-    // 4096 -> 32768 29.0 us against 34.9, 24 rows of 4096 -> 65536 50.7 / 61.3 (in one round one at a time: -> 16384 17.7, two 20.4).
+    // 4096 -> 32768 26.6 us against 31.9, 24 rows of 4096 -> 65536 48.7 / 57.6 (in one round one at a time: -> 16384 16.3, two 18.3).
     if constexpr (SCALED<Tin>)
       if (cut.ctas > num_sms && cut.row_step <= 128) return launch_mid<Tin, Tout, LIMIT, true>(a, act, cut, stream);
     return launch_mid<Tin, Tout, LIMIT, false>(a, act, cut, stream);
@@ -1412,7 +1465,7 @@ template <typename Tin, typename Tout>
 cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
   // In 8 bits 9 to 16 rows read as many bytes of a as of W there, so a W of more than 24 MB goes as the M operand too (16 rows of 4096
-  // -> 16384 18.6 / 15.3 us, 4096 -> 4096 5.9 / 6.0).
+  // -> 16384 18.6 / 15.1 us, 4096 -> 4096 5.9 / 6.2).
   if (a.cap <= 16 && (!SCALED<Tin> || static_cast<long long>(a.N) * a.K <= 24LL * 1024 * 1024))
     return launch_few<Tin, Tout, 2>(a, act, stream);
   return a.wait_limit > 0 ? launch_tiles<Tin, Tout, true>(a, act, num_sms, stream)
