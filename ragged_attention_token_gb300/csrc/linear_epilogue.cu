@@ -1463,11 +1463,14 @@ cudaError_t launch_tiles(const LinearEpiArgs& a, int act, int num_sms, cudaStrea
 
 template <typename Tin, typename Tout>
 cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
-  if (a.cap <= 8) return launch_few<Tin, Tout, 1>(a, act, stream);
-  // In 8 bits 9 to 16 rows read as many bytes of a as of W there, so a W of more than 24 MB goes as the M operand too (16 rows of 4096
-  // -> 16384 18.6 / 15.1 us, 4096 -> 4096 5.9 / 6.2).
-  if (a.cap <= 16 && (!SCALED<Tin> || static_cast<long long>(a.N) * a.K <= 24LL * 1024 * 1024))
-    return launch_few<Tin, Tout, 2>(a, act, stream);
+  // In 8 bits W goes as the M operand too where 16 columns a CTA make more than 5 CTAs an SM, whose set-up in rounds then
+  // outweighs that of the larger tiles (by columns / with W as the M operand, us; 8 rows of 1024 -> 8192 3.9 / 5.3, -> 12288
+  // 5.3 / 5.2, -> 16384 6.7 / 5.4, -> 65536 29.6 / 18.8; of 4096 -> 9728 10.7 / 11.4, -> 16384 15.9 / 14.8; one row of 128 -> 16384
+  // 5.1 / 5.5), and for 9 to 16 rows, which read as many bytes of a as of W, where W has more than 24 MB (16 rows of 4096
+  // -> 9728 12.4 / 11.4, -> 4096 5.9 / 6.2).
+  const bool by_columns = !SCALED<Tin> || (a.N <= 80LL * num_sms && (a.cap <= 8 || static_cast<long long>(a.N) * a.K <= 24LL << 20));
+  if (a.cap <= 8 && by_columns) return launch_few<Tin, Tout, 1>(a, act, stream);
+  if (a.cap <= 16 && by_columns) return launch_few<Tin, Tout, 2>(a, act, stream);
   return a.wait_limit > 0 ? launch_tiles<Tin, Tout, true>(a, act, num_sms, stream)
                           : launch_tiles<Tin, Tout, false>(a, act, num_sms, stream);
 }

@@ -99,6 +99,15 @@ def test_linear_scaled_types(cap, T, act, out):
     _run(T, cap, 144, 264, out, act, True, True, seed=8, in_place=True)
 
 
+@pytest.mark.parametrize("T,cap", [(1, 1), (2, 8), (9, 9), (49, 64), (100, 129), (250, 256)])
+@pytest.mark.parametrize("K,N", [(144, 19464), (1040, 13000), (2064, 20488)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+def test_linear_scaled_many_columns(T, cap, K, N, out):
+    """Tiles of one CTA, in one round and in several."""
+    _run(T, cap, K, N, out, "silu", True, True, seed=T + K, in_place=T % 2 == 1)
+    _run(T, cap, K, N, out, "none", False, False, seed=T + K + 1)
+
+
 @pytest.mark.parametrize("T,cap,K,N", [(4, 4, 4096, 4096), (129, 600, 8192, 264), (40, 64, 1040, 20488), (13, 16, 4096, 8200), (9, 9, 1040, 30008), (61, 64, 2064, 40008), (2569, 2600, 768, 2304),
                                        (300, 300, 80, 8200), (7, 8, 4096, 16384), (16, 16, 2064, 19464), (700, 1200, 1552, 4104), (200, 256, 8208, 1032),
                                        (161, 200, 4112, 4104), (392, 392, 7440, 72), (2, 281, 4784, 136),
