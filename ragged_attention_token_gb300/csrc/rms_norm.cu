@@ -260,13 +260,19 @@ cudaError_t launch_typed(const NormRowsArgs& a, int num_sms, cudaStream_t stream
   // Few rows: as many threads a row as there are chunks, for the shortest way through one.  Many: two chunks a thread
   // (three to 768 elements, where a warp then has a row and needs no barrier) keep more bytes on the way for each barrier.
   // One chunk against that: 512 x 4096 with residual to 8 bits 4.0 / 4.8 us, 16411 x 4096 79.5 / 71.9 us, 2049 x 5120 17.7 /
-  // 15.8, 4096 x 8192 43.7 / 46.0, 12608 x 768 in fp16 10.2 / 8.6 (two 9.0).
+  // 15.8, 12608 x 768 in fp16 10.2 / 8.6 (two 9.0).
+  // With a residual and 8 bits a bound of 80 registers a thread serves best (2 chunks: 5120 at 2049 rows 15.7 -> 15.4, 4096 x 12288
+  // 62.8 -> 59.0, with the residual in fp32 112.9 -> 93.4; without a residual 16.2 -> 16.6 and 39.1 -> 40.3).  Past 6144 elements two
+  // chunks let an SM hold two rows' threads: 4096 x 8192 43.8 -> 38.9, 16411 x 8192 165 -> 140 (a residual in fp32 has no
+  // room for that: 63.8 -> 65.5).
+  constexpr int WIDE = RES && sizeof(Ty) == 1 ? 768 : 512;
   if (a.N > 16384) return launch_nv<T, Tr, Ty, RES, 4, 1024>(a, num_sms, stream);
-  if (a.N > 8192) return launch_nv<T, Tr, Ty, RES, 2, 1024>(a, num_sms, stream);
+  if (WIDE == 768 && a.N > 8192 && a.N <= 12288) return launch_nv<T, Tr, Ty, RES, 2, WIDE>(a, num_sms, stream);
+  if (a.N > 8192 || (sizeof(Tr) == 2 && a.N > 6144 && a.cap >= 2 * num_sms)) return launch_nv<T, Tr, Ty, RES, 2, 1024>(a, num_sms, stream);
   if (a.N > 256 && a.N <= 6144 && a.cap >= 8 * num_sms) {
     if (a.N > 512 && a.N <= 768) return launch_nv<T, Tr, Ty, RES, 3, 256>(a, num_sms, stream);
     if (a.N <= 4096) return launch_nv<T, Tr, Ty, RES, 2, 256>(a, num_sms, stream);
-    return launch_nv<T, Tr, Ty, RES, 2, 512>(a, num_sms, stream);
+    return launch_nv<T, Tr, Ty, RES, 2, WIDE>(a, num_sms, stream);
   }
   if (a.N <= 2048) return launch_nv<T, Tr, Ty, RES, 1, 256>(a, num_sms, stream);
   return launch_nv<T, Tr, Ty, RES, 1, 1024>(a, num_sms, stream);

@@ -83,6 +83,12 @@ def test_rms_norm_many_rows(N):
         _run(T, 2001, N, BF, out, res, True, seed=N)
 
 
+@pytest.mark.parametrize("N", [6160, 8192, 8200, 12288, 12296, 16384])
+def test_rms_norm_many_long_rows(N):
+    for T, cap, out, res in ((701, 720, E4, BF), (330, 330, BF, BF), (640, 1300, BF, None), (500, 500, E4, F32)):
+        _run(T, cap, N, BF, out, res, True, seed=T + N)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("eight", [False, True])
 @pytest.mark.parametrize("res", ["none", "same", "fp32"])
