@@ -13,7 +13,7 @@
 // each looked up one chunk ahead, S = Q K^T, a running reference and sum per row, O += P V.  Then the
 // partial results of all warps are joined through distributed shared memory, each CTA a share of the output.
 //
-// (4 x 4096 keys, 8 of 32 heads, d = 128: 17 us.)
+// (4 x 4096 keys, 8 of 32 heads, d = 128: 18 us.)
 //
 // paged_chunk_kernel: tiles of 128 rows on tcgen05, the rows of a tile the G query heads of one key/value head for
 // 128 / G tokens, so that a K/V byte read serves all of them.  A CTA has one tile at a time, and an SM two CTAs: while one's
@@ -30,9 +30,14 @@
 // never waits for a product, took 451 us (each block's own costs twice as often), a share of the exponentials by polynomials
 // 404 and more (the unit for them is a third in use here).
 //
-// In both, the reference of a row moves only when a maximum exceeds it by more than 8 (log2 units); weights are
-// rounded to the input type for the second product (relative 2^-8 in bf16, 2^-11 in fp16, where a factor 2^7
-// that cancels keeps them out of the subnormal range), their sum is taken unrounded in fp32.
+// In both, the reference of a row moves only when a maximum exceeds it by more than 8 (log2 units), the sum of the
+// weights is taken unrounded in fp32, and in fp16 a factor 2^7 that cancels keeps the weights out of the subnormal range.
+// For few rows a weight enters the second product as two 16-bit values, the second what the first's rounding leaves: the read
+// of the cache bounds that kernel, and the products are no more than 6 % of it (4 x 4096 keys 17.3 -> 17.8 us, four short contexts
+// 4.6 -> 4.8, 16 x 4096 of one head 14.5 -> 15.4).  Tiles round it once (relative 2^-8 in bf16, 2^-11 in fp16), which takes
+// an output's error from 0.0017 to 0.0023 of its size, its own rounding to bf16 among both: two products took 516 us instead of
+// 380 for 2048 tokens on 16384 keys, 102 instead of 82 for a mixed batch, 170 instead of 163 for next tokens of 32 contexts (d = 64
+// 121 instead of 92).
 // What a page holds from kv_len on reaches no output.
 #include <algorithm>
 #include <mutex>
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2)
       mma_16816(sc[0], qf[kk], r[0], r[1], T());
       mma_16816(sc[1], qf[kk], r[2], r[3], T());
     }
-    uint32_t pf[4];
+    uint32_t pf[4], pl[4];                  // the weights, and what their rounding leaves
     float alpha[2] = {1.f, 1.f};
     bool moved = false;
 #pragma unroll
@@ -209,13 +214,8 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2)
         p[e] = fast_exp2(t[e] - mu);
         l_run[x] += p[e];
       }
-      if constexpr (BF) {
-        pf[x] = pack2<__nv_bfloat162>(p[0], p[1]);
-        pf[2 + x] = pack2<__nv_bfloat162>(p[2], p[3]);
-      } else {
-        pf[x] = pack2<__half2>(p[0], p[1]);
-        pf[2 + x] = pack2<__half2>(p[2], p[3]);
-      }
+      split2<BF>(p[0], p[1], pf[x], pl[x]);
+      split2<BF>(p[2], p[3], pf[2 + x], pl[2 + x]);
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(32 * C_WARPS, 2)
       ldmatrix4<true>(r, sv + piece((lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
       mma_16816(o[2 * n], pf, r[0], r[1], T());
       mma_16816(o[2 * n + 1], pf, r[2], r[3], T());
+      mma_16816(o[2 * n], pl, r[0], r[1], T());
+      mma_16816(o[2 * n + 1], pl, r[2], r[3], T());
     }
     __syncwarp();                           // the chunk is read before its stage is filled again
     if (i + C::STAGES < mine) fetch(i + C::STAGES, s, next_id);
