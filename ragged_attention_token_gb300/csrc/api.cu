@@ -1028,6 +1028,7 @@ rra_status rra_attend_paged(const void* q, long long q_stride, const void* k_pag
   g.B = B;
   g.cap = cap;
   g.max_new = max_new < cap ? max_new : cap;
+  g.bound_new = max_new;
   g.max_kv = max_kv;
   g.num_pages = num_pages;
   g.page = page_size;

@@ -61,7 +61,7 @@ struct PagedSeq {
     len = a.kv_len[b];
     int code = RRA_DEVERR_NONE;
     if (n < 0 || len < 0) code = RRA_DEVERR_SEQ_NEGATIVE;
-    else if (n > a.max_new || len > a.max_kv) code = RRA_DEVERR_SEQ_TOO_LONG;
+    else if (n > a.bound_new || len > a.max_kv) code = RRA_DEVERR_SEQ_TOO_LONG;
     else if (s0 < 0 || s0 > a.cap - n) code = RRA_DEVERR_INDEX_RANGE;
     valid = code == RRA_DEVERR_NONE;
     if (!valid && record) record_error(a.err, code);

@@ -119,7 +119,8 @@ struct PagedArgs {
   const int32_t* table;                    // [B, table_width]
   const int32_t* kv_len;
   const int32_t* cu;
-  int B, cap, max_new, max_kv, num_pages, page, table_width, Hq, Hkv;
+  int B, cap, max_new, max_kv, num_pages, page, table_width, Hq, Hkv;   // max_new: no more than cap
+  int bound_new;                           // max_new as the caller gave it
   float scale_log2;
   void* o;
   int32_t* err;
