@@ -40,6 +40,7 @@
 // 121 instead of 92).
 // What a page holds from kv_len on reaches no output.
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "block.cuh"
@@ -1033,10 +1034,10 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
 // bounds at 6.2 TB/s, with 6 for the rest, or the chain of a warp's chunks; as tiles of 128 rows the bytes and 11, in
 // even shares.  (Next tokens, 32 / 8 heads, d = 128, few rows / tiles: 4 x 1024 keys 8.4 / 12.7, 4 x 8192 27.6 / 31.4, 32 x 2048
 // 43.7 / 53.7, 1 x 16384 23.5 / 22.3, 1 x 32768 39.7 / 33.1; 8 x 4096, 12 heads, d = 64 27.6 / 27.7.)  A chain of over 40 us is a
-// matter of lengths that are alike: 2 contexts of 16384 keys among 38 of 100 187 / 35.
+// matter of lengths that are alike: 2 contexts of 16384 keys among 38 of 100 187 / 35.  Nor has a grid more than 2^31 - 1 units.
 bool paged_by_chunks(int B, int max_new, int max_kv, int Hkv, int G, int d) {
   if (G > PT) return false;
-  if (static_cast<long long>(max_new) * G > C_ROWS) return true;
+  if (static_cast<long long>(max_new) * G > C_ROWS || static_cast<long long>(B) * Hkv > INT_MAX) return true;
   constexpr int at_once[4] = {152, 74, 36, 14};
   const int chunks = (max_kv - 1) / CK + 1, per_unit = C_WARPS * few_cluster(static_cast<long long>(B) * Hkv, chunks, at_once);
   const double chain = ((chunks - 1) / per_unit + 1) * (d == 128 ? 1.0 : 0.7);
