@@ -813,7 +813,7 @@ constexpr int M_ROWS = 256;                              // most rows of a in a 
 constexpr int M_SPLIT = 8;                               // most CTAs of a cluster
 constexpr int M_THREADS = 320;                           // warp 0 loads, warp 1 products, warps 2-9 epilogue
 constexpr int M_MAX_STAGES = 9;
-template <bool HALF> constexpr uint32_t M_RING_BYTES = (HALF ? 96 : 192) * 1024;   // 4 to 9 stages; then the partial sums
+template <bool HALF> constexpr uint32_t M_RING_BYTES = (HALF ? 96 : 192) * 1024;   // 3 (HALF) or 4 to 9 stages; then the partial sums
 constexpr uint32_t M_W_BYTES = 128 * 128;
 template <bool HALF> constexpr uint32_t M_OFF_BAR = M_RING_BYTES<HALF>;
 constexpr uint32_t MB_FULL = 0, MB_EMPTY = 8 * M_MAX_STAGES, MB_DONE = 16 * M_MAX_STAGES;
@@ -977,7 +977,8 @@ __global__ void __launch_bounds__(M_THREADS, HALF ? 2 : 1)
     bad = __any_sync(0xffffffffu, bad);
   }
   // fp32: this warp's share of each part, as it finishes, into sums: rows of W by lane, 16 rows of a at 32 y.
-  float sum[PARTS ? M_ROWS / 32 : 1][16] = {};
+  constexpr int MOST = HALF ? M_ROWS / 2 : M_ROWS;       // rows of a tile (sums for 256 spilled in the form of two CTAs an SM)
+  float sum[PARTS ? MOST / 32 : 1][16] = {};
   const int half16 = ((warp - 2) >> 2) * 16;
   if (PARTS && warp >= 2) {
     const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half16;
@@ -988,7 +989,7 @@ __global__ void __launch_bounds__(M_THREADS, HALF ? 2 : 1)
       if (bad) break;
       tc_fence_after();
 #pragma unroll
-      for (int y = 0; y < M_ROWS / 32; ++y) {
+      for (int y = 0; y < MOST / 32; ++y) {
         if (half16 + 32 * y < cols) {
           float x[16];
           tmem_ld16(at + slot * part_cols + 32 * y, x);
@@ -1030,7 +1031,7 @@ __global__ void __launch_bounds__(M_THREADS, HALF ? 2 : 1)
         const bool in = n < a.N;
         const float ws = in ? a.w_scale[n] : 0.f, bias = in && a.bias != nullptr ? a.bias[n] : 0.f;
 #pragma unroll
-        for (int y = 0; y < M_ROWS / 32; ++y) {
+        for (int y = 0; y < MOST / 32; ++y) {
           const int j = half16 + 32 * y;
           if (j < rows) {                                // (of the warp: TMEM is read by all of its lanes)
             const float sa = a.a_scale[t0 + min(j + (lane & 15), rows - 1)];
@@ -1079,7 +1080,7 @@ __global__ void __launch_bounds__(M_THREADS, HALF ? 2 : 1)
     const int quad = warp & 3, n = quad * 32 + lane;
     if constexpr (PARTS) {
 #pragma unroll
-      for (int y = 0; y < M_ROWS / 32; ++y) {
+      for (int y = 0; y < MOST / 32; ++y) {
         if (half16 + 32 * y < cols) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -1451,7 +1452,8 @@ cudaError_t launch_tiles(const LinearEpiArgs& a, int act, int num_sms, cudaStrea
   const long long there = 4 * make_tiling(a.cap, a.N, num_sms / 2, LN_MAX).cost * kchunks;
   if (cut.cycles < there && (cut.ctas <= num_sms || a.cap <= M_ROWS)) {
     // In 8 bits, where several rounds of CTAs take turns on an SM, two at a time hide each other's set-up and output: 64 rows of
-    // 4096 -> 32768 26.6 us against 31.9, 24 rows of 4096 -> 65536 48.7 / 57.6 (in one round one at a time: -> 16384 16.3, two 18.3).
+    // 4096 -> 32768 26.0 us against 31.9, in fp32 26.6 / 32.2 and with SiLU and a residual 29.4 / 37.1; 24 rows of 4096 -> 65536 46.7 /
+    // 57.6, in fp32 47.5 / 58.3 (in one round one at a time: -> 16384 16.3, two 18.3).
     if constexpr (SCALED<Tin>)
       if (cut.ctas > num_sms && cut.row_step <= 128) return launch_mid<Tin, Tout, LIMIT, true>(a, act, cut, stream);
     return launch_mid<Tin, Tout, LIMIT, false>(a, act, cut, stream);
@@ -1465,7 +1467,7 @@ template <typename Tin, typename Tout>
 cudaError_t launch_typed(const LinearEpiArgs& a, int act, int num_sms, cudaStream_t stream) {
   // In 8 bits W goes as the M operand too where 16 columns a CTA make more than 5 CTAs an SM, whose set-up in rounds then
   // outweighs that of the larger tiles (by columns / with W as the M operand, us; 8 rows of 1024 -> 8192 3.9 / 5.3, -> 12288
-  // 5.3 / 5.2, -> 16384 6.7 / 5.4, -> 65536 29.6 / 18.8; of 4096 -> 9728 10.7 / 11.4, -> 16384 15.9 / 14.8; one row of 128 -> 16384
+  // 5.3 / 5.2, -> 16384 6.7 / 5.4, -> 65536 29.6 / 17.8; of 4096 -> 9728 10.7 / 11.4, -> 16384 15.9 / 14.8; one row of 128 -> 16384
   // 5.1 / 5.5), and for 9 to 16 rows, which read as many bytes of a as of W, where W has more than 24 MB (16 rows of 4096
   // -> 9728 12.4 / 11.4, -> 4096 5.9 / 6.2).
   const bool by_columns = !SCALED<Tin> || (a.N <= 80LL * num_sms && (a.cap <= 8 || static_cast<long long>(a.N) * a.K <= 24LL << 20));
