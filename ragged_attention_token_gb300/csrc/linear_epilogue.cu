@@ -547,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L_THREADS, 1)
       auto find_next = [&](long long& t) {
         next_width = 0;
         for (; t < g.all && next_width == 0; t += pairs) piece_at(g, t, a.N, next_m0, next_n0, next_width);
-        next_m0 = next_m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
+        if (next_width > 0) next_m0 = next_m0 * 2 * LM + static_cast<int>(rank) * LM + quad * 32;
       };
       auto ask_next = [&]() {
         if (next_width == 0) return;
