@@ -24,9 +24,10 @@
 // All tiles' key blocks laid end to end are cut into equal shares, one a CTA (each finds its own two cuts from cu_seqlens and
 // kv_len), so that contexts of all lengths, chunks and single tokens fill the SMs evenly: a tile cut between CTAs leaves
 // each part's sums, reference and normaliser in the workspace, and paged_join_kernel joins them.  32 contexts of 1 to 16384 keys, 8
-// of 32 heads, d = 128: 163 us (1.06 GB, 6.5 TB/s); 2048 new tokens on 16384 keys 381 to 405 us (515 GFLOP: 1350 TFLOP/s; the
-// tensor pipe is active 66 % of the time); 2 contexts of 16384 keys among 38 of 100 39 us.  What holds the chunk is the
-// chain S, softmax, P V of a block, which two CTAs overlap only in part: blocks of 64 keys with two S in turn, so that the softmax
+// of 32 heads, d = 128: 163 to 167 us (1.06 GB, 6.4 to 6.5 TB/s); 2048 new tokens on 16384 keys 378 us cool (515 GFLOP: 1360 TFLOP/s; the
+// tensor pipe is active 66 % of the time), 402 to 408 under load (1270); 2 contexts of 16384 keys among 38 of 100 35 us.  What holds
+// the chunk is the chain S, softmax, P V of a block, which two CTAs overlap only in part, and at d = 128 a ring of one K and one V
+// block, so that a K block is asked for when S of the one before is done (the two were not separated): blocks of 64 keys with two S in turn, so that the softmax
 // never waits for a product, took 451 us (each block's own costs twice as often), a share of the exponentials by polynomials
 // 404 and more (the unit for them is a third in use here).
 //
@@ -505,7 +506,8 @@ struct PagedCut {
 };
 static_assert(2 * sizeof(PagedCut) <= G_SCAN - G_PLAN, "the plan's place");
 
-// The cut after snapping, as work of its unit of w: not so near one of the unit's ends that a piece would be of a block or two.
+// The cut after snapping, as work of its unit of w: one nearer an end than PG_SNAP falls on it, so that the piece ahead of a cut has
+// PG_SNAP - PG_START blocks at least and the one behind it PG_SNAP.
 __device__ __forceinline__ int paged_snap(int off, int w) {
   if (w - off < PG_SNAP && 2 * off >= w) return w;
   if (off < PG_SNAP) return 0;
@@ -1033,7 +1035,9 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
 // Up to 16 rows of a head group go as rows of a warp's tile where that takes less by this estimate, in us: the bytes within the
 // bounds at 6.2 TB/s, with 6 for the rest, or the chain of a warp's chunks; as tiles of 128 rows the bytes and 11, in
 // even shares.  (Next tokens, 32 / 8 heads, d = 128, few rows / tiles: 4 x 1024 keys 8.4 / 12.7, 4 x 8192 27.6 / 31.4, 32 x 2048
-// 43.7 / 53.7, 1 x 16384 23.5 / 22.3, 1 x 32768 39.7 / 33.1; 8 x 4096, 12 heads, d = 64 27.6 / 27.7.)  A chain of over 40 us is a
+// 43.7 / 53.7, 1 x 16384 23.5 / 22.3, 1 x 32768 39.7 / 33.1; 8 x 4096, 12 heads, d = 64 27.6 / 27.7; few rows 0.4 to 0.8 more since their
+// weights have two parts, which changes no choice here.)  The clusters that run at once are written out, those of 152 SMs: the
+// workspace is sized by this rule too, where there may be no device to ask (the launch asks it, and fits its clusters to the answer).  A chain of over 40 us is a
 // matter of lengths that are alike: 2 contexts of 16384 keys among 38 of 100 187 / 35.  Nor has a grid more than 2^31 - 1 units.
 bool paged_by_chunks(int B, int max_new, int max_kv, int Hkv, int G, int d) {
   if (G > PT) return false;

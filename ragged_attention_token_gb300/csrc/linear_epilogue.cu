@@ -3,8 +3,9 @@
 // W [N, K] both K-major.
 //
 // In 8 bits (e4m3): c = act(a_scale w_scale (a W^T) + bias) + residual, a scale for each row of a and of W, applied to the
-// fp32 sums.  The kernels are the same, with K counted in bytes: 12608 rows of 768 -> 2304 22.6 us, 8192 of 4096 -> 16384
-// 299 us (3680 TFLOP/s), 4 of 4096 -> 4096 4.6 us.
+// fp32 sums.  The kernels are the same, with K counted in bytes.  On a cool card, by graphs of calls: 12608 rows of 768 -> 2304
+// 23 to 24 us, in fp32 33, 8192 of 4096 -> 16384 299 to 306 us (3600 to 3680 TFLOP/s), 4 of 4096 -> 4096 4.6 us; calls one by one
+// under load 24 to 25, 347 to 361 (3050 to 3170) and 7 to 8.
 //
 // Three kernels, by the rows that a can hold.
 //
