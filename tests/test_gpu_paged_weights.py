@@ -10,7 +10,7 @@ under 4 m f with the joins'.  So before its last rounding a result is off by t <
 mag = sum_j p_j |v_j|, and then by u (|o| + t).  In fp16 the second value of a weight is rounded to a fixed step at the
 smallest, 2^-25 against weights of at least 2^7 at the largest: 2^-32 sum_j |v_j| more; and a result to one of 2^-25.
 
-With weights rounded to one value the error is up to u mag, 30 to 100 times that for results that cancel.
+With weights rounded to one value the error is up to u mag, in bf16 some tens of t, which results that cancel show.
 """
 from __future__ import annotations
 
